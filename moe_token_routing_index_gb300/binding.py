@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe_gb300 (include/moe.h), with the same entry-point names.
+"""ctypes binding of libmoe_gb300 (include/moe.h, include/moe_train.h), with the same entry-point names.
 
 Argument marshalling only: tensors become device pointers and sizes, the
 current PyTorch stream becomes the cudaStream_t, and a non-zero status raises
@@ -18,12 +18,15 @@ import torch
 _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "libmoe_gb300.so"
 HEADER = _PKG.parent / "include" / "moe.h"
+TRAIN_HEADER = HEADER.with_name("moe_train.h")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_WORKSPACE = 0, -1, -2, -3, -4
 MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_E4M3 = 0, 1, 2
 MOE_EPILOGUE_NONE, MOE_EPILOGUE_SILU_MUL, MOE_EPILOGUE_SILU_MUL_QUANT = 0, 1, 2
 MOE_GEMM_CTA_PAIRS = 0x100
 MOE_WEIGHTS_PACKED = 0x200
+MOE_BALANCE_SCORES, MOE_BALANCE_SOFTMAX, MOE_BALANCE_SIGMOID = 0, 1, 2
+MOE_CHECKPOINT_BLOCK = 128
 MOE_DEVERR_BAD_INDEX, MOE_DEVERR_BAD_COUNT, MOE_DEVERR_TIMEOUT = 1, 2, 4
 
 
@@ -42,6 +45,7 @@ def _load() -> ctypes.CDLL:
                           "(the CUDA library is required; there is no fallback)")
     lib = ctypes.CDLL(str(LIB_PATH))
     P, I, L, S, U = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint)
+    F = ctypes.c_float
     sigs = {
         "moe_status_string": ([I], ctypes.c_char_p),
         "moe_last_cuda_error": ([], I),
@@ -69,6 +73,18 @@ def _load() -> ctypes.CDLL:
         "moe_silu_mul": ([P, P, L, I, I, P, P, P], I),
         "moe_silu_mul_quant": ([P, P, L, I, I, P, P, P, P, P], I),
         "moe_scatter_add": ([P, P, P, P, I, I, I, I, P, I, P], I),
+        "moe_layer_norm": ([P, L, I, I, I, P, P, I, F, P, P, P, P, P], I),
+        "moe_layer_norm_backward_workspace_size": ([I, I, ctypes.POINTER(S)], I),
+        "moe_layer_norm_backward": ([P, P, L, I, I, I, P, I, P, P, P, P, P, P, P, P, S, P], I),
+        "moe_balance_loss_workspace_size": ([I, I, ctypes.POINTER(S)], I),
+        "moe_balance_loss": ([P, I, L, L, I, I, I, I, F, P, P, P, P, P, P, S, P], I),
+        "moe_balance_loss_backward": ([P, I, L, L, I, I, I, I, F, P, P, P, P, I, P], I),
+        "moe_checkpoint_pack": ([P, L, I, I, P, P, P, P], I),
+        "moe_checkpoint_unpack": ([P, P, I, I, P, P, P], I),
+        "moe_silu_mul_checkpoint": ([P, P, L, I, I, P, P, P, P, P], I),
+        "moe_silu_mul_backward": ([P, P, P, I, I, P, P, P, P], I),
+        "moe_grouped_weight_grad_workspace_size": ([I, I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_grouped_weight_grad": ([P, P, P, P, I, I, I, I, P, I, I, P, S, P], I),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -80,8 +96,8 @@ _lib = _load()
 
 
 def header_symbols() -> list[str]:
-    """Names of the functions include/moe.h declares."""
-    text = HEADER.read_text()
+    """Names of the functions include/moe.h and include/moe_train.h declare."""
+    text = HEADER.read_text() + TRAIN_HEADER.read_text()
     return sorted(set(re.findall(r"^(?:int|const char\*)\s+(moe_\w+)\s*\(", text, flags=re.M)))
 
 
@@ -549,6 +565,281 @@ def moe_dense_gemm(x, w, valid_rows=None, *, epilogue: int = MOE_EPILOGUE_NONE, 
     _need(out, torch.bfloat16, "out")
     st = _lib.moe_dense_gemm(_ptr(x), M, K, _ptr(w), N, _ptr(valid_rows), _ptr(out), epilogue, _stream(stream))
     _check("moe_dense_gemm", st)
+    return out
+
+
+# ----------------------------------------------------------------- layer norm
+
+def _valid_arg(valid, name: str):
+    if valid is not None:
+        _need(valid, torch.int32, name)
+    return _ptr(valid)
+
+
+def _output(t, shape, dtype, device, name: str) -> torch.Tensor:
+    """A caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _norm_inputs(x, gamma, beta=None) -> int:
+    """Checks x [T, D] (rows of any stride) and the weights [D]; returns D."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, D], got {tuple(x.shape)}")
+    _need(x, x.dtype, "x", contiguous=False)
+    D = x.shape[1]
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _need(t, gamma.dtype, name)
+            if tuple(t.shape) != (D,):
+                raise ValueError(f"{name} must have the shape ({D},), got {tuple(t.shape)}")
+    return D
+
+
+def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1e-5, out=None, mean=None, rstd=None,
+                   stream=None):
+    """Layer norm of x[T, D] (bf16 or fp32, rows of any stride) with gamma, beta [D]: returns
+    (y, mean, rstd), mean and rstd [T] in fp32 for the backward pass."""
+    D = _norm_inputs(x, gamma, beta)
+    T = x.shape[0]
+    out = _output(out, (T, D), x.dtype, x.device, "out")
+    mean = _output(mean, (T,), torch.float32, x.device, "mean")
+    rstd = _output(rstd, (T,), torch.float32, x.device, "rstd")
+    st = _lib.moe_layer_norm(_ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta), _dtype_code(gamma),
+                             eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out), _ptr(mean), _ptr(rstd),
+                             _stream(stream))
+    _check("moe_layer_norm", st)
+    return out, mean, rstd
+
+
+def moe_layer_norm_backward_workspace_size(T: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_layer_norm_backward_workspace_size",
+           _lib.moe_layer_norm_backward_workspace_size(T, D, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, residual_grad=None, out=None,
+                            dgamma=None, dbeta=None, with_beta: bool = True, workspace=None, stream=None):
+    """The gradient of moe_layer_norm: returns (dx [T, D], dgamma [D], dbeta [D]), the last two in
+    fp32 (dbeta None without with_beta).  residual_grad [T, D] is added to dx before its rounding."""
+    D = _norm_inputs(x, gamma)
+    T = x.shape[0]
+    for t, dt, shape, name in ((dy, x.dtype, (T, D), "dy"), (residual_grad, x.dtype, (T, D), "residual_grad"),
+                               (mean, torch.float32, (T,), "mean"), (rstd, torch.float32, (T,), "rstd")):
+        if t is not None:
+            _output(t, shape, dt, x.device, name)
+    out = _output(out, (T, D), x.dtype, x.device, "out")
+    dgamma = _output(dgamma, (D,), torch.float32, x.device, "dgamma")
+    dbeta = _output(dbeta, (D,), torch.float32, x.device, "dbeta") if with_beta else None
+    if workspace is None:
+        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, D), dtype=torch.uint8, device=x.device)
+    st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma),
+                                      _dtype_code(gamma), _ptr(mean), _ptr(rstd),
+                                      _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(residual_grad),
+                                      _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
+                                      _stream(stream))
+    _check("moe_layer_norm_backward", st)
+    return out, dgamma, dbeta
+
+
+# --------------------------------------------------------------- balance loss
+
+def moe_balance_loss_workspace_size(T: int, E: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_balance_loss_workspace_size", _lib.moe_balance_loss_workspace_size(T, E, ctypes.byref(n)))
+    return n.value
+
+
+def _balance_inputs(scores, counts):
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be [T, E], got {tuple(scores.shape)}")
+    if not scores.is_cuda:
+        raise TypeError("scores must be a CUDA tensor")
+    if counts is not None:
+        _need(counts, torch.int32, "counts")
+        if counts.numel() < scores.shape[1]:
+            raise ValueError("counts must hold a count for each expert")
+    return scores.shape
+
+
+def moe_balance_loss(scores, top_k: int, num_valid_tokens=None, *, kind: int = MOE_BALANCE_SCORES,
+                     coefficient: float = 1.0, counts=None, workspace=None, stream=None):
+    """Load-balance loss of a top_k router from its output scores[T, E] (bf16 or fp32, any strides):
+    returns (loss [1] fp32, counts [E + 1] int32, mean_probs [E] fp32).  counts: those of moe_route for
+    the same tokens, when there are some (returned as they are); else the selection is made here."""
+    T, E = _balance_inputs(scores, counts)
+    dev = scores.device
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    mean_probs = torch.empty(E, dtype=torch.float32, device=dev)
+    made = torch.empty(E + 1, dtype=torch.int32, device=dev) if counts is None else None
+    if workspace is None:
+        workspace = torch.empty(moe_balance_loss_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    st = _lib.moe_balance_loss(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E, top_k,
+                               kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(counts),
+                               _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace), workspace.numel(),
+                               _stream(stream))
+    _check("moe_balance_loss", st)
+    return loss, made if counts is None else counts, mean_probs
+
+
+def moe_balance_loss_backward(scores, counts, top_k: int, num_valid_tokens=None, *, kind: int = MOE_BALANCE_SCORES,
+                              coefficient: float = 1.0, dloss=None, out=None, accumulate: bool = False, stream=None):
+    """The gradient of moe_balance_loss with respect to scores (same dtype, [T, E]); dloss: fp32 [1] on the
+    device (None: 1).  With accumulate it is added to out."""
+    T, E = _balance_inputs(scores, counts)
+    if dloss is not None:
+        _need(dloss, torch.float32, "dloss")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to a caller-provided out[T, E]")
+    out = _output(out, (T, E), scores.dtype, scores.device, "out")
+    st = _lib.moe_balance_loss_backward(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E,
+                                        top_k, kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"),
+                                        _ptr(counts), _ptr(dloss), _ptr(out), int(accumulate), _stream(stream))
+    _check("moe_balance_loss_backward", st)
+    return out
+
+
+# ----------------------------------------------------------- 8-bit checkpoints
+
+class Checkpoint:
+    """bf16 rows kept in 8 bits: `codes` [a, W] float8_e4m3fn and `exponents` uint8, one per 128 columns of
+    a row (of a row's half when halves = 2, as moe_silu_mul_checkpoint writes them)."""
+
+    def __init__(self, codes: torch.Tensor, exponents: torch.Tensor, halves: int = 1):
+        if codes.dim() != 2 or halves not in (1, 2) or codes.shape[1] % halves:
+            raise ValueError(f"codes [a, W] in {halves} halves, got {tuple(codes.shape)}")
+        a, W = codes.shape
+        blocks = halves * -(-(W // halves) // MOE_CHECKPOINT_BLOCK)
+        _need(codes, torch.float8_e4m3fn, "codes")
+        _need(exponents, torch.uint8, "exponents")
+        if tuple(exponents.shape) != (a, blocks):
+            raise ValueError(f"exponents must have the shape {(a, blocks)}, got {tuple(exponents.shape)}")
+        self.codes, self.exponents, self.halves = codes, exponents, halves
+
+    @classmethod
+    def empty(cls, a: int, W: int, device, halves: int = 1) -> "Checkpoint":
+        blocks = halves * -(-(W // halves) // MOE_CHECKPOINT_BLOCK)
+        return cls(torch.empty(a, W, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(a, blocks, dtype=torch.uint8, device=device), halves)
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _checkpoint_arg(ck, a: int, W: int, halves: int, device) -> Checkpoint:
+    if ck is None:
+        return Checkpoint.empty(a, W, device, halves)
+    if tuple(ck.shape) != (a, W) or ck.halves != halves:
+        raise ValueError(f"the checkpoint must hold [{a}, {W}] in {halves} half or halves, "
+                         f"got {tuple(ck.shape)} in {ck.halves}")
+    return ck
+
+
+def moe_checkpoint_pack(x, valid_rows=None, *, checkpoint=None, stream=None) -> Checkpoint:
+    """bf16 rows x[a, W] (any row stride) as an 8-bit checkpoint."""
+    a, W = x.shape
+    _need(x, torch.bfloat16, "x", contiguous=False)
+    ck = _checkpoint_arg(checkpoint, a, W, 1, x.device)
+    st = _lib.moe_checkpoint_pack(_ptr(x), x.stride(0), a, W, _valid_arg(valid_rows, "valid_rows"), _ptr(ck.codes),
+                                  _ptr(ck.exponents), _stream(stream))
+    _check("moe_checkpoint_pack", st)
+    return ck
+
+
+def moe_checkpoint_unpack(checkpoint: Checkpoint, valid_rows=None, *, out=None, stream=None):
+    """The bf16 rows [a, W] that a checkpoint (of one half) holds, exactly."""
+    a, W = checkpoint.shape
+    if checkpoint.halves != 1:
+        raise ValueError("a checkpoint in two halves is read by moe_silu_mul_backward")
+    out = _output(out, (a, W), torch.bfloat16, checkpoint.device, "out")
+    st = _lib.moe_checkpoint_unpack(_ptr(checkpoint.codes), _ptr(checkpoint.exponents), a, W,
+                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _stream(stream))
+    _check("moe_checkpoint_unpack", st)
+    return out
+
+
+def moe_silu_mul_checkpoint(y, H: int | None = None, valid_rows=None, *, out=None, checkpoint=None, stream=None):
+    """moe_silu_mul of y[a, 2H] (bf16, any row stride) that keeps y in 8 bits: returns (z [a, H], Checkpoint)."""
+    a, n2 = y.shape
+    H = n2 // 2 if H is None else H
+    if 2 * H > n2:
+        raise ValueError(f"y must hold two halves of {H} columns, got {n2}")
+    _need(y, torch.bfloat16, "y", contiguous=False)
+    out = _output(out, (a, H), torch.bfloat16, y.device, "out")
+    ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, y.device)
+    x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
+    st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, y.stride(0), a, H, _valid_arg(valid_rows, "valid_rows"),
+                                      _ptr(out), _ptr(ck.codes), _ptr(ck.exponents), _stream(stream))
+    _check("moe_silu_mul_checkpoint", st)
+    return out, ck
+
+
+def moe_silu_mul_backward(checkpoint: Checkpoint, dz, valid_rows=None, *, out=None, z=None, with_z: bool = True,
+                          stream=None):
+    """The gradient of silu_mul at a checkpoint's values: returns (dy [a, 2H], z [a, H]), z computed again from
+    them for the gradient of w2 (None without with_z)."""
+    a, H = dz.shape
+    _need(dz, torch.bfloat16, "dz")
+    ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, dz.device)
+    out = _output(out, (a, 2 * H), torch.bfloat16, dz.device, "out")
+    z = _output(z, (a, H), torch.bfloat16, dz.device, "z") if with_z else None
+    st = _lib.moe_silu_mul_backward(_ptr(ck.codes), _ptr(ck.exponents), _ptr(dz), a, H,
+                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _ptr(z), _stream(stream))
+    _check("moe_silu_mul_backward", st)
+    return out, z
+
+
+# --------------------------------------------------------------- weight gradient
+
+def moe_grouped_weight_grad_workspace_size(E: int, a_max: int, N: int, K: int, x_dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_grouped_weight_grad_workspace_size",
+           _lib.moe_grouped_weight_grad_workspace_size(E, a_max, N, K, x_dtype, ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dtype=torch.bfloat16,
+                            accumulate: bool = False, workspace=None, stream=None):
+    """dw[e] = dy_e^T x_e over the rows of each expert: dy[a, N] bf16, x[a, K] bf16 or a Checkpoint,
+    counts[>= E] int32 (E: len(counts), or out's) -> dw[E, N, K] bf16 or fp32.  accumulate adds to an fp32 out."""
+    a_max, N = dy.shape
+    _need(dy, torch.bfloat16, "dy")
+    _need(counts, torch.int32, "counts")
+    packed = isinstance(x, Checkpoint)
+    if packed:
+        if x.halves != 1:
+            raise ValueError("x must be a checkpoint of one half")
+        x_ptr, exps, code = _ptr(x.codes), _ptr(x.exponents), MOE_DTYPE_E4M3
+    else:
+        _need(x, torch.bfloat16, "x")
+        x_ptr, exps, code = _ptr(x), None, MOE_DTYPE_BF16
+    if len(x.shape) != 2 or x.shape[0] != a_max:
+        raise ValueError(f"x must hold {a_max} rows, got {tuple(x.shape)}")
+    K = x.shape[1]
+    if E is None:
+        E = counts.shape[0] if out is None else out.shape[0]
+    if counts.shape[0] < E:
+        raise ValueError(f"counts must hold {E} experts' rows, got {counts.shape[0]}")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to a caller-provided out[E, N, K]")
+    out = _output(out, (E, N, K), dtype if out is None else out.dtype, dy.device, "out")
+    if workspace is None:
+        n = moe_grouped_weight_grad_workspace_size(E, a_max, N, K, code)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+    st = _lib.moe_grouped_weight_grad(_ptr(dy), x_ptr, exps, _ptr(counts), E, a_max, N, K, _ptr(out),
+                                      _dtype_code(out), int(accumulate), _ptr(workspace),
+                                      0 if workspace is None else workspace.numel(), _stream(stream))
+    _check("moe_grouped_weight_grad", st)
     return out
 
 

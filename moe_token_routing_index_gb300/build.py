@@ -38,7 +38,7 @@ def _sources():
 
 
 def _deps():
-    return sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + [ROOT / "include" / "moe.h"]
+    return sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted((ROOT / "include").glob("*.h"))
 
 
 def _stale(target: Path, inputs) -> bool:

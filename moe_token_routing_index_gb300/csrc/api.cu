@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "train_launch.h"
 
 namespace {
 
@@ -70,6 +71,8 @@ int check_scores(const void* scores, int dtype, int E) {
 
 namespace moe {
 void record_cuda_error(int e) { t_last_cuda_error = e; }
+
+int device_error_address(unsigned int** out) { return device_error_word(out); }
 
 unsigned long long current_context_id() {
   using GetCurrent = CUresult (*)(CUcontext*);
