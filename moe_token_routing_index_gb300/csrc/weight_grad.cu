@@ -5,17 +5,28 @@
 // dimension, so a TMA box of 64 rows x 128 bytes lands in shared memory as an
 // MN-major, 128B-swizzled operand and nothing is transposed.
 //
-// Kernel structure (one CTA per SM, persistent, 6 warps), tiles of 128 columns of dY
-// x 256 columns of X of one expert:
-//   warp 0     TMA producer: 64 rows of the two operands per stage (16 + 32 KB) into a
-//              4-stage ring guarded by mbarriers.
-//   warp 1     MMA issuer: tcgen05.mma (M = 128, N = 256, 16 rows each) into one of two
-//              256-column accumulators.  Where an expert's rows end inside a step of 16,
-//              the warp first zeroes the rest of that step in shared memory: those rows
-//              belong to the next expert, or to none, and may hold anything.
+// A cluster of two CTAs (two SMs) computes one tile of 256 columns of dY x 256 columns of
+// X of an expert with tcgen05.mma.cta_group::2: CTA r loads 128 columns of each operand,
+// the MMAs of the leader (rank 0) read both CTAs' shared memory, and each CTA's tensor
+// memory receives its 128 rows of the tile.  Persistent, 7 warps per CTA:
+//   warp 0     TMA producer: 64 rows of this CTA's columns per stage (16 + 16 KB) into a
+//              5-stage ring guarded by mbarriers.
+//              Both CTAs' copies complete on the leader's barrier, except the last of an
+//              expert whose rows end inside a step of 16:
+//   warp 6     zeroes the rest of that step in its CTA's shared memory (those rows belong
+//              to the next expert, or to none, and may hold anything), then tells the
+//              leader.  Doing so for every stage, with the release that an arrival on the
+//              other CTA's barrier needs, held the products to 660 TFLOP/s.
+//   warp 1     (leader) MMA issuer: M = 256, N = 256, 16 rows each, into one of two
+//              256-column accumulators.
 //   warps 2-5  epilogue: accumulator rows through a staging block to TMA stores (or fp32
 //              reductions, for accumulate) that clip at the edges of dW[e].
 // An expert without rows has its tiles written as zeros by the epilogue alone.
+//
+// A tile costs its store whatever its rows, and its products by its rows: the tiles of
+// experts with many rows are bound by the tensor cores, the others by memory.  The experts
+// are therefore ordered by their rows, and each pair takes tiles from the two ends of that
+// order in turn, so that both kinds run at any time.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT,
 // all roles stop, copies and MMAs in flight are drained, and tensor memory is freed.
@@ -29,29 +40,34 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 256;       // tile: columns of dY, columns of X
+constexpr int kTile = 256;                // columns of dY and of X of a pair's tile
+constexpr int kHalf = kTile / 2;          // ... that one CTA loads, and rows of the tile it stores
 constexpr int kBR = 64;                   // rows per stage
 constexpr int kBoxCols = 64, kBoxBytes = kBR * 128;
-constexpr int kABoxes = kBM / kBoxCols, kBBoxes = kBN / kBoxCols;
-constexpr int kStageBytes = (kABoxes + kBBoxes) * kBoxBytes;  // 48 KB
-constexpr int kStages = 4, kAccBufs = 2;
-constexpr int kTmemCols = kAccBufs * kBN;
-constexpr int kThreads = 192;
-constexpr int kEpiStageBytes = 32 * 128;  // per epilogue warp: 32 rows x 128 bytes
+constexpr int kBoxes = kHalf / kBoxCols;  // of each operand
+constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 32 KB
+constexpr int kStages = 5, kAccBufs = 2;
+constexpr int kTmemCols = kAccBufs * kTile;
+constexpr int kThreads = 224;
+constexpr int kMaxSorted = 256;           // experts up to which the rank sort is run
+constexpr int kEpiBlocks = 3;             // staging blocks of an epilogue warp, 32 rows x 128 bytes each
+constexpr int kEpiBlockBytes = 32 * 128;
+constexpr int kEpiStageBytes = kEpiBlocks * kEpiBlockBytes;
 
 struct Smem {
   static constexpr int stage = 0;
   static constexpr int epi = stage + kStages * kStageBytes;
-  static constexpr int bars = epi + 4 * kEpiStageBytes;  // full[S], empty[S], tfull[2], tempty[2], drain
-  static constexpr int misc = bars + (2 * kStages + 2 * kAccBufs + 1) * 8;
-  static constexpr int rows = misc + 16;  // row_off[E + 1]
-  static constexpr int bytes_for(int E) { return rows + (E + 1) * 4; }
+  static constexpr int bars = epi + 4 * kEpiStageBytes;  // full[S], ready[S], empty[S], tfull[2], tempty[2], drain
+  static constexpr int misc = bars + (3 * kStages + 2 * kAccBufs + 1) * 8;
+  static constexpr int rows = misc + 16;  // row_off[E + 1], order[E]
+  static constexpr int bytes_for(int E) { return rows + (2 * E + 1) * 4; }
 };
 
 struct Shape {
   int E, a_max, N, K;
   int mt, kt;       // tiles of an expert along N and K
-  int f32, accumulate;
+  int accumulate;
+  int pairs_even;   // an even number of pairs
 };
 
 // Shared-memory descriptor of an MN-major operand, 128B swizzle: 64-column blocks one
@@ -84,66 +100,161 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// mbar_wait for arrivals that come from the other CTA of the pair too: acquires at cluster scope.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = global_timer_ns();
+    if ((i & 63) == 63 && (*abort_flag || global_timer_ns() - t0 > kWaitTimeoutNs)) return false;
+  }
+}
+
+__device__ __forceinline__ void mma_issue_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Arrive on the barrier at this shared-memory offset in both CTAs of the pair once the
+// leader's MMAs issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)0x3)
+      : "memory");
+}
+
+// TMA load into this CTA's shared memory, completing on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int c0,
+                                                 int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Boxes of one CTA's half of an operand with `cols` columns left.  Boxes past the columns are
+// not loaded: what they leave stale reaches only accumulator rows and columns that are not stored.
+__device__ __forceinline__ int boxes(int cols) { return max(0, min(kBoxes, (cols + kBoxCols - 1) / kBoxCols)); }
+
+// Whether the stage that starts with `left` rows of its expert to go ends inside a step of 16 rows.
+__device__ __forceinline__ bool ragged(int left) { return left < kBR && (left & 15) != 0; }
+
+// Arrival on the leader's barrier by a warp that has read its accumulator rows (tcgen05.wait::ld):
+// nothing it wrote has to be seen, so no release at cluster scope, whose fence would wait.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 struct Tile {
   int expert, n0, k0, row0, rows;
 };
 
-// Tile id -> expert and place: an expert's tiles in groups of 16 along N, N innermost,
-// so the CTAs running together read few columns of either operand.
-__device__ __forceinline__ Tile locate(const Shape& p, int64_t tile, const int* row_off) {
+// The pair's it-th tile (sequence number i = it * pairs + pair).  Even sequence numbers
+// count from the front of the expert order, odd ones from its back; a pair changes ends
+// every time (an even number of pairs: then the two of i and i ^ 1 are in the same turn).  An expert's tiles come in
+// groups of 8 along N, N innermost, so that the pairs running together read few columns
+// of either operand.
+__device__ __forceinline__ Tile locate(const Shape& p, int64_t i, int64_t it, int64_t total, const int* row_off,
+                                       const int* order) {
+  const int64_t j = i ^ (it & p.pairs_even);
+  if (j < total) i = j;
+  const int64_t tile = (i & 1) ? total - 1 - (i >> 1) : i >> 1;
   const int per = p.mt * p.kt;
   Tile t;
-  t.expert = (int)(tile / per);
-  const int local = (int)(tile - (int64_t)t.expert * per);
-  const int group = local / (16 * p.kt), in = local - group * 16 * p.kt;
-  const int width = min(16, p.mt - group * 16);
-  t.n0 = (group * 16 + in % width) * kBM;
-  t.k0 = in / width * kBN;
+  const int rank = (int)(tile / per);
+  t.expert = order[rank];
+  const int local = (int)(tile - (int64_t)rank * per);
+  const int group = local / (8 * p.kt), in = local - group * 8 * p.kt;
+  const int width = min(8, p.mt - group * 8);
+  t.n0 = (group * 8 + in % width) * kTile;
+  t.k0 = in / width * kTile;
   t.row0 = row_off[t.expert];
   t.rows = row_off[t.expert + 1] - t.row0;
   return t;
 }
 
-// One accumulator tile of one epilogue warp: rows n0 + 32 sub + lane, in chunks of 128
-// bytes of a row.  zero: the tile of an expert without rows.
-__device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int sub, int lane, uint32_t tbase, bool zero,
-                                           uint8_t* stage, const CUtensorMap* map) {
-  const int row = t.n0 + 32 * sub;
+// 64 consecutive fp32 accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* v = r + 32 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr + 32 * h));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// One epilogue warp's rows of a tile: row (its first) + lane, 64 columns at a time, through
+// the next of its staging blocks (*blk) 128 bytes of a row each.  zero: the tile of an
+// expert without rows.
+template <bool F32>
+__device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int row, int lane, uint32_t tbase, bool zero,
+                                           uint8_t* stage, int* blk, const CUtensorMap* map) {
   if (row >= p.N) return;
-  const int step = p.f32 ? 32 : 64;
-  const int cols = min(kBN, p.K - t.k0);
+  const int cols = min(kTile, p.K - t.k0);
 #pragma unroll 1
-  for (int c = 0; c < cols; c += step) {
-    float v[64];
+  for (int c = 0; c < cols; c += 64) {
+    uint32_t v[64];
     if (zero) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+      for (int i = 0; i < 64; ++i) v[i] = 0u;
     } else {
-      tmem_ld32(tbase + c, v);
-      if (!p.f32) tmem_ld32(tbase + c + 32, v + 32);
+      tmem_ld64(tbase + c, v);
     }
-    if (lane == 0) bulk_wait_group_read0();  // the previous store has read the staging block
-    __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      uint4 o;
-      if (p.f32)
-        o = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                       __float_as_uint(v[4 * q + 3]));
-      else
-        o = f32_to_bf16x8(v + 8 * q);
-      *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
-    }
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      if (p.accumulate) tma_add_3d(map, smem_u32(stage), t.k0 + c, row, t.expert);
-      else tma_store_3d(map, smem_u32(stage), t.k0 + c, row, t.expert);
-      bulk_commit_group();
+    for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+      if (F32 && c + 32 * h >= cols) break;
+      // the store that last used this block has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kEpiBlocks - 1) : "memory");
+      __syncwarp();
+      uint8_t* b = stage + *blk * kEpiBlockBytes;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint4 o;
+        if (F32) {
+          const uint32_t* w = v + 32 * h + 4 * q;
+          o = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          o = f32_to_bf16x8(reinterpret_cast<const float*>(v) + 8 * q);
+        }
+        *reinterpret_cast<uint4*>(b + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (F32 && p.accumulate) tma_add_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, t.expert);
+        else tma_store_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, t.expert);
+        bulk_commit_group();
+      }
+      if (++*blk == kEpiBlocks) *blk = 0;
     }
   }
 }
 
+template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
                        const __grid_constant__ CUtensorMap map_dw, const int32_t* __restrict__ counts, const Shape p,
@@ -153,24 +264,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank() & 1u;
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
-  auto bar_full = [&](int s) { return smem_u32(&bars[s]); };
-  auto bar_empty = [&](int s) { return smem_u32(&bars[kStages + s]); };
-  auto bar_tfull = [&](int b) { return smem_u32(&bars[2 * kStages + b]); };
-  auto bar_tempty = [&](int b) { return smem_u32(&bars[2 * kStages + kAccBufs + b]); };
-  const uint32_t bar_drain = smem_u32(&bars[2 * kStages + 2 * kAccBufs]);
+  auto bar_full = [&](int s) { return smem_u32(&bars[s]); };               // this CTA's copies of a ragged end
+  auto bar_ready = [&](int s) { return smem_u32(&bars[kStages + s]); };    // leader's: both CTAs' stages are whole
+  auto bar_empty = [&](int s) { return smem_u32(&bars[2 * kStages + s]); };
+  auto bar_tfull = [&](int b) { return smem_u32(&bars[3 * kStages + b]); };
+  auto bar_tempty = [&](int b) { return smem_u32(&bars[3 * kStages + kAccBufs + b]); };
+  const uint32_t bar_drain = smem_u32(&bars[3 * kStages + 2 * kAccBufs]);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
   int* row_off = reinterpret_cast<int*>(smem + Smem::rows);
+  int* order = row_off + p.E + 1;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar_full(s), 1);
+      mbar_init(bar_ready(s), 2);
       mbar_init(bar_empty(s), 1);
     }
     for (int b = 0; b < kAccBufs; ++b) {
       mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), 4);
+      mbar_init(bar_tempty(b), 8);  // 4 epilogue warps in each CTA of the pair
     }
     mbar_init(bar_drain, 1);
     *s_abort = 0;
@@ -181,10 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_dw);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
                  "r"(kTmemCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (warp == 2) {
     // row offsets: a warp-wide scan of the counts, cut at a_max (64-bit: bad counts may add up past 31 bits)
@@ -212,8 +329,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) flag_error(err, MOE_DEVERR_BAD_COUNT);
   }
+  __syncthreads();
+  // the experts by descending rows (equal ones by number): each one's rank by counting
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    int at = e;
+    if (p.E <= kMaxSorted) {
+      const int mine = row_off[e + 1] - row_off[e];
+      at = 0;
+      for (int i = 0; i < p.E; ++i) {
+        const int other = row_off[i + 1] - row_off[i];
+        at += other > mine || (other == mine && i < e);
+      }
+    }
+    order[at] = e;
+  }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
   tc_fence_after();
 
   const uint32_t tmem_base = *s_tmem;
@@ -222,27 +354,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     if (lane == 0) {
+      const uint32_t ready0 = map_to_rank(bar_ready(0), 0);
       int s = 0;
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const Tile t = locate(p, tile, row_off);
-        // boxes that lie past the columns are not loaded: what they leave stale reaches only
-        // accumulator rows and columns that are not stored
-        const int na = min(kABoxes, (p.N - t.n0 + kBoxCols - 1) / kBoxCols);
-        const int nb = min(kBBoxes, (p.K - t.k0 + kBoxCols - 1) / kBoxCols);
+      int64_t it = 0;
+      for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
+        const Tile t = locate(p, i, it, total, row_off, order);
+        const int n0 = t.n0 + (int)rank * kHalf, k0 = t.k0 + (int)rank * kHalf;
+        const int na = boxes(p.N - n0), nb = boxes(p.K - k0);
+        const int both = boxes(p.N - t.n0) + boxes(p.N - t.n0 - kHalf) + boxes(p.K - t.k0) + boxes(p.K - t.k0 - kHalf);
         for (int r = 0; r < t.rows; r += kBR) {
           if (!mbar_wait(bar_empty(s), phase ^ 1u, s_abort)) {
             ok = false;
             break;
           }
           const uint32_t dst = sbase + Smem::stage + s * kStageBytes;
-          mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * kBoxBytes);
-          for (int i = 0; i < na; ++i)
-            tma_load_2d(dst + i * kBoxBytes, &map_dy, bar_full(s), t.n0 + i * kBoxCols, t.row0 + r);
-          for (int i = 0; i < nb; ++i)
-            tma_load_2d(dst + (kABoxes + i) * kBoxBytes, &map_x, bar_full(s), t.k0 + i * kBoxCols, t.row0 + r);
+          if (ragged(t.rows - r)) {
+            mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * kBoxBytes);
+            for (int b = 0; b < na; ++b)
+              tma_load_2d(dst + b * kBoxBytes, &map_dy, bar_full(s), n0 + b * kBoxCols, t.row0 + r);
+            for (int b = 0; b < nb; ++b)
+              tma_load_2d(dst + (kBoxes + b) * kBoxBytes, &map_x, bar_full(s), k0 + b * kBoxCols, t.row0 + r);
+          } else {
+            const uint32_t ready = ready0 + (uint32_t)(s * 8);
+            if (leader) {
+              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)both * kBoxBytes);
+              mbar_arrive(bar_ready(s));
+            }
+            for (int b = 0; b < na; ++b)
+              tma_load_2d_pair(dst + b * kBoxBytes, &map_dy, ready, n0 + b * kBoxCols, t.row0 + r);
+            for (int b = 0; b < nb; ++b)
+              tma_load_2d_pair(dst + (kBoxes + b) * kBoxBytes, &map_x, ready, k0 + b * kBoxCols, t.row0 + r);
+          }
           issued_mask |= 1u << s;
           issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
           if (++s == kStages) {
@@ -251,87 +396,118 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (ok) {
+        // every stage this CTA filled has been read by the pair's MMAs before it exits
+        for (int b = 0; b < kStages; ++b)
+          if ((issued_mask >> b) & 1u && !mbar_wait(bar_empty(b), (issued_parity >> b) & 1u, s_abort)) ok = false;
+      }
       if (!ok) {
         flag_error(err, MOE_DEVERR_TIMEOUT);
         *s_abort = 1;
-        for (int i = 0; i < kStages; ++i)
-          if ((issued_mask >> i) & 1u) mbar_wait(bar_full(i), (issued_parity >> i) & 1u, nullptr, kDrainTimeoutNs);
+        const uint64_t t0 = global_timer_ns();  // copies in flight complete on either barrier: give them time to land
+        while (global_timer_ns() - t0 < kDrainTimeoutNs) {
+        }
       }
     }
-  } else if (warp == 1) {
-    // --------------------------------------------------------------- MMA
-    // fp32 accumulate, bf16 operands, both MN-major
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                           ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-    int s = 0;
-    uint32_t phase = 0;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    bool ok = true, issued_any = false;
-    for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const Tile t = locate(p, tile, row_off);
+  } else if (warp == 6) {
+    // ------------------------------------------------------- ragged ends
+    const uint32_t ready0 = map_to_rank(bar_ready(0), 0);
+    uint32_t parity = 0;   // of each stage's next use of its full barrier
+    int64_t block = 0;     // stages filled before this tile
+    bool ok = true;
+    int64_t it = 0;
+    for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
+      const Tile t = locate(p, i, it, total, row_off, order);
       if (t.rows == 0) continue;
-      if (!warp_wait(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(acc * kBN);
-      for (int r = 0; r < t.rows; r += kBR) {
-        if (!warp_wait(bar_full(s), phase, s_abort)) {
-          ok = false;
-          break;
-        }
-        const uint32_t a = sbase + Smem::stage + s * kStageBytes, b = a + kABoxes * kBoxBytes;
-        const int left = min(t.rows - r, kBR), steps = (left + 15) / 16;
-        if (left < steps * 16) {
-          // zero rows left .. 16 * steps - 1 of every box (128-byte lines: the swizzle stays inside them)
-          const int pieces = (steps * 16 - left) * 8;
-          uint8_t* st = smem + Smem::stage + s * kStageBytes + left * 128;
-          for (int box = 0; box < kABoxes + kBBoxes; ++box)
-            for (int i = lane; i < pieces; i += 32)
-              *reinterpret_cast<uint4*>(st + box * kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_shared();
-        }
-        __syncwarp();
-        tc_fence_after();
-        if (lane == 0) {
-          for (int k = 0; k < steps; ++k)
-            mma_issue<false>(d, desc_mn(a + k * 2048), desc_mn(b + k * 2048), idesc, (r | k) != 0);
-          mma_commit(bar_empty(s));
-        }
-        issued_any = true;
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1u;
-        }
-      }
+      block += (t.rows + kBR - 1) / kBR;
+      const int left = t.rows - (t.rows - 1) / kBR * kBR;  // rows of the last stage
+      if (!ragged(left)) continue;
+      const int s = (int)((block - 1) % kStages);
+      ok = warp_wait(bar_full(s), (parity >> s) & 1u, s_abort);
       if (!ok) break;
-      if (lane == 0) mma_commit(bar_tfull(acc));
-      if (++acc == kAccBufs) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      parity ^= 1u << s;
+      // rows left .. the next multiple of 16 of every box (128-byte lines: the swizzle stays inside them)
+      const int pieces = (16 - (left & 15)) * 8;
+      uint8_t* st = smem + Smem::stage + s * kStageBytes + left * 128;
+      for (int box = 0; box < 2 * kBoxes; ++box)
+        for (int j = lane; j < pieces; j += 32)
+          *reinterpret_cast<uint4*>(st + box * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(ready0 + (uint32_t)(s * 8));
     }
     if (!ok && lane == 0) {
       flag_error(err, MOE_DEVERR_TIMEOUT);
       *s_abort = 1;
-      if (issued_any) {
-        mma_commit(bar_drain);
-        mbar_wait(bar_drain, 0, nullptr, kDrainTimeoutNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA (leader)
+    if (lane == 0 && leader) {
+      // fp32 accumulate, bf16 operands, both MN-major
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                             ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+      int s = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true, issued_any = false;
+      int64_t it = 0;
+      for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
+        const Tile t = locate(p, i, it, total, row_off, order);
+        if (t.rows == 0) continue;
+        if (!mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kTile);
+        for (int r = 0; r < t.rows; r += kBR) {
+          if (!mbar_wait_cluster(bar_ready(s), phase, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = sbase + Smem::stage + s * kStageBytes, b = a + kBoxes * kBoxBytes;
+          const int steps = (min(t.rows - r, kBR) + 15) / 16;
+          for (int k = 0; k < steps; ++k)
+            mma_issue_pair(d, desc_mn(a + k * 2048), desc_mn(b + k * 2048), idesc, (r | k) != 0);
+          mma_commit_pair(bar_empty(s));
+          issued_any = true;
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(bar_tfull(acc));
+        if (++acc == kAccBufs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        flag_error(err, MOE_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        if (issued_any) {  // the MMAs in flight finish before tensor memory is freed
+          mma_commit_pair(bar_drain);
+          mbar_wait(bar_drain, 0, nullptr, kDrainTimeoutNs);
+        }
       }
     }
-    __syncwarp();
   } else {
-    // ---------------------------------------------------------- epilogue
+    // ------------------------------------------------- epilogue (both CTAs)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
     uint8_t* stage = smem + Smem::epi + (warp - 2) * kEpiStageBytes;
+    const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const Tile t = locate(p, tile, row_off);
+    int64_t it = 0;
+    int blk = 0;
+    for (int64_t i = pair; i < total; i += pairs, ++it) {
+      const Tile t = locate(p, i, it, total, row_off, order);
+      const int row = t.n0 + (int)rank * kHalf + 32 * sub;
       if (t.rows == 0) {
-        if (!p.accumulate) store_tile(p, t, sub, lane, 0, true, stage, &map_dw);
+        if (!p.accumulate) store_tile<F32>(p, t, row, lane, 0, true, stage, &blk, &map_dw);
         continue;
       }
       if (!warp_wait(bar_tfull(acc), acc_phase, s_abort)) {
@@ -340,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      store_tile(p, t, sub, lane, tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kBN), false, stage,
-                 &map_dw);
+      store_tile<F32>(p, t, row, lane, tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kTile), false, stage,
+                      &blk, &map_dw);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_tempty(acc));
+      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
       if (++acc == kAccBufs) {
         acc = 0;
         acc_phase ^= 1u;
@@ -353,11 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the block exits
   }
 
+  // the pair meets, then frees its tensor memory together
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
 }
 
 // ------------------------------------------------------------------- host
@@ -398,20 +576,41 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     x = g.ws;
   }
-  const Shape p{g.E, g.a_max, g.N, g.K, (g.N + kBM - 1) / kBM, (g.K + kBN - 1) / kBN, g.dw_dtype == MOE_DTYPE_F32,
-                g.accumulate};
+  Shape p{g.E, g.a_max, g.N, g.K, (g.N + kTile - 1) / kTile, (g.K + kTile - 1) / kTile, g.accumulate, 0};
+  const bool f32 = g.dw_dtype == MOE_DTYPE_F32;
   CUtensorMap dw, dy, mx;
-  if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, p.f32)) return cudaErrorInvalidValue;
+  if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
   dy = mx = dw;  // without rows nothing is loaded
   if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
                       !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR)))
     return cudaErrorInvalidValue;
   const int smem = Smem::bytes_for(g.E) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(device_sm_count() / 2 * 2);
+  int pairs = 0;
+  e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+  if (e != cudaSuccess) return e;
+  if (pairs < 1) return cudaErrorNotSupported;
   const int64_t tiles = (int64_t)g.E * p.mt * p.kt;
-  const int sms = device_sm_count();
-  weight_grad_kernel<<<(int)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(dy, mx, dw, g.counts, p, g.err);
+  if (tiles <= pairs) pairs = (int)tiles;       // one tile each
+  else if (pairs > 1) pairs = pairs / 2 * 2;
+  p.pairs_even = pairs % 2 == 0;
+  cfg.gridDim = dim3(2 * pairs);
+  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, g.counts, p, g.err);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
