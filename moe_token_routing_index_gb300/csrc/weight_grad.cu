@@ -10,7 +10,7 @@
 // the MMAs of the leader (rank 0) read both CTAs' shared memory, and each CTA's tensor
 // memory receives its 128 rows of the tile.  Persistent, 7 warps per CTA:
 //   warp 0     TMA producer: 64 rows of this CTA's columns per stage (16 + 16 KB) into a
-//              5-stage ring guarded by mbarriers.
+//              6-stage ring guarded by mbarriers.
 //              Both CTAs' copies complete on the leader's barrier, except the last of an
 //              expert whose rows end inside a step of 16:
 //   warp 6     zeroes the rest of that step in its CTA's shared memory (those rows belong
@@ -46,28 +46,53 @@ constexpr int kBR = 64;                   // rows per stage
 constexpr int kBoxCols = 64, kBoxBytes = kBR * 128;
 constexpr int kBoxes = kHalf / kBoxCols;  // of each operand
 constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 32 KB
-constexpr int kStages = 5, kAccBufs = 2;
+constexpr int kStages = 6, kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kThreads = 224;
 constexpr int kMaxSorted = 256;           // experts up to which the rank sort is run
-constexpr int kEpiBlocks = 3;             // staging blocks of an epilogue warp, 32 rows x 128 bytes each
-constexpr int kEpiBlockBytes = 32 * 128;
-constexpr int kEpiStageBytes = kEpiBlocks * kEpiBlockBytes;
+constexpr int kEpiBlockBytes = 32 * 128;  // staging block of an epilogue warp: 32 rows x 128 bytes
+// Staging blocks of an epilogue warp: two, which short experts' tiles need to write at 6.3
+// TB/s (6.1 with one); one where the expert tables want the room.
+constexpr int kTwoBlocksMaxE = 256;
+// Tiles with more rows than this use one block whatever there is: their stores then spread
+// over the products of the next tile.  In bursts they delay its loads: 16 experts of 512
+// rows, N = K = 8192: 800 us with three blocks in flight, 740 us with one.
+constexpr int kBurstRows = 128;
 
 struct Smem {
   static constexpr int stage = 0;
   static constexpr int epi = stage + kStages * kStageBytes;
-  static constexpr int bars = epi + 4 * kEpiStageBytes;  // full[S], ready[S], empty[S], tfull[2], tempty[2], drain
+  // after 4 * blocks staging blocks:
+  static constexpr int bars = 0;  // full[S], ready[S], empty[S], tfull[2], tempty[2], drain
   static constexpr int misc = bars + (3 * kStages + 2 * kAccBufs + 1) * 8;
-  static constexpr int rows = misc + 16;  // row_off[E + 1], order[E]
-  static constexpr int bytes_for(int E) { return rows + (2 * E + 1) * 4; }
+  static constexpr int rows = misc + 16;  // row_off[E + 1], then order[E] in 16 bits
+  static constexpr int tail(int blocks) { return epi + 4 * blocks * kEpiBlockBytes; }
+  static constexpr int bytes_for(int E, int blocks) { return tail(blocks) + rows + (E + 1) * 4 + E * 2; }
 };
+
+// n / d for 0 <= n < 2^31 by one multiplication and a correction: a tile's place costs its
+// roles tens of cycles, where 64-bit divisions held tiles of one stage to 0.8 us.
+struct Divisor {
+  uint32_t d, m;
+};
+inline Divisor divisor(int d) { return {(uint32_t)d, d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)d)}; }
+__device__ __forceinline__ int quotient(int n, Divisor v) {
+  const uint32_t q = __umulhi((uint32_t)n, v.m);  // n / d or one less
+  return (int)(q + ((uint32_t)n - q * v.d >= v.d));
+}
+
+constexpr int kGroup = 8;  // tiles along N of a group in the tile order
 
 struct Shape {
   int E, a_max, N, K;
-  int mt, kt;       // tiles of an expert along N and K
+  int total;         // tiles
+  int mt, kt;        // tiles of an expert along N and K
+  Divisor per;       // tiles of an expert
+  Divisor band;      // tiles of a group of kGroup along N
+  Divisor last;      // tiles along N of an expert's last group
   int accumulate;
-  int pairs_even;   // an even number of pairs
+  int pairs_even;    // an even number of pairs
+  int blocks;        // staging blocks of an epilogue warp
 };
 
 // Shared-memory descriptor of an MN-major operand, 128B swizzle: 64-column blocks one
@@ -82,11 +107,15 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   return d;
 }
 
+// The store is written once and not read here: it leaves L2 first, for the operands to stay
+// (64 experts of 16 rows, N = K = 4096: 374 -> 313 us).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], pol;\n\t}" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -167,23 +196,24 @@ struct Tile {
 
 // The pair's it-th tile (sequence number i = it * pairs + pair).  Even sequence numbers
 // count from the front of the expert order, odd ones from its back; a pair changes ends
-// every time (an even number of pairs: then the two of i and i ^ 1 are in the same turn).  An expert's tiles come in
-// groups of 8 along N, N innermost, so that the pairs running together read few columns
-// of either operand.
-__device__ __forceinline__ Tile locate(const Shape& p, int64_t i, int64_t it, int64_t total, const int* row_off,
-                                       const int* order) {
-  const int64_t j = i ^ (it & p.pairs_even);
-  if (j < total) i = j;
-  const int64_t tile = (i & 1) ? total - 1 - (i >> 1) : i >> 1;
-  const int per = p.mt * p.kt;
+// every time (an even number of pairs: then the two of i and i ^ 1 are in the same turn).
+// An expert's tiles come in groups of kGroup along N, N innermost, so that the pairs
+// running together read few columns of either operand.
+__device__ __forceinline__ Tile locate(const Shape& p, int i, int it, const int* row_off,
+                                       const uint16_t* order) {
+  const int j = i ^ (it & p.pairs_even);
+  if (j < p.total) i = j;
+  const int tile = (i & 1) ? p.total - 1 - (i >> 1) : i >> 1;
   Tile t;
-  const int rank = (int)(tile / per);
+  const int rank = quotient(tile, p.per);
   t.expert = order[rank];
-  const int local = (int)(tile - (int64_t)rank * per);
-  const int group = local / (8 * p.kt), in = local - group * 8 * p.kt;
-  const int width = min(8, p.mt - group * 8);
-  t.n0 = (group * 8 + in % width) * kTile;
-  t.k0 = in / width * kTile;
+  const int local = tile - rank * (int)p.per.d;
+  const int group = quotient(local, p.band), in = local - group * (int)p.band.d;
+  const bool whole = (group + 1) * kGroup <= p.mt;
+  const int k = whole ? in / kGroup : quotient(in, p.last);
+  const int n = in - k * (whole ? kGroup : (int)p.last.d);
+  t.n0 = (group * kGroup + n) * kTile;
+  t.k0 = k * kTile;
   t.row0 = row_off[t.expert];
   t.rows = row_off[t.expert + 1] - t.row0;
   return t;
@@ -227,8 +257,10 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
 #pragma unroll
     for (int h = 0; h < (F32 ? 2 : 1); ++h) {
       if (F32 && c + 32 * h >= cols) break;
-      // the store that last used this block has read it
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kEpiBlocks - 1) : "memory");
+      if (lane == 0) {  // the store that last used this block has read it
+        if (p.blocks == 1 || t.rows > kBurstRows) bulk_wait_group_read0();
+        else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      }
       __syncwarp();
       uint8_t* b = stage + *blk * kEpiBlockBytes;
 #pragma unroll
@@ -249,7 +281,7 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
         else tma_store_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, t.expert);
         bulk_commit_group();
       }
-      if (++*blk == kEpiBlocks) *blk = 0;
+      if (++*blk == p.blocks) *blk = 0;
     }
   }
 }
@@ -267,17 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank() & 1u;
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
+  uint8_t* tail = smem + Smem::tail(p.blocks);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tail + Smem::bars);
   auto bar_full = [&](int s) { return smem_u32(&bars[s]); };               // this CTA's copies of a ragged end
   auto bar_ready = [&](int s) { return smem_u32(&bars[kStages + s]); };    // leader's: both CTAs' stages are whole
   auto bar_empty = [&](int s) { return smem_u32(&bars[2 * kStages + s]); };
   auto bar_tfull = [&](int b) { return smem_u32(&bars[3 * kStages + b]); };
   auto bar_tempty = [&](int b) { return smem_u32(&bars[3 * kStages + kAccBufs + b]); };
   const uint32_t bar_drain = smem_u32(&bars[3 * kStages + 2 * kAccBufs]);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::misc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
-  int* row_off = reinterpret_cast<int*>(smem + Smem::rows);
-  int* order = row_off + p.E + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tail + Smem::misc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tail + Smem::misc + 4);
+  int* row_off = reinterpret_cast<int*>(tail + Smem::rows);
+  uint16_t* order = reinterpret_cast<uint16_t*>(row_off + p.E + 1);
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -341,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at += other > mine || (other == mine && i < e);
       }
     }
-    order[at] = e;
+    order[at] = (uint16_t)e;
   }
   tc_fence_before();
   __syncthreads();
@@ -349,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   const uint32_t tmem_base = *s_tmem;
-  const int64_t total = (int64_t)p.E * p.mt * p.kt;
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
@@ -359,9 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      int64_t it = 0;
-      for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
-        const Tile t = locate(p, i, it, total, row_off, order);
+      int it = 0;
+      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
+        const Tile t = locate(p, i, it, row_off, order);
         const int n0 = t.n0 + (int)rank * kHalf, k0 = t.k0 + (int)rank * kHalf;
         const int na = boxes(p.N - n0), nb = boxes(p.K - k0);
         const int both = boxes(p.N - t.n0) + boxes(p.N - t.n0 - kHalf) + boxes(p.K - t.k0) + boxes(p.K - t.k0 - kHalf);
@@ -413,28 +445,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- ragged ends
     const uint32_t ready0 = map_to_rank(bar_ready(0), 0);
     uint32_t parity = 0;   // of each stage's next use of its full barrier
-    int64_t block = 0;     // stages filled before this tile
+    int s = 0;             // the stage of this tile's first rows
     bool ok = true;
-    int64_t it = 0;
-    for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
-      const Tile t = locate(p, i, it, total, row_off, order);
+    int it = 0;
+    for (int i = pair; i < p.total && ok; i += pairs, ++it) {
+      const Tile t = locate(p, i, it, row_off, order);
       if (t.rows == 0) continue;
-      block += (t.rows + kBR - 1) / kBR;
+      const int last = (s + (t.rows - 1) / kBR) % kStages;
       const int left = t.rows - (t.rows - 1) / kBR * kBR;  // rows of the last stage
+      s = last + 1 == kStages ? 0 : last + 1;
       if (!ragged(left)) continue;
-      const int s = (int)((block - 1) % kStages);
-      ok = warp_wait(bar_full(s), (parity >> s) & 1u, s_abort);
+      ok = warp_wait(bar_full(last), (parity >> last) & 1u, s_abort);
       if (!ok) break;
-      parity ^= 1u << s;
+      parity ^= 1u << last;
       // rows left .. the next multiple of 16 of every box (128-byte lines: the swizzle stays inside them)
       const int pieces = (16 - (left & 15)) * 8;
-      uint8_t* st = smem + Smem::stage + s * kStageBytes + left * 128;
+      uint8_t* st = smem + Smem::stage + last * kStageBytes + left * 128;
       for (int box = 0; box < 2 * kBoxes; ++box)
         for (int j = lane; j < pieces; j += 32)
           *reinterpret_cast<uint4*>(st + box * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(ready0 + (uint32_t)(s * 8));
+      if (lane == 0) mbar_arrive_cluster(ready0 + (uint32_t)(last * 8));
     }
     if (!ok && lane == 0) {
       flag_error(err, MOE_DEVERR_TIMEOUT);
@@ -451,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true, issued_any = false;
-      int64_t it = 0;
-      for (int64_t i = pair; i < total && ok; i += pairs, ++it) {
-        const Tile t = locate(p, i, it, total, row_off, order);
+      int it = 0;
+      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
+        const Tile t = locate(p, i, it, row_off, order);
         if (t.rows == 0) continue;
         if (!mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
           ok = false;
@@ -497,14 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------- epilogue (both CTAs)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
-    uint8_t* stage = smem + Smem::epi + (warp - 2) * kEpiStageBytes;
+    uint8_t* stage = smem + Smem::epi + (warp - 2) * p.blocks * kEpiBlockBytes;
     const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    int64_t it = 0;
+    int it = 0;
     int blk = 0;
-    for (int64_t i = pair; i < total; i += pairs, ++it) {
-      const Tile t = locate(p, i, it, total, row_off, order);
+    for (int i = pair; i < p.total; i += pairs, ++it) {
+      const Tile t = locate(p, i, it, row_off, order);
       const int row = t.n0 + (int)rank * kHalf + 32 * sub;
       if (t.rows == 0) {
         if (!p.accumulate) store_tile<F32>(p, t, row, lane, 0, true, stage, &blk, &map_dw);
@@ -576,7 +608,13 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     x = g.ws;
   }
-  Shape p{g.E, g.a_max, g.N, g.K, (g.N + kTile - 1) / kTile, (g.K + kTile - 1) / kTile, g.accumulate, 0};
+  const int mt = (g.N + kTile - 1) / kTile, kt = (g.K + kTile - 1) / kTile;
+  const int64_t tiles = (int64_t)g.E * mt * kt;
+  if (tiles > INT32_MAX / 2) return cudaErrorNotSupported;
+  Shape p{g.E,        g.a_max,      g.N,
+          g.K,        (int)tiles,   mt,
+          kt,         divisor(mt * kt), divisor(kGroup * kt),
+          divisor(mt % kGroup ? mt % kGroup : kGroup), g.accumulate, 0, g.E <= kTwoBlocksMaxE ? 2 : 1};
   const bool f32 = g.dw_dtype == MOE_DTYPE_F32;
   CUtensorMap dw, dy, mx;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
@@ -584,7 +622,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
                       !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR)))
     return cudaErrorInvalidValue;
-  const int smem = Smem::bytes_for(g.E) + 1024;
+  const int smem = Smem::bytes_for(g.E, p.blocks) + 1024;
   auto kern = f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -604,7 +642,6 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
   if (e != cudaSuccess) return e;
   if (pairs < 1) return cudaErrorNotSupported;
-  const int64_t tiles = (int64_t)g.E * p.mt * p.kt;
   if (tiles <= pairs) pairs = (int)tiles;       // one tile each
   else if (pairs > 1) pairs = pairs / 2 * 2;
   p.pairs_even = pairs % 2 == 0;
