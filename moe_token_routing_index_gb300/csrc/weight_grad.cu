@@ -11,12 +11,14 @@
 // memory receives its 128 rows of the tile.  Persistent, 7 warps per CTA:
 //   warp 0     TMA producer: 64 rows of this CTA's columns per stage (16 + 16 KB) into a
 //              6-stage ring guarded by mbarriers.
-//              Both CTAs' copies complete on the leader's barrier, except the last of an
-//              expert whose rows end inside a step of 16:
-//   warp 6     zeroes the rest of that step in its CTA's shared memory (those rows belong
-//              to the next expert, or to none, and may hold anything), then tells the
-//              leader.  Doing so for every stage, with the release that an arrival on the
-//              other CTA's barrier needs, held the products to 660 TFLOP/s.
+//              Both CTAs' copies complete on the leader's barrier.  Where an expert's rows
+//              end inside a step of 16, the rest of that step holds rows of the next expert,
+//              or of none, which may be anything: those copies complete on the CTA's own
+//              barrier, and then
+//   warp 6     writes zeros over them by copies from beyond the operand's last row, which
+//              complete on the leader's barrier in their turn.  (Zeroed by the threads, that
+//              needs a release at cluster scope, whose fence waits for the epilogue's
+//              stores: 16 experts of 509 rows, N = K = 4096, took 232 us that way.)
 //   warp 1     (leader) MMA issuer: M = 256, N = 256, 16 rows each, into one of two
 //              256-column accumulators.
 //   warps 2-5  epilogue: accumulator rows through a staging block to TMA stores (or fp32
@@ -129,10 +131,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // mbar_wait for arrivals that come from the other CTA of the pair too: acquires at cluster scope.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t t0 = 0;
@@ -181,8 +179,10 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 // not loaded: what they leave stale reaches only accumulator rows and columns that are not stored.
 __device__ __forceinline__ int boxes(int cols) { return max(0, min(kBoxes, (cols + kBoxCols - 1) / kBoxCols)); }
 
-// Whether the stage that starts with `left` rows of its expert to go ends inside a step of 16 rows.
-__device__ __forceinline__ bool ragged(int left) { return left < kBR && (left & 15) != 0; }
+// Whether the rows of an expert end inside a step of 16 rows, and the rows of that step to
+// zero.
+__device__ __forceinline__ bool ragged(int rows) { return (rows & 15) != 0; }
+__device__ __forceinline__ int zero_rows(int rows) { return 16 - (rows & 15); }
 
 // Arrival on the leader's barrier by a warp that has read its accumulator rows (tcgen05.wait::ld):
 // nothing it wrote has to be seen, so no release at cluster scope, whose fence would wait.
@@ -289,7 +289,8 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
-                       const __grid_constant__ CUtensorMap map_dw, const int32_t* __restrict__ counts, const Shape p,
+                       const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_zero4,
+                       const __grid_constant__ CUtensorMap map_zero1, const int32_t* __restrict__ counts, const Shape p,
                        unsigned int* err) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -403,7 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t dst = sbase + Smem::stage + s * kStageBytes;
-          if (ragged(t.rows - r)) {
+          if (t.rows - r <= kBR && ragged(t.rows)) {
+            if (leader) {  // the zeros of both CTAs
+              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)(both * zero_rows(t.rows)) * 128);
+              mbar_arrive(bar_ready(s));
+            }
             mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * kBoxBytes);
             for (int b = 0; b < na; ++b)
               tma_load_2d(dst + b * kBoxBytes, &map_dy, bar_full(s), n0 + b * kBoxCols, t.row0 + r);
@@ -444,33 +449,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 6) {
     // ------------------------------------------------------- ragged ends
     const uint32_t ready0 = map_to_rank(bar_ready(0), 0);
-    uint32_t parity = 0;   // of each stage's next use of its full barrier
-    int s = 0;             // the stage of this tile's first rows
-    bool ok = true;
-    int it = 0;
-    for (int i = pair; i < p.total && ok; i += pairs, ++it) {
-      const Tile t = locate(p, i, it, row_off, order);
-      if (t.rows == 0) continue;
-      const int last = (s + (t.rows - 1) / kBR) % kStages;
-      const int left = t.rows - (t.rows - 1) / kBR * kBR;  // rows of the last stage
-      s = last + 1 == kStages ? 0 : last + 1;
-      if (!ragged(left)) continue;
-      ok = warp_wait(bar_full(last), (parity >> last) & 1u, s_abort);
-      if (!ok) break;
-      parity ^= 1u << last;
-      // rows left .. the next multiple of 16 of every box (128-byte lines: the swizzle stays inside them)
-      const int pieces = (16 - (left & 15)) * 8;
-      uint8_t* st = smem + Smem::stage + last * kStageBytes + left * 128;
-      for (int box = 0; box < 2 * kBoxes; ++box)
-        for (int j = lane; j < pieces; j += 32)
-          *reinterpret_cast<uint4*>(st + box * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(ready0 + (uint32_t)(last * 8));
-    }
-    if (!ok && lane == 0) {
-      flag_error(err, MOE_DEVERR_TIMEOUT);
-      *s_abort = 1;
+    if (lane == 0) {
+      uint32_t parity = 0;   // of each stage's next use of its full barrier
+      int s = 0;             // the stage of this tile's first block
+      int it = 0;
+      bool ok = true;
+      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
+        const Tile t = locate(p, i, it, row_off, order);
+        if (t.rows == 0) continue;
+        const int before = (t.rows - 1) / kBR, left = t.rows - before * kBR;  // blocks before the last, its rows
+        const int mine = (s + before) % kStages;
+        s = mine + 1 == kStages ? 0 : mine + 1;
+        if (!ragged(t.rows)) continue;
+        ok = mbar_wait(bar_full(mine), (parity >> mine) & 1u, s_abort);
+        if (!ok) break;
+        parity ^= 1u << mine;
+        const int na = boxes(p.N - t.n0 - (int)rank * kHalf), nb = boxes(p.K - t.k0 - (int)rank * kHalf);
+        const uint32_t st = sbase + Smem::stage + mine * kStageBytes, ready = ready0 + (uint32_t)(mine * 8);
+        for (int b = 0; b < 2 * kBoxes; ++b) {
+          if (b < kBoxes ? b >= na : b - kBoxes >= nb) continue;
+          // 128-byte lines: the operand's swizzle stays inside them
+          uint32_t at = st + b * kBoxBytes + left * 128, end = at + zero_rows(t.rows) * 128;
+          for (; at + 512 <= end; at += 512) tma_load_2d_pair(at, &map_zero4, ready, 0, p.a_max);
+          for (; at < end; at += 128) tma_load_2d_pair(at, &map_zero1, ready, 0, p.a_max);
+        }
+      }
+      if (!ok) {
+        flag_error(err, MOE_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        const uint64_t t0 = global_timer_ns();  // copies in flight complete on the leader's barrier: let them land
+        while (global_timer_ns() - t0 < kDrainTimeoutNs) {
+        }
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA (leader)
@@ -586,6 +596,20 @@ bool make_dw_map(CUtensorMap* map, void* base, int E, int N, int K, bool f32) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of `rows` rows x 128 bytes of dY without a swizzle: read past its last row, they are
+// zeros.  (N columns of 2 bytes; N may be below the box's 64.)
+bool make_zero_map(CUtensorMap* map, const void* dy, int a_max, int N, int rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)a_max};
+  cuuint64_t strides[1] = {(cuuint64_t)N * 2};
+  cuuint32_t box[2] = {kBoxCols, (cuuint32_t)rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(dy), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 size_t weight_grad_workspace_bytes(int, int a_max, int, int K, bool packed) {
@@ -616,11 +640,12 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
           kt,         divisor(mt * kt), divisor(kGroup * kt),
           divisor(mt % kGroup ? mt % kGroup : kGroup), g.accumulate, 0, g.E <= kTwoBlocksMaxE ? 2 : 1};
   const bool f32 = g.dw_dtype == MOE_DTYPE_F32;
-  CUtensorMap dw, dy, mx;
+  CUtensorMap dw, dy, mx, z4, z1;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
-  dy = mx = dw;  // without rows nothing is loaded
+  dy = mx = z4 = z1 = dw;  // without rows nothing is loaded
   if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
-                      !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR)))
+                      !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR) ||
+                      !make_zero_map(&z4, g.dy, g.a_max, g.N, 4) || !make_zero_map(&z1, g.dy, g.a_max, g.N, 1)))
     return cudaErrorInvalidValue;
   const int smem = Smem::bytes_for(g.E, p.blocks) + 1024;
   auto kern = f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
@@ -646,7 +671,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   else if (pairs > 1) pairs = pairs / 2 * 2;
   p.pairs_even = pairs % 2 == 0;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, g.counts, p, g.err);
+  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, g.counts, p, g.err);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
