@@ -26,9 +26,10 @@
 // An expert without rows has its tiles written as zeros by the epilogue alone.
 //
 // A tile costs its store whatever its rows, and its products by its rows: the tiles of
-// experts with many rows are bound by the tensor cores, the others by memory.  The experts
-// are therefore ordered by their rows, and each pair takes tiles from the two ends of that
-// order in turn, so that both kinds run at any time.
+// experts with many rows are bound by the tensor cores, the others by memory.  So that both
+// are busy at any time, the experts are ordered by their rows, and each pair works through
+// its tiles of that order from both ends at once, a long one in one accumulator and short
+// ones in the other (Schedule).
 //
 // Every mbarrier wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT,
 // all roles stop, copies and MMAs in flight are drained, and tensor memory is freed.
@@ -93,7 +94,6 @@ struct Shape {
   Divisor band;      // tiles of a group of kGroup along N
   Divisor last;      // tiles along N of an expert's last group
   int accumulate;
-  int pairs_even;    // an even number of pairs
   int blocks;        // staging blocks of an epilogue warp
 };
 
@@ -194,16 +194,9 @@ struct Tile {
   int expert, n0, k0, row0, rows;
 };
 
-// The pair's it-th tile (sequence number i = it * pairs + pair).  Even sequence numbers
-// count from the front of the expert order, odd ones from its back; a pair changes ends
-// every time (an even number of pairs: then the two of i and i ^ 1 are in the same turn).
-// An expert's tiles come in groups of kGroup along N, N innermost, so that the pairs
-// running together read few columns of either operand.
-__device__ __forceinline__ Tile locate(const Shape& p, int i, int it, const int* row_off,
-                                       const uint16_t* order) {
-  const int j = i ^ (it & p.pairs_even);
-  if (j < p.total) i = j;
-  const int tile = (i & 1) ? p.total - 1 - (i >> 1) : i >> 1;
+// Tile `tile` in the order of the experts' ranks.  An expert's tiles come in groups of kGroup
+// along N, N innermost, so that the pairs running together read few columns of either operand.
+__device__ __forceinline__ Tile locate(const Shape& p, int tile, const int* row_off, const uint16_t* order) {
   Tile t;
   const int rank = quotient(tile, p.per);
   t.expert = order[rank];
@@ -217,6 +210,59 @@ __device__ __forceinline__ Tile locate(const Shape& p, int i, int it, const int*
   t.row0 = row_off[t.expert];
   t.rows = row_off[t.expert + 1] - t.row0;
   return t;
+}
+
+// A pair's work in order, the same for all of its roles.  Its tiles are every pairs-th of
+// the order of ranks, most rows first; accumulator 0 takes them from the front and
+// accumulator 1 from the back until they meet.  A tile from the back is multiplied whole;
+// of the one from the front kChunk blocks follow each time, the time that storing a tile
+// takes, or all that is left when that is no more than twice as many.  Tiles of one length
+// so alternate between the accumulators.  On 128 experts of Zipf-like load, N = 7168,
+// K = 2048, taking whole tiles from the two ends in turn took 990 us.
+constexpr int kChunk = 6;
+
+struct Schedule {
+  int pair, pairs, front, back;  // the next tile of this pair from either end
+  int done;                      // blocks multiplied of the front's tile, 0: none is under way
+  bool short_turn;
+  Tile t;                        // the front's tile
+
+  __device__ Schedule(const Shape& p, int pair_, int pairs_)
+      : pair(pair_), pairs(pairs_), front(0), back((p.total - 1 - pair_) / pairs_), done(0), short_turn(true) {}
+};
+
+// Blocks first .. first + count - 1 of a tile of `blocks` blocks, in accumulator acc.
+struct Chunk {
+  Tile t;
+  int acc, first, count, blocks;
+};
+
+__device__ __forceinline__ bool next_chunk(Schedule& w, const Shape& p, const int* row_off, const uint16_t* order,
+                                           Chunk* c) {
+  const bool take_back = w.short_turn && w.front <= w.back;
+  w.short_turn = !take_back;
+  if (take_back) {
+    c->t = locate(p, w.pair + w.back * w.pairs, row_off, order);
+    --w.back;
+    c->acc = 1;
+    c->first = 0;
+    c->count = c->blocks = (c->t.rows + kBR - 1) / kBR;
+    return true;
+  }
+  if (w.done == 0) {
+    if (w.front > w.back) return false;
+    w.t = locate(p, w.pair + w.front * w.pairs, row_off, order);
+    ++w.front;
+  }
+  c->t = w.t;
+  c->acc = 0;
+  c->blocks = (w.t.rows + kBR - 1) / kBR;
+  c->first = w.done;
+  const int left = c->blocks - w.done;
+  c->count = left <= 2 * kChunk || w.front > w.back ? left : kChunk;
+  w.done += c->count;
+  if (w.done == c->blocks) w.done = 0;
+  return true;
 }
 
 // 64 consecutive fp32 accumulator columns of this thread's TMEM lane.
@@ -392,13 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      int it = 0;
-      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
-        const Tile t = locate(p, i, it, row_off, order);
+      Schedule work(p, pair, pairs);
+      Chunk c;
+      while (ok && next_chunk(work, p, row_off, order, &c)) {
+        const Tile& t = c.t;
         const int n0 = t.n0 + (int)rank * kHalf, k0 = t.k0 + (int)rank * kHalf;
         const int na = boxes(p.N - n0), nb = boxes(p.K - k0);
         const int both = boxes(p.N - t.n0) + boxes(p.N - t.n0 - kHalf) + boxes(p.K - t.k0) + boxes(p.K - t.k0 - kHalf);
-        for (int r = 0; r < t.rows; r += kBR) {
+        for (int r = c.first * kBR; r < min((c.first + c.count) * kBR, t.rows); r += kBR) {
           if (!mbar_wait(bar_empty(s), phase ^ 1u, s_abort)) {
             ok = false;
             break;
@@ -451,16 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ready0 = map_to_rank(bar_ready(0), 0);
     if (lane == 0) {
       uint32_t parity = 0;   // of each stage's next use of its full barrier
-      int s = 0;             // the stage of this tile's first block
-      int it = 0;
+      int s = 0;             // the stage of this chunk's first block
       bool ok = true;
-      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
-        const Tile t = locate(p, i, it, row_off, order);
-        if (t.rows == 0) continue;
-        const int before = (t.rows - 1) / kBR, left = t.rows - before * kBR;  // blocks before the last, its rows
-        const int mine = (s + before) % kStages;
+      Schedule work(p, pair, pairs);
+      Chunk c;
+      while (ok && next_chunk(work, p, row_off, order, &c)) {
+        const Tile& t = c.t;
+        if (c.count == 0) continue;
+        const int mine = (s + c.count - 1) % kStages, left = t.rows - (c.blocks - 1) * kBR;
         s = mine + 1 == kStages ? 0 : mine + 1;
-        if (!ragged(t.rows)) continue;
+        if (c.first + c.count < c.blocks || !ragged(t.rows)) continue;
         ok = mbar_wait(bar_full(mine), (parity >> mine) & 1u, s_abort);
         if (!ok) break;
         parity ^= 1u << mine;
@@ -490,20 +537,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                              ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
       int s = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      uint32_t acc_parity = 0;  // of each accumulator's next use
       bool ok = true, issued_any = false;
-      int it = 0;
-      for (int i = pair; i < p.total && ok; i += pairs, ++it) {
-        const Tile t = locate(p, i, it, row_off, order);
-        if (t.rows == 0) continue;
-        if (!mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
-          ok = false;
-          break;
+      Schedule work(p, pair, pairs);
+      Chunk c;
+      while (ok && next_chunk(work, p, row_off, order, &c)) {
+        const Tile& t = c.t;
+        if (c.count == 0) continue;
+        if (c.first == 0) {
+          if (!mbar_wait_cluster(bar_tempty(c.acc), ((acc_parity >> c.acc) & 1u) ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
         }
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * kTile);
-        for (int r = 0; r < t.rows; r += kBR) {
+        const uint32_t d = tmem_base + (uint32_t)(c.acc * kTile);
+        for (int r = c.first * kBR; r < min((c.first + c.count) * kBR, t.rows); r += kBR) {
           if (!mbar_wait_cluster(bar_ready(s), phase, s_abort)) {
             ok = false;
             break;
@@ -521,10 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        mma_commit_pair(bar_tfull(acc));
-        if (++acc == kAccBufs) {
-          acc = 0;
-          acc_phase ^= 1u;
+        if (c.first + c.count == c.blocks) {
+          mma_commit_pair(bar_tfull(c.acc));
+          acc_parity ^= 1u << c.acc;
         }
       }
       if (!ok) {
@@ -541,32 +589,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
     uint8_t* stage = smem + Smem::epi + (warp - 2) * p.blocks * kEpiBlockBytes;
     const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    int it = 0;
+    uint32_t acc_parity = 0;
     int blk = 0;
-    for (int i = pair; i < p.total; i += pairs, ++it) {
-      const Tile t = locate(p, i, it, row_off, order);
-      const int row = t.n0 + (int)rank * kHalf + 32 * sub;
-      if (t.rows == 0) {
-        if (!p.accumulate) store_tile<F32>(p, t, row, lane, 0, true, stage, &blk, &map_dw);
+    Schedule work(p, pair, pairs);
+    Chunk c;
+    while (next_chunk(work, p, row_off, order, &c)) {
+      if (c.first + c.count < c.blocks) continue;
+      const int row = c.t.n0 + (int)rank * kHalf + 32 * sub;
+      if (c.t.rows == 0) {
+        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw);
         continue;
       }
-      if (!warp_wait(bar_tfull(acc), acc_phase, s_abort)) {
+      if (!warp_wait(bar_tfull(c.acc), (acc_parity >> c.acc) & 1u, s_abort)) {
         if (lane == 0) flag_error(err, MOE_DEVERR_TIMEOUT);
         *s_abort = 1;
         break;
       }
+      acc_parity ^= 1u << c.acc;
       tc_fence_after();
-      store_tile<F32>(p, t, row, lane, tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kTile), false, stage,
-                      &blk, &map_dw);
+      store_tile<F32>(p, c.t, row, lane, tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(c.acc * kTile), false,
+                      stage, &blk, &map_dw);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
-      if (++acc == kAccBufs) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(c.acc * 8));
     }
     if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the block exits
   }
@@ -638,7 +683,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   Shape p{g.E,        g.a_max,      g.N,
           g.K,        (int)tiles,   mt,
           kt,         divisor(mt * kt), divisor(kGroup * kt),
-          divisor(mt % kGroup ? mt % kGroup : kGroup), g.accumulate, 0, g.E <= kTwoBlocksMaxE ? 2 : 1};
+          divisor(mt % kGroup ? mt % kGroup : kGroup), g.accumulate, g.E <= kTwoBlocksMaxE ? 2 : 1};
   const bool f32 = g.dw_dtype == MOE_DTYPE_F32;
   CUtensorMap dw, dy, mx, z4, z1;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
@@ -667,9 +712,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
   if (e != cudaSuccess) return e;
   if (pairs < 1) return cudaErrorNotSupported;
-  if (tiles <= pairs) pairs = (int)tiles;       // one tile each
-  else if (pairs > 1) pairs = pairs / 2 * 2;
-  p.pairs_even = pairs % 2 == 0;
+  if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs);
   e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, g.counts, p, g.err);
   if (e != cudaSuccess) return e;
