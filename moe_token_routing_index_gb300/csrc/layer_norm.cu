@@ -533,8 +533,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Rows straight into registers.
+// Blocks of a direct kernel that share an SM's registers: with single columns one row in
+// flight does not hide its loads (5000 rows of 4097 in bf16 took 110 us so).
+constexpr int direct_blocks(int vec, int threads) { return vec == 1 ? (threads <= 320 ? 3 : 2) : 1; }
+
 template <typename T, typename W, int VEC, int N, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_kernel(const NormArgs g, int R, float inv_d) {
+__global__ void __launch_bounds__(THREADS, direct_blocks(VEC, THREADS)) norm_kernel(const NormArgs g, int R, float inv_d) {
   __shared__ float2 s_sum[2][2][THREADS / 32];  // by turns, two sums of each warp
   const int groups = blockDim.x / R, group = threadIdx.x / R, gt = threadIdx.x - group * R;
   const int n = read_count(g.valid, g.T, g.err), D = g.D;
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const NormArgs g, int 
 }
 
 template <typename T, typename W, int VEC, int N, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const NormArgs g, int R, float inv_d, float* partial) {
+__global__ void __launch_bounds__(THREADS, VEC == 1 && THREADS <= 512 ? 2 : 1) norm_grad_kernel(const NormArgs g, int R, float inv_d, float* partial) {
   extern __shared__ __align__(128) uint8_t s_mem[];  // the groups' sums
   __shared__ float2 s_sum[2][THREADS / 32];
   pdl_launch_dependents();
@@ -691,13 +695,12 @@ constexpr int kForwardThreads = 768;  // of a ring kernel's block, in whole grou
 constexpr int kBackwardThreads = 512;
 constexpr int kRingBytes = 216 * 1024;
 
-// The backward's grid: a block for each SM, fewer for few rows (its workspace size is asked
-// for without a GPU, or the rows' alignment: no kernel has more groups in a block).
-int grad_blocks(int T, int D) {
-  const int groups = shape(D, D <= 8 * 32 ? 8 : D <= kWarpColumns ? 16 : kRingValues, kBackwardThreads).groups;
-  const int64_t need = ((int64_t)T + groups - 1) / groups;
-  return (int)(need < kNumSmsGB300 ? need : kNumSmsGB300);
+// The backward's grid: up to `each` blocks for each SM, fewer for few rows.
+int grad_blocks(int T, const Shape& sh, int each) {
+  const int64_t need = ((int64_t)T + sh.groups - 1) / sh.groups, most = (int64_t)kNumSmsGB300 * each;
+  return (int)(need < most ? need : most);
 }
+constexpr int kMaxGradEach = 2;
 
 // The ring kernels' shape: the most groups that leave two stages or more for each beside
 // `fixed` bytes; stages 0: none do.
@@ -724,30 +727,32 @@ cudaError_t forward_ring(const NormArgs& g, const Shape& sh, int stages, cudaStr
 template <typename T, typename W, int VEC, int N, int THREADS>
 cudaError_t forward(const NormArgs& g, const Shape& sh, cudaStream_t s) {
   const int64_t need = ((int64_t)g.T + sh.groups - 1) / sh.groups;
-  const int64_t most = (int64_t)device_sm_count() * (2048 / THREADS);
+  const int64_t most = (int64_t)device_sm_count() * (VEC == 1 ? direct_blocks(VEC, THREADS) : 2048 / THREADS);
   norm_kernel<T, W, VEC, N, THREADS>
       <<<(int)(need < most ? need : most), sh.groups * sh.R, 0, s>>>(g, sh.R, 1.0f / g.D);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t backward_ring(const NormArgs& g, const Shape& sh, int stages, cudaStream_t s) {
+cudaError_t backward_ring(const NormArgs& g, const Shape& sh, int stages, int* blocks, cudaStream_t s) {
   auto kern = norm_grad_ring_kernel<T, kBackwardThreads>;
   size_t smem = (size_t)4 * g.D + (size_t)sh.groups * stages * 2 * g.D * sizeof(T);
   if (smem < (size_t)sh.groups * 8 * g.D) smem = (size_t)sh.groups * 8 * g.D;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grad_blocks(g.T, g.D), sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, stages, static_cast<float*>(g.ws));
+  *blocks = grad_blocks(g.T, sh, 1);
+  kern<<<*blocks, sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, stages, static_cast<float*>(g.ws));
   return cudaGetLastError();
 }
 
 template <typename T, typename W, int VEC, int N, int THREADS>
-cudaError_t backward(const NormArgs& g, const Shape& sh, cudaStream_t s) {
+cudaError_t backward(const NormArgs& g, const Shape& sh, int* blocks, cudaStream_t s) {
   auto kern = norm_grad_kernel<T, W, VEC, N, THREADS>;
   const size_t smem = (size_t)sh.groups * 8 * g.D;  // at most 128 KB: one group of 16384 columns
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grad_blocks(g.T, g.D), sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, static_cast<float*>(g.ws));
+  *blocks = grad_blocks(g.T, sh, VEC == 1 ? kMaxGradEach : 1);
+  kern<<<*blocks, sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, static_cast<float*>(g.ws));
   return cudaGetLastError();
 }
 
@@ -769,37 +774,39 @@ cudaError_t launch_layer_norm(const NormArgs& g, cudaStream_t s) {
       if (stages) return forward_ring<T, kForwardThreads>(g, sh, stages, s);
       return forward<T, W, VEC, 32, 512>(g, sh, s);
     } else {
-      if (D <= 8 * 1024) return forward<T, W, VEC, 8, 1024>(g, shape(D, 8, 1024), s);
-      return forward<T, W, VEC, 16, 1024>(g, shape(D, 16, 1024), s);
+      if (D <= 8 * 256) return forward<T, W, VEC, 8, 256>(g, shape(D, 8, 256), s);
+      if (D <= 16 * 512) return forward<T, W, VEC, 16, 512>(g, shape(D, 16, 512), s);
+      return forward<T, W, VEC, 32, 512>(g, shape(D, 32, 512), s);
     }
   });
 }
 
 size_t layer_norm_backward_workspace_bytes(int T, int D) {
   if (D == 0) return 0;
-  return (size_t)grad_blocks(T, D) * 2 * D * sizeof(float);
+  // of the kernel with the most blocks (which one runs goes by the rows' alignment too)
+  const int64_t most = (int64_t)kNumSmsGB300 * kMaxGradEach;
+  return (size_t)(T < most ? T : most) * 2 * D * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_backward(const NormArgs& g, cudaStream_t s) {
-  const int blocks = grad_blocks(g.T, g.D);
-  if (blocks > 0) {
+  int blocks = 0;
+  if (g.T > 0) {
     cudaError_t e = by_types(g, [&](auto x, auto w, auto vec) {
       using T = decltype(x);
       using W = decltype(w);
       constexpr int VEC = decltype(vec)::v;
       const int D = g.D;
       if constexpr (VEC == 8) {
-        if (D <= 8 * 32) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), s);
-        if (D <= kWarpColumns) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), s);
+        if (D <= 8 * 32) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
+        if (D <= kWarpColumns) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
         int stages;
         const Shape sh = ring_shape(D, kBackwardThreads, (int64_t)4 * D, (int64_t)2 * D * sizeof(T), &stages);
-        if (stages) return backward_ring<T>(g, sh, stages, s);
-        return backward<T, W, VEC, 32, 512>(g, sh, s);
+        if (stages) return backward_ring<T>(g, sh, stages, &blocks, s);
+        return backward<T, W, VEC, 32, 512>(g, sh, &blocks, s);
       } else {
-        // single columns: 1003 rows of 2051 in fp32 take 17.3 us so, 18.9 with 8 values and up to 1024 threads
-        if (D <= 8 * 32) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), s);
-        if (D <= 16 * 320) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), s);
-        return backward<T, W, VEC, 16, 1024>(g, shape(D, 16, 1024), s);
+        if (D <= 8 * 320) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
+        if (D <= 16 * 320) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
+        return backward<T, W, VEC, 16, 1024>(g, shape(D, 16, 1), &blocks, s);
       }
     });
     if (e != cudaSuccess) return e;
