@@ -111,12 +111,19 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it, which costs a call 2.6 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -581,8 +588,8 @@ def _output(t, shape, dtype, device, name: str) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
     return t
 
 
@@ -592,11 +599,9 @@ def _norm_inputs(x, gamma, beta=None) -> int:
         raise ValueError(f"x must be [T, D], got {tuple(x.shape)}")
     _need(x, x.dtype, "x", contiguous=False)
     D = x.shape[1]
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _need(t, gamma.dtype, name)
-            if tuple(t.shape) != (D,):
-                raise ValueError(f"{name} must have the shape ({D},), got {tuple(t.shape)}")
+    _output(gamma, (D,), gamma.dtype, x.device, "gamma")
+    if beta is not None:
+        _output(beta, (D,), gamma.dtype, x.device, "beta")
     return D
 
 
