@@ -137,6 +137,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
     """dtype, device and layout checks of a matrix argument: the C ABI reads it as a
     dense row-major array (contiguous=False: only the last dimension must be dense)."""
+    if t.dtype == dtype and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -682,12 +684,12 @@ def moe_balance_loss(scores, top_k: int, num_valid_tokens=None, *, kind: int = M
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     mean_probs = torch.empty(E, dtype=torch.float32, device=dev)
     made = torch.empty(E + 1, dtype=torch.int32, device=dev) if counts is None else None
-    if workspace is None:
-        workspace = torch.empty(moe_balance_loss_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    if workspace is None and (ws_bytes := moe_balance_loss_workspace_size(T, E)):
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     st = _lib.moe_balance_loss(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E, top_k,
                                kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(counts),
-                               _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace), workspace.numel(),
-                               _stream(stream))
+                               _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace),
+                               0 if workspace is None else workspace.numel(), _stream(stream))
     _check("moe_balance_loss", st)
     return loss, made if counts is None else counts, mean_probs
 

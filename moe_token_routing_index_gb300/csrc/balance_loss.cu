@@ -1,5 +1,16 @@
 // The router's load-balance loss, per-expert counts and its gradient
-// (include/moe_train.h).  A warp owns a token; lane l holds experts l, l + 32, ...
+// (include/moe_train.h).
+//
+// LANES lanes of a warp own a token, V neighbouring experts each (4 x 4 lanes for 16
+// experts up to 32 x 32 for 1024), so a lane's experts stay the same from token to token
+// and their sums of p and counts stay in registers.  Blocks leave partial sums; one block
+// adds them in order.  A batch that one block gets through is a single launch.
+//
+// The top_k largest of a token: top_k rounds of the largest value below the last one
+// found, over the lane, then over the lanes; the last is the threshold.  Of bf16 inputs
+// the key carries the expert below the value, so that keys differ and ties fall to the
+// lower expert; fp32 inputs that tie in value are noticed by their count and selected
+// again one by one.  The rounds bind the forward (65536 x 128 fp32, top 8): not memory.
 #include "common.cuh"
 #include "launch.h"
 #include "train_launch.h"
@@ -7,14 +18,86 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 304;
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kMaxWarps = 32;
+constexpr int kOneBlockTurns = 4;  // turns of a block's tokens up to which it does a batch alone
 
-__device__ __forceinline__ float warp_sum(float v) {
+// How the selection is made: the counts are given, or by keys of bf16 or fp32 inputs.
+enum Select { kGiven, kBf16Keys, kF32Keys };
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
+}
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (LANES == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+  }
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return ~group_max<LANES>(~v);
+}
+template <int LANES>
+__device__ __forceinline__ int group_count(int v) {
+  if constexpr (LANES == 32) {
+    return __reduce_add_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  }
+}
+
+// A lane's V values of token t from expert e0 on (0 past E).  wide: its experts are whole
+// 8- or 16-byte pieces of a dense row.
+template <int V>
+__device__ __forceinline__ void load_values(const BalanceArgs& g, int64_t t, int e0, bool wide, float* a) {
+  if (wide) {
+    if (e0 >= g.E) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[i] = 0.0f;
+    } else if (g.dtype == MOE_DTYPE_F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g.scores) + t * g.stride_t + e0);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 v = __ldg(p + i);
+        a[4 * i] = v.x;
+        a[4 * i + 1] = v.y;
+        a[4 * i + 2] = v.z;
+        a[4 * i + 3] = v.w;
+      }
+    } else {
+      const uint2* p =
+          reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g.scores) + t * g.stride_t + e0);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const uint2 v = __ldg(p + i);
+        const float2 lo = bf16x2_bits_to_f32(v.x), hi = bf16x2_bits_to_f32(v.y);
+        a[4 * i] = lo.x;
+        a[4 * i + 1] = lo.y;
+        a[4 * i + 2] = hi.x;
+        a[4 * i + 3] = hi.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    a[i] = e0 + i < g.E ? load_score(g.scores, g.dtype, t * g.stride_t + (e0 + i) * g.stride_e) : 0.0f;
 }
 
 // sigmoid(a) and 1 - sigmoid(a) = sigmoid(-a), each to full relative precision: from
@@ -25,39 +108,111 @@ __device__ __forceinline__ void sigmoid_both(float a, float* s, float* rest) {
   *rest = a >= 0.0f ? er : r;
 }
 
-// The token's row a[V] (padding: 0) becomes unnormalised weights in place, rest[V] (SIGMOID)
-// what each sigmoid lacks to 1; returns 1 / the sum of the weights, or 0.
-template <int V, int KIND>
-__device__ __forceinline__ float weights(float* a, float* rest, int E, int lane) {
-  if (KIND == MOE_BALANCE_SOFTMAX) {
+// The token's values become unnormalised weights in place (0 past E), rest[V] what each
+// sigmoid lacks to 1; returns 1 / the sum of the weights, or 0.
+template <int V, int LANES>
+__device__ __forceinline__ float weights(float* a, float* rest, int kind, int E, int e0) {
+  if (kind == MOE_BALANCE_SOFTMAX) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < E) m = fmaxf(m, a[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (e0 + i < E) m = fmaxf(m, a[i]);
+    m = group_max<LANES>(m);
     if (m == -INFINITY) m = 0.0f;  // every expert masked: all weights are 0
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = lane + 32 * i < E ? __expf(a[i] - m) : 0.0f;
-  } else if (KIND == MOE_BALANCE_SIGMOID) {
+    for (int i = 0; i < V; ++i) a[i] = e0 + i < E ? __expf(a[i] - m) : 0.0f;
+  } else if (kind == MOE_BALANCE_SIGMOID) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       sigmoid_both(a[i], a + i, rest + i);
-      if (lane + 32 * i >= E) a[i] = 0.0f;
+      if (e0 + i >= E) a[i] = 0.0f;
     }
   }
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) s += a[i];
-  s = warp_sum(s);
+  s = group_sum<LANES>(s);
   return s == 0.0f ? 0.0f : 1.0f / s;
 }
 
-template <int V, int KIND, bool SELECT>
-__global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceArgs g, float* psum, int* csum) {
-  extern __shared__ float sh[];  // [kWarps][E] p sums, then [kWarps][E] counts
+// Which of the lane's values are among the token's k largest, one bit each.
+template <int V, int LANES, int SELECT>
+__device__ __forceinline__ uint32_t choose(const float* a, int k, int E, int e0) {
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = route_order_key(a[i]);
+    // a bf16 value's order is in the upper half of its key; the lower expert is the larger key
+    if (SELECT == kBf16Keys) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - (e0 + i));
+    if (e0 + i >= E) key[i] = 0u;
+  }
+  uint32_t limit = kAll;
+  for (int r = 0; r < k; ++r) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, key[i] < limit ? key[i] : 0u);
+    limit = group_max<LANES>(m);
+  }
+  uint32_t bits = 0u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) bits |= (key[i] >= limit && e0 + i < E ? 1u : 0u) << i;
+  if (SELECT == kF32Keys && __any_sync(kAll, group_count<LANES>(__popc(bits)) != k)) {
+    // equal values among them: one at a time, the lowest expert of the largest value
+    bits = 0u;
+    for (int r = 0; r < k; ++r) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = max(m, key[i]);
+      m = group_max<LANES>(m);
+      uint32_t at = kAll;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (key[i] == m && e0 + i < E) at = (uint32_t)(e0 + i);
+      at = group_min<LANES>(at);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (at == (uint32_t)(e0 + i)) {
+          key[i] = 0u;
+          bits |= 1u << i;
+        }
+    }
+  }
+  return bits;
+}
+
+// The loss, mean_probs and counts from each expert's sum of p and count: threads e < E hold
+// them, all threads of a block of up to 1024 call it.
+__device__ __forceinline__ void finish(const BalanceArgs& g, int n, int e, float p, int c) {
+  __shared__ float s_loss[kMaxWarps];
+  float part = 0.0f;
+  if (e < g.E) {
+    if (g.counts_in) c = __ldg(g.counts_in + e);
+    else g.counts_out[e] = c;
+    p = n > 0 ? p / n : 0.0f;
+    g.mean_probs[e] = p;
+    if (n > 0) part = (float)c * ((float)g.E / ((float)g.top_k * n)) * p;
+  }
+  part = group_sum<32>(part);
+  if ((threadIdx.x & 31) == 0) s_loss[threadIdx.x >> 5] = part;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float l = 0.0f;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) l += s_loss[i];
+    *g.loss = g.coefficient * l;
+    if (!g.counts_in) g.counts_out[g.E] = n * g.top_k;
+  }
+}
+
+// partial: [blocks][2][E], p sums and (as int) counts; unused by a single block.
+template <int V, int LANES, int SELECT>
+__global__ void __launch_bounds__(V <= 8 ? 1024 : 256)
+    balance_kernel(const BalanceArgs g, bool wide, float* partial) {
+  extern __shared__ float sh[];  // [warps][E] p sums, then [warps][E] counts
+  pdl_launch_dependents();
+  constexpr int TOKENS = 32 / LANES;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
+  const int e0 = (lane & (LANES - 1)) * V;
   const int n = read_count(g.valid, g.T, g.err);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
   float ps[V];
   int cs[V];
 #pragma unroll
@@ -65,197 +220,246 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceArgs g, 
     ps[i] = 0.0f;
     cs[i] = 0;
   }
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < n; t += (int64_t)gridDim.x * kWarps) {
-    float a[V];
+  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
+  for (int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS; t0 < n; t0 += stride) {
+    const int64_t t = t0 + lane / LANES;
+    const bool live = t < n;
+    float a[V], rest[V];
+    load_values<V>(g, live ? t : t0, e0, wide, a);
+    if (SELECT != kGiven) {
+      uint32_t bits = choose<V, LANES, SELECT>(a, g.top_k, E, e0);
+      if (!live) bits = 0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      a[i] = e < E ? load_score(g.scores, g.dtype, t * g.stride_t + e * g.stride_e) : 0.0f;
+      for (int i = 0; i < V; ++i) cs[i] += (bits >> i) & 1u;
     }
-    if (SELECT) {
-      uint32_t key[V];
+    float inv = weights<V, LANES>(a, rest, g.kind, E, e0);
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < E ? route_order_key(a[i]) : 0u;
-      for (int k = 0; k < g.top_k; ++k) {
-        uint32_t m = 0;
+    for (int i = 0; i < V; ++i)
+      if (live) ps[i] += a[i] * inv;  // (a row past the count may hold anything)
+  }
+  // the warp's groups, then the block's warps, in order
+  int* shc = reinterpret_cast<int*>(sh + warps * E);
 #pragma unroll
-        for (int i = 0; i < V; ++i) m = max(m, key[i]);
-        m = __reduce_max_sync(0xffffffffu, m);
-        unsigned at = 0xffffffffu;
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-          if (key[i] == m) at = lane + 32 * i;
-        at = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at == (unsigned)(lane + 32 * i)) {
-            key[i] = 0u;
-            ++cs[i];
-          }
+    for (int o = LANES; o < 32; o <<= 1) {
+      ps[i] += __shfl_xor_sync(kAll, ps[i], o);
+      if (SELECT != kGiven) cs[i] += __shfl_xor_sync(kAll, cs[i], o);
+    }
+    if (lane < LANES && e0 + i < E) {
+      sh[warp * E + e0 + i] = ps[i];
+      if (SELECT != kGiven) shc[warp * E + e0 + i] = cs[i];
+    }
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1 && E <= (int)blockDim.x;
+  for (int e = threadIdx.x; e < E || (alone && e < (int)blockDim.x); e += blockDim.x) {
+    float p = 0.0f;
+    int c = 0;
+    if (e < E)
+      for (int w = 0; w < warps; ++w) {
+        p += sh[w * E + e];
+        if (SELECT != kGiven) c += shc[w * E + e];
       }
+    if (alone) {
+      finish(g, n, e, p, c);
+      return;
     }
-    float rest[V];
-    const float inv = weights<V, KIND>(a, rest, E, lane);
-#pragma unroll
-    for (int i = 0; i < V; ++i) ps[i] += a[i] * inv;
-  }
-  int* shc = reinterpret_cast<int*>(sh + kWarps * E);
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane + 32 * i < E) {
-      sh[warp * E + lane + 32 * i] = ps[i];
-      if (SELECT) shc[warp * E + lane + 32 * i] = cs[i];
-    }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float p = 0.0f;
-    int c = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      p += sh[w * E + e];
-      if (SELECT) c += shc[w * E + e];
-    }
-    psum[(int64_t)blockIdx.x * E + e] = p;
-    if (SELECT) csum[(int64_t)blockIdx.x * E + e] = c;
+    partial[(int64_t)blockIdx.x * 2 * E + e] = p;
+    if (SELECT != kGiven) partial[((int64_t)blockIdx.x * 2 + 1) * E + e] = __int_as_float(c);
   }
 }
 
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs g, int blocks, const float* psum,
-                                                              const int* csum) {
-  __shared__ float s_loss[32];
-  const int n = read_count(g.valid, g.T, nullptr), E = g.E, e = threadIdx.x;
-  float part = 0.0f;
-  if (e < E) {
-    float p = 0.0f;
-    int c = 0;
-    for (int b = 0; b < blocks; ++b) {
-      p += psum[(int64_t)b * E + e];
-      if (!g.counts_in) c += csum[(int64_t)b * E + e];
+// Adds the blocks' partial sums: 1024 / width threads of each expert (width: a power of two,
+// at least E) take every so manieth block's, and are added in order.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs g, const float* __restrict__ partial,
+                                                              int blocks, int width) {
+  __shared__ float s_p[1024];
+  __shared__ int s_c[1024];
+  pdl_wait();
+  const int n = read_count(g.valid, g.T, nullptr), E = g.E;
+  const int e = threadIdx.x & (width - 1), part = threadIdx.x / width, parts = 1024 / width;
+  float p = 0.0f;
+  int c = 0;
+  if (e < E)
+    for (int b = part; b < blocks; b += parts) {
+      p += partial[(int64_t)b * 2 * E + e];
+      if (!g.counts_in) c += __float_as_int(partial[((int64_t)b * 2 + 1) * E + e]);
     }
-    if (g.counts_in) c = g.counts_in[e];
-    else g.counts_out[e] = c;
-    p = n > 0 ? p / n : 0.0f;
-    g.mean_probs[e] = p;
-    if (n > 0) part = (float)c * ((float)E / ((float)g.top_k * n)) * p;
-  }
-  part = warp_sum(part);
-  if ((threadIdx.x & 31) == 0) s_loss[threadIdx.x >> 5] = part;
+  s_p[threadIdx.x] = p;
+  s_c[threadIdx.x] = c;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float l = 0.0f;
-    for (int i = 0; i < 32; ++i) l += s_loss[i];
-    *g.loss = g.coefficient * l;
-    if (!g.counts_in) g.counts_out[E] = n * g.top_k;
-  }
+  if (part == 0)
+    for (int i = 1; i < parts; ++i) {
+      p += s_p[i * width + e];
+      c += s_c[i * width + e];
+    }
+  finish(g, n, part == 0 ? e : E, p, c);
 }
 
-template <int V, int KIND>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArgs g) {
+template <int V, int LANES>
+__global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
+  constexpr int TOKENS = 32 / LANES;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
+  const int e0 = (lane & (LANES - 1)) * V;
   const int n = read_count(g.valid, g.T, g.err);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
   if (n == 0) return;
-  const float w = g.coefficient / n * (g.dloss ? *g.dloss : 1.0f);
+  const float w = g.coefficient / n * (g.dloss ? __ldg(g.dloss) : 1.0f);
   // f_e - 1 for f_e: the p of a token add up to 1, so the differences f_e - q are the
   // same, and near balance they keep their digits (c E - k Tv is exact in integers)
   float f[V];
+  const int64_t kt = (int64_t)g.top_k * n;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    const int64_t kt = (int64_t)g.top_k * n;
-    f[i] = e < E ? (float)((int64_t)g.counts_in[e] * E - kt) / (float)kt : 0.0f;
-  }
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < n; t += (int64_t)gridDim.x * kWarps) {
-    float a[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      a[i] = e < E ? load_score(g.scores, g.dtype, t * g.stride_t + e * g.stride_e) : 0.0f;
-    }
-    float rest[V];
-    const float inv = weights<V, KIND>(a, rest, E, lane);
+  for (int i = 0; i < V; ++i)
+    f[i] = e0 + i < E ? (float)((int64_t)__ldg(g.counts_in + e0 + i) * E - kt) / (float)kt : 0.0f;
+  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
+  for (int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS; t0 < n; t0 += stride) {
+    const int64_t t = t0 + lane / LANES;
+    const bool live = t < n;
+    float a[V], rest[V];
+    load_values<V>(g, live ? t : t0, e0, wide, a);
+    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0);
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) q += f[i] * a[i];
-    q = warp_sum(q) * inv;
+    q = group_sum<LANES>(q) * inv;
+    float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= E) continue;
-      float d = w * (f[i] - q) * inv;
-      if (KIND == MOE_BALANCE_SOFTMAX) d *= a[i];
-      if (KIND == MOE_BALANCE_SIGMOID) d *= a[i] * rest[i];
-      const int64_t at = t * E + e;
+      d[i] = w * (f[i] - q) * inv;
+      if (g.kind == MOE_BALANCE_SOFTMAX) d[i] *= a[i];
+      if (g.kind == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
+    }
+    if (!live) continue;
+    const int64_t at = t * E + e0;
+    if (wide_out) {
+      if (e0 >= E) continue;
       if (g.dtype == MOE_DTYPE_F32) {
-        float* o = static_cast<float*>(g.dscores) + at;
-        *o = g.accumulate ? *o + d : d;
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.dscores) + at);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          float4 v = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+          if (g.accumulate) {
+            const float4 b = o[i];
+            v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+          }
+          o[i] = v;
+        }
       } else {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.dscores) + at;
-        *o = __float2bfloat16_rn(g.accumulate ? __bfloat162float(*o) + d : d);
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.dscores) + at);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          float v[4] = {d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
+          if (g.accumulate) {
+            const uint2 b = o[i];
+            const float2 lo = bf16x2_bits_to_f32(b.x), hi = bf16x2_bits_to_f32(b.y);
+            v[0] += lo.x;
+            v[1] += lo.y;
+            v[2] += hi.x;
+            v[3] += hi.y;
+          }
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+          o[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (e0 + i >= E) continue;
+        if (g.dtype == MOE_DTYPE_F32) {
+          float* o = static_cast<float*>(g.dscores) + at + i;
+          *o = g.accumulate ? *o + d[i] : d[i];
+        } else {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.dscores) + at + i;
+          *o = __float2bfloat16_rn(g.accumulate ? __bfloat162float(*o) + d[i] : d[i]);
+        }
       }
     }
   }
 }
 
-template <int V>
-struct Values {
-  static constexpr int v = V;
+template <int V_, int LANES_>
+struct Layout {
+  static constexpr int V = V_, LANES = LANES_;
 };
 
-// f(Values<V>, Kind) for the least V in 1, 2, 4, .. 32 with 32 V >= E.
+// f(Layout) for E experts: 4 a lane while they fit a warp.
 template <typename F>
 void by_experts(int E, F f) {
-  if (E <= 32) f(Values<1>{});
-  else if (E <= 64) f(Values<2>{});
-  else if (E <= 128) f(Values<4>{});
-  else if (E <= 256) f(Values<8>{});
-  else if (E <= 512) f(Values<16>{});
-  else f(Values<32>{});
+  if (E <= 16) f(Layout<4, 4>{});
+  else if (E <= 32) f(Layout<4, 8>{});
+  else if (E <= 64) f(Layout<4, 16>{});
+  else if (E <= 128) f(Layout<4, 32>{});
+  else if (E <= 256) f(Layout<8, 32>{});
+  else if (E <= 512) f(Layout<16, 32>{});
+  else f(Layout<32, 32>{});
 }
 
-template <typename F>
-void by_kind(int kind, F f) {
-  if (kind == MOE_BALANCE_SCORES) f(Values<MOE_BALANCE_SCORES>{});
-  else if (kind == MOE_BALANCE_SOFTMAX) f(Values<MOE_BALANCE_SOFTMAX>{});
-  else f(Values<MOE_BALANCE_SIGMOID>{});
-}
+int values_of(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+int lanes_of(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32; }
+int warps_of(int E) { return E <= 256 ? kMaxWarps : 8; }  // of a forward block
 
-int blocks_for(int T) {
-  const int64_t b = ((int64_t)T + kWarps - 1) / kWarps;
-  return (int)(b < kMaxBlocks ? b : kMaxBlocks);
+// Forward blocks: one while it gets through the tokens in a few turns and has a thread for
+// each expert, which then finishes by itself; else up to one a SM.
+int forward_blocks(int T, int E) {
+  const int64_t turn = (int64_t)warps_of(E) * (32 / lanes_of(E));
+  if (T <= kOneBlockTurns * turn && E <= warps_of(E) * 32) return 1;
+  const int64_t need = (T + turn - 1) / turn;
+  return (int)(need < kNumSmsGB300 ? need : kNumSmsGB300);
+}
+bool finishes_alone(int blocks, int E) { return blocks <= 1 && E <= warps_of(E) * 32; }
+
+// Whether rows of `stride` elements hold each lane's V values as whole aligned pieces.
+bool whole_pieces(const void* base, int dtype, int64_t stride, int E) {
+  const int piece = dtype == MOE_DTYPE_F32 ? 16 : 8;  // 4 values
+  return E % values_of(E) == 0 && stride % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & (piece - 1)) == 0;
 }
 
 }  // namespace
 
-size_t balance_loss_workspace_bytes(int T, int E) { return 16 + (size_t)blocks_for(T) * E * 8; }
+size_t balance_loss_workspace_bytes(int T, int E) {
+  const int blocks = forward_blocks(T, E);
+  return finishes_alone(blocks, E) ? 0 : (size_t)blocks * 2 * E * sizeof(float);
+}
 
 cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
-  const int blocks = blocks_for(g.T);
-  float* psum = reinterpret_cast<float*>(static_cast<char*>(g.ws) + 16);
-  int* csum = reinterpret_cast<int*>(psum + (size_t)blocks * g.E);
-  const size_t smem = (size_t)kWarps * g.E * 8;
+  const int blocks = forward_blocks(g.T, g.E), warps = warps_of(g.E);
+  const size_t smem = (size_t)warps * g.E * 8;  // at most 64 KB
+  const bool wide = g.stride_e == 1 && whole_pieces(g.scores, g.dtype, g.stride_t, g.E);
+  float* partial = static_cast<float*>(g.ws);
   cudaError_t e = cudaSuccess;
-  if (blocks > 0)
-    by_experts(g.E, [&](auto v) {
-      by_kind(g.kind, [&](auto k) {
-        auto kern = g.counts_in ? balance_kernel<decltype(v)::v, decltype(k)::v, false>
-                                : balance_kernel<decltype(v)::v, decltype(k)::v, true>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) {
-          kern<<<blocks, kThreads, smem, s>>>(g, psum, csum);
-          e = cudaGetLastError();
-        }
-      });
-    });
+  if (blocks > 0) by_experts(g.E, [&](auto l) {
+    constexpr int V = decltype(l)::V, LANES = decltype(l)::LANES;
+    auto kern = g.counts_in ? balance_kernel<V, LANES, kGiven>
+                : g.dtype == MOE_DTYPE_BF16 ? balance_kernel<V, LANES, kBf16Keys>
+                                            : balance_kernel<V, LANES, kF32Keys>;
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return;
+    kern<<<blocks, warps * 32, smem, s>>>(g, wide, partial);
+    e = cudaGetLastError();
+  });
+  if (e != cudaSuccess || finishes_alone(blocks, g.E)) return e;
+  int width = 32;
+  while (width < g.E) width *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, balance_finish_kernel, g, (const float*)partial, blocks, width);
   if (e != cudaSuccess) return e;
-  balance_finish_kernel<<<1, 1024, 0, s>>>(g, blocks, psum, csum);
   return cudaGetLastError();
 }
 
 cudaError_t launch_balance_loss_backward(const BalanceArgs& g, cudaStream_t s) {
-  const int64_t b = ((int64_t)g.T + kWarps - 1) / kWarps, cap = (int64_t)device_sm_count() * 8;
-  by_experts(g.E, [&](auto v) {
-    by_kind(g.kind, [&](auto k) {
-      balance_grad_kernel<decltype(v)::v, decltype(k)::v><<<(int)(b < cap ? b : cap), kThreads, 0, s>>>(g);
-    });
+  const bool wide = g.stride_e == 1 && whole_pieces(g.scores, g.dtype, g.stride_t, g.E);
+  const bool wide_out = whole_pieces(g.dscores, g.dtype, g.E, g.E);
+  const int64_t turn = 8 * (32 / lanes_of(g.E)), b = (g.T + turn - 1) / turn, most = (int64_t)device_sm_count() * 8;
+  by_experts(g.E, [&](auto l) {
+    balance_grad_kernel<decltype(l)::V, decltype(l)::LANES>
+        <<<(int)(b < most ? b : most), 256, 0, s>>>(g, wide, wide_out);
   });
   return cudaGetLastError();
 }

@@ -141,8 +141,9 @@ int moe_balance_loss(const void* scores, int scores_dtype, int64_t stride_t, int
                      cudaStream_t stream) {
   int rc = check_balance(scores, scores_dtype, stride_t, stride_e, T, E, top_k, kind, coefficient);
   if (rc != MOE_OK) return rc;
-  if (!mean_probs || !loss || (!counts_in && !counts_out) || !ws) return MOE_ERR_INVALID;
-  if (ws_bytes < moe::balance_loss_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+  const size_t need = moe::balance_loss_workspace_bytes(T, E);
+  if (!mean_probs || !loss || (!counts_in && !counts_out) || (need > 0 && !ws)) return MOE_ERR_INVALID;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return MOE_ERR_INVALID;
   moe::BalanceArgs g{};
   g.scores = scores;
