@@ -1,16 +1,18 @@
 // The router's load-balance loss, per-expert counts and its gradient
 // (include/moe_train.h).
 //
-// LANES lanes of a warp own a token, V neighbouring experts each (4 x 4 lanes for 16
-// experts up to 32 x 32 for 1024), so a lane's experts stay the same from token to token
+// LANES lanes of a warp own a token, V neighbouring experts each (4 in 4 lanes for 16
+// experts up to 32 in 32 for 1024), so a lane's experts stay the same from token to token
 // and their sums of p and counts stay in registers.  Blocks leave partial sums; one block
 // adds them in order.  A batch that one block gets through is a single launch.
 //
-// The top_k largest of a token: top_k rounds of the largest value below the last one
-// found, over the lane, then over the lanes; the last is the threshold.  Of bf16 inputs
-// the key carries the expert below the value, so that keys differ and ties fall to the
-// lower expert; fp32 inputs that tie in value are noticed by their count and selected
-// again one by one.  The rounds bind the forward (65536 x 128 fp32, top 8): not memory.
+// The top_k largest of a token: each lane sorts its values, and top_k rounds take the
+// largest of the lanes' heads, whose lanes move on; the last one taken is the threshold.
+// Of bf16 inputs the key carries the expert below the value, so that keys differ and ties
+// fall to the lower expert; fp32 inputs that tie across lanes are noticed by the count
+// above the threshold and selected again one by one.  The rounds bind the forward, not
+// memory: looking for the next smaller value of each lane's four in every round, 65536
+// tokens of 128 experts in fp32, top 8, took 33.6 us, with the integer pipe 75% busy.
 #include "common.cuh"
 #include "launch.h"
 #include "train_launch.h"
@@ -108,19 +110,24 @@ __device__ __forceinline__ void sigmoid_both(float a, float* s, float* rest) {
   *rest = a >= 0.0f ? er : r;
 }
 
+// The order of scores as in routing (route_order_key), -0 folded onto +0 by an addition.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
 // The token's values become unnormalised weights in place (0 past E), rest[V] what each
-// sigmoid lacks to 1; returns 1 / the sum of the weights, or 0.
+// sigmoid lacks to 1; returns 1 / the sum of the weights, or 0.  top: their largest value
+// (softmax only).
 template <int V, int LANES>
-__device__ __forceinline__ float weights(float* a, float* rest, int kind, int E, int e0) {
+__device__ __forceinline__ float weights(float* a, float* rest, int kind, int E, int e0, float top) {
   if (kind == MOE_BALANCE_SOFTMAX) {
-    float m = -INFINITY;
+    if (top == -INFINITY) top = 0.0f;  // every expert masked: all weights are 0
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i < E) m = fmaxf(m, a[i]);
-    m = group_max<LANES>(m);
-    if (m == -INFINITY) m = 0.0f;  // every expert masked: all weights are 0
-#pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = e0 + i < E ? __expf(a[i] - m) : 0.0f;
+    for (int i = 0; i < V; ++i) a[i] = e0 + i < E ? __expf(a[i] - top) : 0.0f;
   } else if (kind == MOE_BALANCE_SIGMOID) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -135,49 +142,101 @@ __device__ __forceinline__ float weights(float* a, float* rest, int kind, int E,
   return s == 0.0f ? 0.0f : 1.0f / s;
 }
 
-// Which of the lane's values are among the token's k largest, one bit each.
+template <int V, int LANES>
+__device__ __forceinline__ float largest(const float* a, int E, int e0) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (e0 + i < E) m = fmaxf(m, a[i]);
+  return group_max<LANES>(m);
+}
+
+// Sorts keys descending (odd-even merge network; V a power of two).
+template <int V>
+__device__ __forceinline__ void sort_descending(uint32_t* k) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int d = p; d > 0; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+          if (j + i + d < V && (j + i) / (2 * p) == (j + i + d) / (2 * p)) {
+            const uint32_t a = k[j + i], b = k[j + i + d];
+            k[j + i] = max(a, b);
+            k[j + i + d] = min(a, b);
+          }
+}
+
+// Adds 1 to the counts cs[V] of the lane's values that are among the token's k largest, where
+// the token is live; *top: the largest value.
 template <int V, int LANES, int SELECT>
-__device__ __forceinline__ uint32_t choose(const float* a, int k, int E, int e0) {
+__device__ __forceinline__ void choose(const float* a, int k, int E, int e0, bool live, int* cs, float* top) {
   uint32_t key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    key[i] = route_order_key(a[i]);
+    key[i] = order_key(a[i]);
     // a bf16 value's order is in the upper half of its key; the lower expert is the larger key
     if (SELECT == kBf16Keys) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - (e0 + i));
     if (e0 + i >= E) key[i] = 0u;
   }
-  uint32_t limit = kAll;
-  for (int r = 0; r < k; ++r) {
-    uint32_t m = 0u;
+  uint32_t limit = 0u;
+  if constexpr (V <= 16) {
+    uint32_t head[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, key[i] < limit ? key[i] : 0u);
-    limit = group_max<LANES>(m);
-  }
-  uint32_t bits = 0u;
+    for (int i = 0; i < V; ++i) head[i] = key[i];
+    sort_descending<V>(head);
+    for (int r = 0; r < k; ++r) {
+      limit = group_max<LANES>(head[0]);
+      if (r == 0) *top = key_value(limit);
+      if (head[0] == limit) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) bits |= (key[i] >= limit && e0 + i < E ? 1u : 0u) << i;
-  if (SELECT == kF32Keys && __any_sync(kAll, group_count<LANES>(__popc(bits)) != k)) {
-    // equal values among them: one at a time, the lowest expert of the largest value
-    bits = 0u;
+        for (int i = 0; i + 1 < V; ++i) head[i] = head[i + 1];
+        head[V - 1] = 0u;
+      }
+    }
+  } else {
+    limit = kAll;
     for (int r = 0; r < k; ++r) {
       uint32_t m = 0u;
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = max(m, key[i]);
-      m = group_max<LANES>(m);
-      uint32_t at = kAll;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == m && e0 + i < E) at = (uint32_t)(e0 + i);
-      at = group_min<LANES>(at);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at == (uint32_t)(e0 + i)) {
-          key[i] = 0u;
-          bits |= 1u << i;
-        }
+      for (int i = 0; i < V; ++i) m = max(m, key[i] < limit ? key[i] : 0u);
+      limit = group_max<LANES>(m);
+      if (r == 0) *top = key_value(limit);
     }
   }
-  return bits;
+  limit = max(limit, 1u);  // (0: past E)
+  if (SELECT == kBf16Keys) *top = __uint_as_float(__float_as_uint(*top) & 0xffff0000u);
+  if (SELECT == kF32Keys) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += key[i] >= limit ? 1 : 0;
+    if (__any_sync(kAll, group_count<LANES>(n) != k)) {
+      // equal values among them: one at a time, the lowest expert of the largest value
+      for (int r = 0; r < k; ++r) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = max(m, key[i]);
+        m = group_max<LANES>(m);
+        uint32_t at = kAll;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == m && e0 + i < E) at = (uint32_t)(e0 + i);
+        at = group_min<LANES>(at);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at == (uint32_t)(e0 + i)) {
+            key[i] = 0u;
+            cs[i] += live ? 1 : 0;
+          }
+      }
+      return;
+    }
+  }
+  if (!live) limit = kAll;
+#pragma unroll
+  for (int i = 0; i < V; ++i) cs[i] += key[i] >= limit ? 1 : 0;
 }
 
 // The loss, mean_probs and counts from each expert's sum of p and count: threads e < E hold
@@ -205,7 +264,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& g, int n, int e, float
 
 // partial: [blocks][2][E], p sums and (as int) counts; unused by a single block.
 template <int V, int LANES, int SELECT>
-__global__ void __launch_bounds__(V <= 8 ? 1024 : 256)
+__global__ void __launch_bounds__(V <= 8 ? 1024 : V <= 16 ? 512 : 256)
     balance_kernel(const BalanceArgs g, bool wide, float* partial) {
   extern __shared__ float sh[];  // [warps][E] p sums, then [warps][E] counts
   pdl_launch_dependents();
@@ -226,13 +285,10 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : 256)
     const bool live = t < n;
     float a[V], rest[V];
     load_values<V>(g, live ? t : t0, e0, wide, a);
-    if (SELECT != kGiven) {
-      uint32_t bits = choose<V, LANES, SELECT>(a, g.top_k, E, e0);
-      if (!live) bits = 0u;
-#pragma unroll
-      for (int i = 0; i < V; ++i) cs[i] += (bits >> i) & 1u;
-    }
-    float inv = weights<V, LANES>(a, rest, g.kind, E, e0);
+    float top = 0.0f;
+    if (SELECT != kGiven) choose<V, LANES, SELECT>(a, g.top_k, E, e0, live, cs, &top);
+    else if (g.kind == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a, E, e0);
+    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (live) ps[i] += a[i] * inv;  // (a row past the count may hold anything)
@@ -281,10 +337,22 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
   const int e = threadIdx.x & (width - 1), part = threadIdx.x / width, parts = 1024 / width;
   float p = 0.0f;
   int c = 0;
+  constexpr int kAtOnce = 5;  // loads under way together
   if (e < E)
-    for (int b = part; b < blocks; b += parts) {
-      p += partial[(int64_t)b * 2 * E + e];
-      if (!g.counts_in) c += __float_as_int(partial[((int64_t)b * 2 + 1) * E + e]);
+    for (int b = part; b < blocks; b += kAtOnce * parts) {
+      float vp[kAtOnce], vc[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t at = (int64_t)(b + i * parts) * 2 * E + e;
+        const bool in = b + i * parts < blocks;
+        vp[i] = in ? partial[at] : 0.0f;
+        vc[i] = in && !g.counts_in ? partial[at + E] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        p += vp[i];
+        c += __float_as_int(vc[i]);
+      }
     }
   s_p[threadIdx.x] = p;
   s_c[threadIdx.x] = c;
@@ -318,7 +386,8 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, 
     const bool live = t < n;
     float a[V], rest[V];
     load_values<V>(g, live ? t : t0, e0, wide, a);
-    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0);
+    const float top = g.kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a, E, e0) : 0.0f;
+    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) q += f[i] * a[i];
@@ -383,7 +452,9 @@ struct Layout {
   static constexpr int V = V_, LANES = LANES_;
 };
 
-// f(Layout) for E experts: 4 a lane while they fit a warp.
+// f(Layout) for E experts: 4 a lane while they fit a warp, which keeps small batches short
+// (500 tokens of 128 experts: 6.1 us; 7.7 with 8 in 16 lanes, which takes 27.1 us for 65536
+// against 29.6), then 8 and more in a whole one.
 template <typename F>
 void by_experts(int E, F f) {
   if (E <= 16) f(Layout<4, 4>{});
@@ -397,7 +468,7 @@ void by_experts(int E, F f) {
 
 int values_of(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 int lanes_of(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32; }
-int warps_of(int E) { return E <= 256 ? kMaxWarps : 8; }  // of a forward block
+int warps_of(int E) { return E <= 256 ? kMaxWarps : E <= 512 ? 16 : 8; }  // of a forward block
 
 // Forward blocks: one while it gets through the tokens in a few turns and has a thread for
 // each expert, which then finishes by itself; else up to one a SM.
