@@ -179,8 +179,10 @@ int moe_silu_mul_backward(const void* codes, const uint8_t* exponents, const voi
  * read into any result, whatever they hold.
  * N and K multiples of 16, E <= 1024 (MOE_ERR_UNSUPPORTED).
  * ws: device workspace of moe_grouped_weight_grad_workspace_size bytes (x_dtype
- * MOE_DTYPE_BF16 or MOE_DTYPE_E4M3; 0 bytes for bf16 in this build), 256-byte
- * aligned; its contents on entry do not matter.
+ * MOE_DTYPE_BF16 or MOE_DTYPE_E4M3; it may be 0: ws may then be NULL), 256-byte
+ * aligned; its contents on entry do not matter.  It holds the unpacked rows of a
+ * checkpoint, and fp32 parts of dw where few tiles make it worth cutting long
+ * experts' rows; the parts are added in order.
  */
 int moe_grouped_weight_grad_workspace_size(int E, int a_max, int N, int K, int x_dtype, size_t* bytes);
 int moe_grouped_weight_grad(const void* dy, const void* x, const uint8_t* x_exponents, const int32_t* counts, int E,

@@ -25,6 +25,10 @@
 //              reductions, for accumulate) that clip at the edges of dW[e].
 // An expert without rows has its tiles written as zeros by the epilogue alone.
 //
+// Where an expert's dW is too few tiles for the device, experts with many rows are cut into
+// parts of equal length; a part's tiles go to the workspace in fp32, and a second kernel
+// adds an expert's parts in order.  One expert of 32768 rows, N = K = 256: 147 us uncut.
+//
 // A tile costs its store whatever its rows, and its products by its rows: the tiles of
 // experts with many rows are bound by the tensor cores, the others by memory.  So that both
 // are busy at any time, the experts are ordered by their rows, and each pair works through
@@ -52,10 +56,13 @@ constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 32 KB
 constexpr int kStages = 6, kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kThreads = 224;
-constexpr int kMaxSorted = 256;           // experts up to which the rank sort is run
+constexpr int kMaxSorted = 384;           // experts (or parts) up to which the rank sort is run
+constexpr int kPairsGB300 = kNumSmsGB300 / 2;
+constexpr int kMinPart = 256;             // rows
+constexpr int kWhole = 0xffff;            // the slot of an expert that is not cut
 constexpr int kEpiBlockBytes = 32 * 128;  // staging block of an epilogue warp: 32 rows x 128 bytes
 // Staging blocks of an epilogue warp: two, which short experts' tiles need to write at 6.3
-// TB/s (6.1 with one); one where the expert tables want the room.
+// TB/s (6.1 with one); one where the tables of experts or parts want the room.
 constexpr int kTwoBlocksMaxE = 256;
 // Tiles with more rows than this use one block whatever there is: their stores then spread
 // over the products of the next tile.  In bursts they delay its loads: 16 experts of 512
@@ -68,9 +75,11 @@ struct Smem {
   // after 4 * blocks staging blocks:
   static constexpr int bars = 0;  // full[S], ready[S], empty[S], tfull[2], tempty[2], drain
   static constexpr int misc = bars + (3 * kStages + 2 * kAccBufs + 1) * 8;
-  static constexpr int rows = misc + 16;  // row_off[E + 1], then order[E] in 16 bits
+  static constexpr int units = misc + 16;  // off[U + 1], then order, owner and slot [U] in 16 bits
   static constexpr int tail(int blocks) { return epi + 4 * blocks * kEpiBlockBytes; }
-  static constexpr int bytes_for(int E, int blocks) { return tail(blocks) + rows + (E + 1) * 4 + E * 2; }
+  static constexpr int bytes_for(int units_most, bool split, int blocks) {
+    return tail(blocks) + units + (units_most + 1) * 4 + units_most * (split ? 6 : 2);
+  }
 };
 
 // n / d for 0 <= n < 2^31 by one multiplication and a correction: a tile's place costs its
@@ -88,7 +97,8 @@ constexpr int kGroup = 8;  // tiles along N of a group in the tile order
 
 struct Shape {
   int E, a_max, N, K;
-  int total;         // tiles
+  int units;         // most units: experts, or their parts
+  int part;          // rows of a part; 0: experts are not cut
   int mt, kt;        // tiles of an expert along N and K
   Divisor per;       // tiles of an expert
   Divisor band;      // tiles of a group of kGroup along N
@@ -190,16 +200,26 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-struct Tile {
-  int expert, n0, k0, row0, rows;
+// The units of work: an expert's rows, or a part of them.  Unit u holds the rows from
+// off[u] to off[u + 1] of expert owner[u]; slot[u]: where its part goes (kWhole: to dW).
+struct Units {
+  int* off;
+  uint16_t* order;  // by descending rows
+  uint16_t* owner;
+  uint16_t* slot;
+  int n, total;     // units; tiles of them all
 };
 
-// Tile `tile` in the order of the experts' ranks.  An expert's tiles come in groups of kGroup
+struct Tile {
+  int unit, n0, k0, row0, rows;
+};
+
+// Tile `tile` in the order of the units' ranks.  A unit's tiles come in groups of kGroup
 // along N, N innermost, so that the pairs running together read few columns of either operand.
-__device__ __forceinline__ Tile locate(const Shape& p, int tile, const int* row_off, const uint16_t* order) {
+__device__ __forceinline__ Tile locate(const Shape& p, int tile, const Units& units) {
   Tile t;
   const int rank = quotient(tile, p.per);
-  t.expert = order[rank];
+  t.unit = units.order[rank];
   const int local = tile - rank * (int)p.per.d;
   const int group = quotient(local, p.band), in = local - group * (int)p.band.d;
   const bool whole = (group + 1) * kGroup <= p.mt;
@@ -207,8 +227,8 @@ __device__ __forceinline__ Tile locate(const Shape& p, int tile, const int* row_
   const int n = in - k * (whole ? kGroup : (int)p.last.d);
   t.n0 = (group * kGroup + n) * kTile;
   t.k0 = k * kTile;
-  t.row0 = row_off[t.expert];
-  t.rows = row_off[t.expert + 1] - t.row0;
+  t.row0 = units.off[t.unit];
+  t.rows = units.off[t.unit + 1] - t.row0;
   return t;
 }
 
@@ -227,8 +247,9 @@ struct Schedule {
   bool short_turn;
   Tile t;                        // the front's tile
 
-  __device__ Schedule(const Shape& p, int pair_, int pairs_)
-      : pair(pair_), pairs(pairs_), front(0), back((p.total - 1 - pair_) / pairs_), done(0), short_turn(true) {}
+  __device__ Schedule(const Units& units, int pair_, int pairs_)
+      : pair(pair_), pairs(pairs_), front(0), back(units.total > pair_ ? (units.total - 1 - pair_) / pairs_ : -1),
+        done(0), short_turn(true) {}
 };
 
 // Blocks first .. first + count - 1 of a tile of `blocks` blocks, in accumulator acc.
@@ -237,12 +258,11 @@ struct Chunk {
   int acc, first, count, blocks;
 };
 
-__device__ __forceinline__ bool next_chunk(Schedule& w, const Shape& p, const int* row_off, const uint16_t* order,
-                                           Chunk* c) {
+__device__ __forceinline__ bool next_chunk(Schedule& w, const Shape& p, const Units& units, Chunk* c) {
   const bool take_back = w.short_turn && w.front <= w.back;
   w.short_turn = !take_back;
   if (take_back) {
-    c->t = locate(p, w.pair + w.back * w.pairs, row_off, order);
+    c->t = locate(p, w.pair + w.back * w.pairs, units);
     --w.back;
     c->acc = 1;
     c->first = 0;
@@ -251,7 +271,7 @@ __device__ __forceinline__ bool next_chunk(Schedule& w, const Shape& p, const in
   }
   if (w.done == 0) {
     if (w.front > w.back) return false;
-    w.t = locate(p, w.pair + w.front * w.pairs, row_off, order);
+    w.t = locate(p, w.pair + w.front * w.pairs, units);
     ++w.front;
   }
   c->t = w.t;
@@ -284,11 +304,11 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
 }
 
 // One epilogue warp's rows of a tile: row (its first) + lane, 64 columns at a time, through
-// the next of its staging blocks (*blk) 128 bytes of a row each.  zero: the tile of an
-// expert without rows.
+// the next of its staging blocks (*blk) 128 bytes of a row each, to matrix `at` of map.
+// zero: the tile of an expert without rows; add: to what is there (fp32).
 template <bool F32>
 __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int row, int lane, uint32_t tbase, bool zero,
-                                           uint8_t* stage, int* blk, const CUtensorMap* map) {
+                                           uint8_t* stage, int* blk, const CUtensorMap* map, int at, bool add) {
   if (row >= p.N) return;
   const int cols = min(kTile, p.K - t.k0);
 #pragma unroll 1
@@ -323,8 +343,8 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        if (F32 && p.accumulate) tma_add_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, t.expert);
-        else tma_store_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, t.expert);
+        if (F32 && add) tma_add_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, at);
+        else tma_store_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, at);
         bulk_commit_group();
       }
       if (++*blk == p.blocks) *blk = 0;
@@ -332,12 +352,13 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
   }
 }
 
-template <bool F32>
+// first_part [E][2] (SPLIT): an expert's first slot and number of parts, for the join.
+template <bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
                        const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_zero4,
-                       const __grid_constant__ CUtensorMap map_zero1, const int32_t* __restrict__ counts, const Shape p,
-                       unsigned int* err) {
+                       const __grid_constant__ CUtensorMap map_zero1, const __grid_constant__ CUtensorMap map_part,
+                       const int32_t* __restrict__ counts, const Shape p, int* first_part, unsigned int* err) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -356,8 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_drain = smem_u32(&bars[3 * kStages + 2 * kAccBufs]);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tail + Smem::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tail + Smem::misc + 4);
-  int* row_off = reinterpret_cast<int*>(tail + Smem::rows);
-  uint16_t* order = reinterpret_cast<uint16_t*>(row_off + p.E + 1);
+  int* s_units = reinterpret_cast<int*>(tail + Smem::misc + 8);
+  Units units;
+  units.off = reinterpret_cast<int*>(tail + Smem::units);
+  units.order = reinterpret_cast<uint16_t*>(units.off + p.units + 1);
+  units.owner = units.order + p.units;
+  units.slot = units.owner + p.units;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -384,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (warp == 2) {
-    // row offsets: a warp-wide scan of the counts, cut at a_max (64-bit: bad counts may add up past 31 bits)
+    // the units' row offsets: a warp-wide scan of the counts, cut at a_max (64-bit: bad counts may add up
+    // past 31 bits)
     int64_t run = 0;
+    int first = 0, slot = 0;  // the next unit and slot
     bool bad = false;
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
@@ -400,28 +427,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (e < p.E) row_off[e] = (int)min(run + incl - c, (int64_t)p.a_max);
+      const int row0 = (int)min(run + incl - c, (int64_t)p.a_max), row1 = (int)min(run + incl, (int64_t)p.a_max);
+      if constexpr (SPLIT) {
+        const int parts = max(1, (row1 - row0 + p.part - 1) / p.part);
+        const int slots = parts > 1 ? parts : 0;
+        int nu = e < p.E ? parts : 0, ns = e < p.E ? slots : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, nu, o), v = __shfl_up_sync(0xffffffffu, ns, o);
+          if (lane >= o) {
+            nu += u;
+            ns += v;
+          }
+        }
+        if (e < p.E) {
+          const int u0 = first + nu - parts, s0 = slot + ns - slots;
+          for (int k = 0; k < parts; ++k) {
+            units.off[u0 + k] = row0 + k * p.part;
+            units.owner[u0 + k] = (uint16_t)e;
+            units.slot[u0 + k] = (uint16_t)(slots ? s0 + k : kWhole);
+          }
+          if (blockIdx.x == 0) {
+            first_part[2 * e] = s0;
+            first_part[2 * e + 1] = slots;
+          }
+        }
+        first += __shfl_sync(0xffffffffu, nu, 31);
+        slot += __shfl_sync(0xffffffffu, ns, 31);
+      } else {
+        if (e < p.E) units.off[e] = row0;
+      }
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      row_off[p.E] = (int)min(run, (int64_t)p.a_max);
+      const int n = SPLIT ? first : p.E;
+      units.off[n] = (int)min(run, (int64_t)p.a_max);
+      *s_units = n;
       if (run > p.a_max) bad = true;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) flag_error(err, MOE_DEVERR_BAD_COUNT);
   }
   __syncthreads();
-  // the experts by descending rows (equal ones by number): each one's rank by counting
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    int at = e;
-    if (p.E <= kMaxSorted) {
-      const int mine = row_off[e + 1] - row_off[e];
+  units.n = *s_units;
+  units.total = units.n * (int)p.per.d;
+  // the units by descending rows (equal ones by number): each one's rank by counting
+  for (int u = threadIdx.x; u < units.n; u += kThreads) {
+    int at = u;
+    if (units.n <= kMaxSorted) {
+      const int mine = units.off[u + 1] - units.off[u];
       at = 0;
-      for (int i = 0; i < p.E; ++i) {
-        const int other = row_off[i + 1] - row_off[i];
-        at += other > mine || (other == mine && i < e);
+      for (int i = 0; i < units.n; ++i) {
+        const int other = units.off[i + 1] - units.off[i];
+        at += other > mine || (other == mine && i < u);
       }
     }
-    order[at] = (uint16_t)e;
+    units.order[at] = (uint16_t)u;
   }
   tc_fence_before();
   __syncthreads();
@@ -438,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      Schedule work(p, pair, pairs);
+      Schedule work(units, pair, pairs);
       Chunk c;
-      while (ok && next_chunk(work, p, row_off, order, &c)) {
+      while (ok && next_chunk(work, p, units, &c)) {
         const Tile& t = c.t;
         const int n0 = t.n0 + (int)rank * kHalf, k0 = t.k0 + (int)rank * kHalf;
         const int na = boxes(p.N - n0), nb = boxes(p.K - k0);
@@ -500,9 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t parity = 0;   // of each stage's next use of its full barrier
       int s = 0;             // the stage of this chunk's first block
       bool ok = true;
-      Schedule work(p, pair, pairs);
+      Schedule work(units, pair, pairs);
       Chunk c;
-      while (ok && next_chunk(work, p, row_off, order, &c)) {
+      while (ok && next_chunk(work, p, units, &c)) {
         const Tile& t = c.t;
         if (c.count == 0) continue;
         const int mine = (s + c.count - 1) % kStages, left = t.rows - (c.blocks - 1) * kBR;
@@ -539,9 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       uint32_t acc_parity = 0;  // of each accumulator's next use
       bool ok = true, issued_any = false;
-      Schedule work(p, pair, pairs);
+      Schedule work(units, pair, pairs);
       Chunk c;
-      while (ok && next_chunk(work, p, row_off, order, &c)) {
+      while (ok && next_chunk(work, p, units, &c)) {
         const Tile& t = c.t;
         if (c.count == 0) continue;
         if (c.first == 0) {
@@ -591,13 +651,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
     uint32_t acc_parity = 0;
     int blk = 0;
-    Schedule work(p, pair, pairs);
+    Schedule work(units, pair, pairs);
     Chunk c;
-    while (next_chunk(work, p, row_off, order, &c)) {
+    while (next_chunk(work, p, units, &c)) {
       if (c.first + c.count < c.blocks) continue;
       const int row = c.t.n0 + (int)rank * kHalf + 32 * sub;
+      const int slot = SPLIT ? units.slot[c.t.unit] : kWhole;
+      const int expert = SPLIT ? units.owner[c.t.unit] : c.t.unit;
       if (c.t.rows == 0) {
-        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw);
+        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw, expert, false);
         continue;
       }
       if (!warp_wait(bar_tfull(c.acc), (acc_parity >> c.acc) & 1u, s_abort)) {
@@ -607,8 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       acc_parity ^= 1u << c.acc;
       tc_fence_after();
-      store_tile<F32>(p, c.t, row, lane, tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(c.acc * kTile), false,
-                      stage, &blk, &map_dw);
+      const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(c.acc * kTile);
+      if (SPLIT && slot != kWhole) store_tile<true>(p, c.t, row, lane, tbase, false, stage, &blk, &map_part, slot, false);
+      else store_tile<F32>(p, c.t, row, lane, tbase, false, stage, &blk, &map_dw, expert, p.accumulate);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(c.acc * 8));
@@ -625,7 +688,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
 }
 
+// dW of the experts that were cut: their parts in order.  n4: float4s of an expert's dW.
+template <bool F32>
+__global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ parts,
+                                                         const int* __restrict__ first_part, int64_t n4, bool accumulate,
+                                                         void* dw) {
+  pdl_wait();
+  const int slot = first_part[2 * blockIdx.y], count = first_part[2 * blockIdx.y + 1];
+  if (count == 0) return;
+  const float4* p = parts + slot * n4;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int kAtOnce = 8;  // loads under way together
+    for (int k = 0; k < count; k += kAtOnce) {
+      float4 a[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        a[j] = k + j < count ? __ldcs(p + (k + j) * n4 + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) v = make_float4(v.x + a[j].x, v.y + a[j].y, v.z + a[j].z, v.w + a[j].w);
+    }
+    const int64_t at = blockIdx.y * n4 + i;
+    if (F32) {
+      float4* o = static_cast<float4*>(dw) + at;
+      if (accumulate) {
+        const float4 b = *o;
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+      }
+      *o = v;
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      static_cast<uint2*>(dw)[at] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
+}
+
 // ------------------------------------------------------------------- host
+
+int64_t tiles_of(int n) { return (n + kTile - 1) / kTile; }
+
+// Rows of a part, 0: experts are not cut.  A part for each pair when one expert has all the
+// rows; dW of a tile for each pair needs none.
+int part_rows(int a_max, int N, int K) {
+  const int64_t tiles = tiles_of(N) * tiles_of(K);
+  if (tiles >= kPairsGB300) return 0;
+  int64_t rows = (a_max * tiles + kPairsGB300 - 1) / kPairsGB300;
+  rows = (rows + kBR - 1) / kBR * kBR;
+  if (rows < kMinPart) rows = kMinPart;
+  return rows >= a_max ? 0 : (int)rows;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t unpacked_bytes(int a_max, int K) { return up256((size_t)a_max * K * 2); }
+// Slots: an expert that is cut has more than one part, of which all but the last are whole.
+int64_t most_slots(int a_max, int part) { return 2 * (int64_t)a_max / part; }
 
 // dW [E, N, K] as a 3-D map, boxes of 32 rows x 128 bytes in one expert: stores clip at its edges.
 bool make_dw_map(CUtensorMap* map, void* base, int E, int N, int K, bool f32) {
@@ -657,43 +774,63 @@ bool make_zero_map(CUtensorMap* map, const void* dy, int a_max, int N, int rows)
 
 }  // namespace
 
-size_t weight_grad_workspace_bytes(int, int a_max, int, int K, bool packed) {
-  return packed ? ((size_t)a_max * K * 2 + 255) / 256 * 256 : 0;
+size_t weight_grad_workspace_bytes(int E, int a_max, int N, int K, bool packed) {
+  size_t n = packed ? unpacked_bytes(a_max, K) : 0;
+  if (const int part = part_rows(a_max, N, K))
+    n += up256((size_t)E * 8) + (size_t)most_slots(a_max, part) * N * K * sizeof(float);
+  return n;
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   const void* x = g.x;
+  char* ws = static_cast<char*>(g.ws);
   if (g.exponents && g.a_max > 0) {
     CheckpointArgs c{};
     c.a = g.a_max;
     c.W = g.K;
     c.codes = const_cast<void*>(g.x);
     c.exponents = const_cast<uint8_t*>(g.exponents);
-    c.out = g.ws;
+    c.out = ws;
     c.sum_counts = g.counts;
     c.E = g.E;
     c.err = g.err;
     cudaError_t e = launch_checkpoint_unpack(c, s);
     if (e != cudaSuccess) return e;
-    x = g.ws;
+    x = ws;
+    ws += unpacked_bytes(g.a_max, g.K);
   }
-  const int mt = (g.N + kTile - 1) / kTile, kt = (g.K + kTile - 1) / kTile;
-  const int64_t tiles = (int64_t)g.E * mt * kt;
-  if (tiles > INT32_MAX / 2) return cudaErrorNotSupported;
-  Shape p{g.E,        g.a_max,      g.N,
-          g.K,        (int)tiles,   mt,
-          kt,         divisor(mt * kt), divisor(kGroup * kt),
-          divisor(mt % kGroup ? mt % kGroup : kGroup), g.accumulate, g.E <= kTwoBlocksMaxE ? 2 : 1};
+  const int64_t mt = tiles_of(g.N), kt = tiles_of(g.K);
   const bool f32 = g.dw_dtype == MOE_DTYPE_F32;
-  CUtensorMap dw, dy, mx, z4, z1;
+  Shape p{};
+  p.E = g.E;
+  p.a_max = g.a_max;
+  p.N = g.N;
+  p.K = g.K;
+  p.part = part_rows(g.a_max, g.N, g.K);
+  p.units = g.E + (p.part ? g.a_max / p.part : 0);
+  const int64_t tiles = p.units * mt * kt;  // at most
+  if (tiles > INT32_MAX / 2) return cudaErrorNotSupported;
+  p.mt = (int)mt;
+  p.kt = (int)kt;
+  p.per = divisor((int)(mt * kt));
+  p.band = divisor((int)(kGroup * kt));
+  p.last = divisor(mt % kGroup ? (int)(mt % kGroup) : kGroup);
+  p.accumulate = g.accumulate;
+  p.blocks = !p.part && g.E <= kTwoBlocksMaxE ? 2 : 1;
+  int* first_part = reinterpret_cast<int*>(ws);
+  float* parts = reinterpret_cast<float*>(ws + up256((size_t)g.E * 8));
+  CUtensorMap dw, dy, mx, z4, z1, mp;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
-  dy = mx = z4 = z1 = dw;  // without rows nothing is loaded
+  mp = dy = mx = z4 = z1 = dw;  // without rows nothing is loaded, without parts none are stored
+  if (p.part && !make_dw_map(&mp, parts, (int)most_slots(g.a_max, p.part), g.N, g.K, true))
+    return cudaErrorInvalidValue;
   if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
                       !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR) ||
                       !make_zero_map(&z4, g.dy, g.a_max, g.N, 4) || !make_zero_map(&z1, g.dy, g.a_max, g.N, 1)))
     return cudaErrorInvalidValue;
-  const int smem = Smem::bytes_for(g.E, p.blocks) + 1024;
-  auto kern = f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
+  const int smem = Smem::bytes_for(p.units, p.part != 0, p.blocks) + 1024;
+  auto kern = p.part ? (f32 ? weight_grad_kernel<true, true> : weight_grad_kernel<false, true>)
+                     : (f32 ? weight_grad_kernel<true, false> : weight_grad_kernel<false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -714,7 +851,20 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   if (pairs < 1) return cudaErrorNotSupported;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, g.counts, p, g.err);
+  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, mp, g.counts, p, first_part, g.err);
+  if (e != cudaSuccess) return e;
+  if (!p.part) return cudaGetLastError();
+  const int64_t n4 = (int64_t)g.N * g.K / 4, want = (n4 + 255) / 256;
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3((unsigned)(want < 304 ? want : 304), (unsigned)g.E);
+  join.blockDim = dim3(256);
+  join.stream = s;
+  cudaLaunchAttribute pdl[1] = {pdl_attribute()};
+  join.attrs = pdl;
+  join.numAttrs = 1;
+  auto jk = f32 ? join_parts_kernel<true> : join_parts_kernel<false>;
+  e = cudaLaunchKernelEx(&join, jk, reinterpret_cast<const float4*>(parts), (const int*)first_part, n4, g.accumulate,
+                         g.dw);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
