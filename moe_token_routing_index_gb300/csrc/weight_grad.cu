@@ -27,7 +27,7 @@
 //
 // Where an expert's dW is too few tiles for the device, experts with many rows are cut into
 // parts of equal length; a part's tiles go to the workspace in fp32, and a second kernel
-// adds an expert's parts in order.  One expert of 32768 rows, N = K = 256: 147 us uncut.
+// adds an expert's parts in order (one expert of 32768 rows, N = K = 256: 181 us uncut).
 //
 // A tile costs its store whatever its rows, and its products by its rows: the tiles of
 // experts with many rows are bound by the tensor cores, the others by memory.  So that both
@@ -58,7 +58,7 @@ constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kThreads = 224;
 constexpr int kMaxSorted = 384;           // experts (or parts) up to which the rank sort is run
 constexpr int kPairsGB300 = kNumSmsGB300 / 2;
-constexpr int kMinPart = 256;             // rows
+constexpr int kMinPart = 1024;            // rows
 constexpr int kWhole = 0xffff;            // the slot of an expert that is not cut
 constexpr int kEpiBlockBytes = 32 * 128;  // staging block of an epilogue warp: 32 rows x 128 bytes
 // Staging blocks of an epilogue warp: two, which short experts' tiles need to write at 6.3
@@ -352,13 +352,14 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
   }
 }
 
-// first_part [E][2] (SPLIT): an expert's first slot and number of parts, for the join.
+// cut (SPLIT): for the join, the number of experts that are cut, then of each its number,
+// first slot and number of parts.
 template <bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
                        const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_zero4,
                        const __grid_constant__ CUtensorMap map_zero1, const __grid_constant__ CUtensorMap map_part,
-                       const int32_t* __restrict__ counts, const Shape p, int* first_part, unsigned int* err) {
+                       const int32_t* __restrict__ counts, const Shape p, int* cut, unsigned int* err) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -384,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   units.owner = units.order + p.units;
   units.slot = units.owner + p.units;
 
+  if (SPLIT) pdl_launch_dependents();  // the join waits for this grid's end
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar_full(s), 1);
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the units' row offsets: a warp-wide scan of the counts, cut at a_max (64-bit: bad counts may add up
     // past 31 bits)
     int64_t run = 0;
-    int first = 0, slot = 0;  // the next unit and slot
+    int first = 0, slot = 0, ncut = 0;  // the next unit and slot; experts cut
     bool bad = false;
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
@@ -447,11 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             units.owner[u0 + k] = (uint16_t)e;
             units.slot[u0 + k] = (uint16_t)(slots ? s0 + k : kWhole);
           }
-          if (blockIdx.x == 0) {
-            first_part[2 * e] = s0;
-            first_part[2 * e + 1] = slots;
-          }
         }
+        const uint32_t more = __ballot_sync(0xffffffffu, e < p.E && slots > 0);
+        if (blockIdx.x == 0 && e < p.E && slots > 0) {
+          int* entry = cut + 1 + 3 * (ncut + __popc(more & ((1u << lane) - 1u)));
+          entry[0] = e;
+          entry[1] = slot + ns - slots;
+          entry[2] = slots;
+        }
+        ncut += __popc(more);
         first += __shfl_sync(0xffffffffu, nu, 31);
         slot += __shfl_sync(0xffffffffu, ns, 31);
       } else {
@@ -461,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       const int n = SPLIT ? first : p.E;
+      if (SPLIT && blockIdx.x == 0) cut[0] = ncut;
       units.off[n] = (int)min(run, (int64_t)p.a_max);
       *s_units = n;
       if (run > p.a_max) bad = true;
@@ -688,39 +695,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
 }
 
-// dW of the experts that were cut: their parts in order.  n4: float4s of an expert's dW.
+// dW of the experts that were cut.  32 float4 columns a block, 8 threads each, which add every
+// eighth part in order and are then added in order.  n4: float4s of an expert's dW.
 template <bool F32>
 __global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ parts,
-                                                         const int* __restrict__ first_part, int64_t n4, bool accumulate,
+                                                         const int* __restrict__ cut, int64_t n4, bool accumulate,
                                                          void* dw) {
+  __shared__ float4 s[8][32];
   pdl_wait();
-  const int slot = first_part[2 * blockIdx.y], count = first_part[2 * blockIdx.y + 1];
-  if (count == 0) return;
-  const float4* p = parts + slot * n4;
-  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+  const int c = threadIdx.x & 31, l = threadIdx.x >> 5;
+  const int64_t per = n4 / 32, work = cut[0] * per;  // (n4 is a multiple of 64)
+  for (int64_t u = blockIdx.x; u < work; u += gridDim.x) {
+    const int* entry = cut + 1 + 3 * (u / per);
+    const int expert = entry[0], slot = entry[1], count = entry[2];
+    const int64_t i = u % per * 32 + c;
+    const float4* p = parts + slot * n4 + i;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    constexpr int kAtOnce = 8;  // loads under way together
-    for (int k = 0; k < count; k += kAtOnce) {
+    constexpr int kAtOnce = 4;  // loads under way together
+    for (int k = l; k < count; k += 8 * kAtOnce) {
       float4 a[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
-        a[j] = k + j < count ? __ldcs(p + (k + j) * n4 + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        a[j] = k + 8 * j < count ? __ldcs(p + (k + 8 * j) * n4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) v = make_float4(v.x + a[j].x, v.y + a[j].y, v.z + a[j].z, v.w + a[j].w);
     }
-    const int64_t at = blockIdx.y * n4 + i;
-    if (F32) {
-      float4* o = static_cast<float4*>(dw) + at;
-      if (accumulate) {
-        const float4 b = *o;
+    s[l][c] = v;
+    __syncthreads();
+    if (l == 0) {
+      const int most = count < 8 ? count : 8;
+      for (int k = 1; k < most; ++k) {
+        const float4 b = s[k][c];
         v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
       }
-      *o = v;
-    } else {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-      static_cast<uint2*>(dw)[at] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      const int64_t at = expert * n4 + i;
+      if (F32) {
+        float4* o = static_cast<float4*>(dw) + at;
+        if (accumulate) {
+          const float4 b = *o;
+          v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+        }
+        *o = v;
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        static_cast<uint2*>(dw)[at] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -743,6 +765,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t unpacked_bytes(int a_max, int K) { return up256((size_t)a_max * K * 2); }
 // Slots: an expert that is cut has more than one part, of which all but the last are whole.
 int64_t most_slots(int a_max, int part) { return 2 * (int64_t)a_max / part; }
+size_t cut_bytes(int E) { return up256((size_t)(1 + 3 * E) * sizeof(int)); }
 
 // dW [E, N, K] as a 3-D map, boxes of 32 rows x 128 bytes in one expert: stores clip at its edges.
 bool make_dw_map(CUtensorMap* map, void* base, int E, int N, int K, bool f32) {
@@ -777,7 +800,7 @@ bool make_zero_map(CUtensorMap* map, const void* dy, int a_max, int N, int rows)
 size_t weight_grad_workspace_bytes(int E, int a_max, int N, int K, bool packed) {
   size_t n = packed ? unpacked_bytes(a_max, K) : 0;
   if (const int part = part_rows(a_max, N, K))
-    n += up256((size_t)E * 8) + (size_t)most_slots(a_max, part) * N * K * sizeof(float);
+    n += cut_bytes(E) + (size_t)most_slots(a_max, part) * N * K * sizeof(float);
   return n;
 }
 
@@ -817,8 +840,8 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   p.last = divisor(mt % kGroup ? (int)(mt % kGroup) : kGroup);
   p.accumulate = g.accumulate;
   p.blocks = !p.part && g.E <= kTwoBlocksMaxE ? 2 : 1;
-  int* first_part = reinterpret_cast<int*>(ws);
-  float* parts = reinterpret_cast<float*>(ws + up256((size_t)g.E * 8));
+  int* cut = reinterpret_cast<int*>(ws);
+  float* parts = reinterpret_cast<float*>(ws + cut_bytes(g.E));
   CUtensorMap dw, dy, mx, z4, z1, mp;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
   mp = dy = mx = z4 = z1 = dw;  // without rows nothing is loaded, without parts none are stored
@@ -851,19 +874,19 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   if (pairs < 1) return cudaErrorNotSupported;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, mp, g.counts, p, first_part, g.err);
+  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, mp, g.counts, p, cut, g.err);
   if (e != cudaSuccess) return e;
   if (!p.part) return cudaGetLastError();
-  const int64_t n4 = (int64_t)g.N * g.K / 4, want = (n4 + 255) / 256;
+  const int64_t n4 = (int64_t)g.N * g.K / 4, want = n4 / 32 * g.E, most = 8 * (int64_t)device_sm_count();
   cudaLaunchConfig_t join = {};
-  join.gridDim = dim3((unsigned)(want < 304 ? want : 304), (unsigned)g.E);
+  join.gridDim = dim3((unsigned)(want < most ? want : most));
   join.blockDim = dim3(256);
   join.stream = s;
   cudaLaunchAttribute pdl[1] = {pdl_attribute()};
   join.attrs = pdl;
   join.numAttrs = 1;
   auto jk = f32 ? join_parts_kernel<true> : join_parts_kernel<false>;
-  e = cudaLaunchKernelEx(&join, jk, reinterpret_cast<const float4*>(parts), (const int*)first_part, n4, g.accumulate,
+  e = cudaLaunchKernelEx(&join, jk, reinterpret_cast<const float4*>(parts), (const int*)cut, n4, g.accumulate,
                          g.dw);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
