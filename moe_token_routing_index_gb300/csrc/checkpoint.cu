@@ -2,7 +2,8 @@
 // (include/moe_train.h).  Bound by memory: 32768 rows of 2 x 2048, SiLU*mul 83 us (6.4
 // TB/s), its gradient 102 us (6.6 TB/s).  The passes that quantise are close to bound by
 // instruction issue as well, so a block's largest value is found on pairs of bf16 as they
-// were loaded, and their registers are held to four blocks a SM (three: 94 us, five: 100).
+// were loaded.  Registers are held to four blocks a SM forward (three: 94 us, five: 100),
+// five backward (two: 117 us).
 //
 // A thread holds 16 columns (32 bytes of bf16, 16 bytes of codes); the 8 threads of
 // an aligned group hold one 128-column block and find its largest value by shuffles.
@@ -102,7 +103,7 @@ __device__ int row_count(const CheckpointArgs& g) {
 enum Op { kPack, kUnpack, kSilu, kSiluGrad };
 
 template <int OP>
-__global__ void __launch_bounds__(kThreads, OP == kSilu ? 4 : 1) checkpoint_kernel(const CheckpointArgs g) {
+__global__ void __launch_bounds__(kThreads, OP == kSilu ? 4 : 5) checkpoint_kernel(const CheckpointArgs g) {
   const int nb = (g.W + MOE_CHECKPOINT_BLOCK - 1) / MOE_CHECKPOINT_BLOCK;
   const int64_t units = (int64_t)row_count(g) * nb * 8;  // a multiple of 8: groups of 8 threads are whole
   const int64_t rounded = (units + 31) / 32 * 32;        // and every warp's threads run the same passes
