@@ -9,7 +9,7 @@ not been built (``python -m moe_token_routing_index_gb300.build``).
 
 import importlib
 
-_SUBMODULES = ("binding", "build", "forward", "workloads")
+_SUBMODULES = ("binding", "build", "forward", "training", "workloads")
 __all__ = list(_SUBMODULES)
 
 
