@@ -303,52 +303,68 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// One epilogue warp's rows of a tile: row (its first) + lane, 64 columns at a time, through
-// the next of its staging blocks (*blk) 128 bytes of a row each, to matrix `at` of map.
-// zero: the tile of an expert without rows; add: to what is there (fp32).
-template <bool F32>
+// Stores a staging block's 32 rows x 128 bytes (o[q]: piece q of this lane's row) as columns
+// from c on, rows from row on of matrix `at` of map; add: to what is there (fp32).
+__device__ __forceinline__ void store_block(const Shape& p, const Tile& t, const uint4* o, int c, int row, int lane,
+                                            uint8_t* stage, int* blk, const CUtensorMap* map, int at, bool add) {
+  if (lane == 0) {  // the store that last used this block has read it
+    if (p.blocks == 1 || t.rows > kBurstRows) bulk_wait_group_read0();
+    else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  }
+  __syncwarp();
+  uint8_t* b = stage + *blk * kEpiBlockBytes;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(b + lane * 128 + ((q ^ (lane & 7)) << 4)) = o[q];
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    if (add) tma_add_3d(map, smem_u32(b), t.k0 + c, row, at);
+    else tma_store_3d(map, smem_u32(b), t.k0 + c, row, at);
+    bulk_commit_group();
+  }
+  if (++*blk == p.blocks) *blk = 0;
+}
+
+// One epilogue warp's rows of a tile: row (its first) + lane, to matrix `at` of map.  zero:
+// the tile of an expert without rows.  release() gives the accumulator back: for bf16 once
+// all of it is in registers as pairs, before the stores, which take most of the time (128
+// experts of Zipf-like load, N = 7168, K = 2048: 987 us when it came after them).
+template <bool F32, typename Release>
 __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int row, int lane, uint32_t tbase, bool zero,
-                                           uint8_t* stage, int* blk, const CUtensorMap* map, int at, bool add) {
-  if (row >= p.N) return;
+                                           uint8_t* stage, int* blk, const CUtensorMap* map, int at, bool add,
+                                           Release release) {
+  if (row >= p.N) {
+    release();
+    return;
+  }
   const int cols = min(kTile, p.K - t.k0);
+  if constexpr (F32) {
 #pragma unroll 1
-  for (int c = 0; c < cols; c += 64) {
-    uint32_t v[64];
-    if (zero) {
+    for (int c = 0; c < cols; c += 64) {
+      uint32_t v[64] = {};
+      if (!zero) tmem_ld64(tbase + c, v);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = 0u;
-    } else {
-      tmem_ld64(tbase + c, v);
+      for (int h = 0; h < 2; ++h)
+        if (c + 32 * h < cols)
+          store_block(p, t, reinterpret_cast<const uint4*>(v + 32 * h), c + 32 * h, row, lane, stage, blk, map, at, add);
     }
+    release();
+  } else {
+    uint4 w[kTile / 64][8] = {};
+    if (!zero) {
 #pragma unroll
-    for (int h = 0; h < (F32 ? 2 : 1); ++h) {
-      if (F32 && c + 32 * h >= cols) break;
-      if (lane == 0) {  // the store that last used this block has read it
-        if (p.blocks == 1 || t.rows > kBurstRows) bulk_wait_group_read0();
-        else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      }
-      __syncwarp();
-      uint8_t* b = stage + *blk * kEpiBlockBytes;
+      for (int j = 0; j < kTile / 64; ++j)
+        if (64 * j < cols) {
+          uint32_t v[64];
+          tmem_ld64(tbase + 64 * j, v);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint4 o;
-        if (F32) {
-          const uint32_t* w = v + 32 * h + 4 * q;
-          o = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          o = f32_to_bf16x8(reinterpret_cast<const float*>(v) + 8 * q);
+          for (int q = 0; q < 8; ++q) w[j][q] = f32_to_bf16x8(reinterpret_cast<const float*>(v) + 8 * q);
         }
-        *reinterpret_cast<uint4*>(b + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        if (F32 && add) tma_add_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, at);
-        else tma_store_3d(map, smem_u32(b), t.k0 + c + 32 * h, row, at);
-        bulk_commit_group();
-      }
-      if (++*blk == p.blocks) *blk = 0;
     }
+    release();
+#pragma unroll
+    for (int j = 0; j < kTile / 64; ++j)
+      if (64 * j < cols) store_block(p, t, w[j], 64 * j, row, lane, stage, blk, map, at, false);
   }
 }
 
@@ -666,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = SPLIT ? units.slot[c.t.unit] : kWhole;
       const int expert = SPLIT ? units.owner[c.t.unit] : c.t.unit;
       if (c.t.rows == 0) {
-        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw, expert, false);
+        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw, expert, false, [] {});
         continue;
       }
       if (!warp_wait(bar_tfull(c.acc), (acc_parity >> c.acc) & 1u, s_abort)) {
@@ -677,11 +693,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc_parity ^= 1u << c.acc;
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(c.acc * kTile);
-      if (SPLIT && slot != kWhole) store_tile<true>(p, c.t, row, lane, tbase, false, stage, &blk, &map_part, slot, false);
-      else store_tile<F32>(p, c.t, row, lane, tbase, false, stage, &blk, &map_dw, expert, p.accumulate);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(c.acc * 8));
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(c.acc * 8));
+      };
+      if (SPLIT && slot != kWhole)
+        store_tile<true>(p, c.t, row, lane, tbase, false, stage, &blk, &map_part, slot, false, release);
+      else
+        store_tile<F32>(p, c.t, row, lane, tbase, false, stage, &blk, &map_dw, expert, p.accumulate, release);
     }
     if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the block exits
   }
