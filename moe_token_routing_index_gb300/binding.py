@@ -10,6 +10,7 @@ the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import re
 from pathlib import Path
 
@@ -623,6 +624,7 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
     return out, mean, rstd
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_layer_norm_backward_workspace_size(T: int, D: int) -> int:
     n = ctypes.c_size_t(0)
     _check("moe_layer_norm_backward_workspace_size",
@@ -656,6 +658,7 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
 
 # --------------------------------------------------------------- balance loss
 
+@functools.lru_cache(maxsize=1024)
 def moe_balance_loss_workspace_size(T: int, E: int) -> int:
     n = ctypes.c_size_t(0)
     _check("moe_balance_loss_workspace_size", _lib.moe_balance_loss_workspace_size(T, E, ctypes.byref(n)))
@@ -808,6 +811,7 @@ def moe_silu_mul_backward(checkpoint: Checkpoint, dz, valid_rows=None, *, out=No
 
 # --------------------------------------------------------------- weight gradient
 
+@functools.lru_cache(maxsize=1024)
 def moe_grouped_weight_grad_workspace_size(E: int, a_max: int, N: int, K: int, x_dtype: int) -> int:
     n = ctypes.c_size_t(0)
     _check("moe_grouped_weight_grad_workspace_size",
