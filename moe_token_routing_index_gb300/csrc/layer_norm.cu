@@ -13,11 +13,18 @@
 //
 // Rows wider than a warp's go through a ring of rows in shared memory for each group,
 // filled by bulk copies several rows ahead (Ring), with the weights in fp32 beside it;
-// narrower, unaligned and very wide fp32 rows are loaded straight into registers.  Loaded
-// one row ahead into registers, 11000 rows of 4096 took 49 us and the gradient of 8192 rows
-// of 5120 took 106 us (bf16): the values held ahead left too few warps to hide the
-// reductions.  Arithmetic is in pairs (fma.rn.f32x2), and 32 values a thread spread a
-// row's fixed cost over enough elements.
+// narrower rows, few rows, very wide fp32 rows and rows whose tensors are aligned apart are
+// loaded straight into registers.  Loaded one row ahead into registers, 11000 rows of 4096
+// took 49 us and the gradient of 8192 rows of 5120 took 106 us (bf16): the values held
+// ahead left too few warps to hide the reductions; through the ring 35 and 54 us, 5.2 and
+// 4.7 TB/s.  Arithmetic is in pairs (fma.rn.f32x2), and 32 values a thread spread a row's
+// fixed cost over enough elements.
+//
+// Dense rows of a width that is no multiple of 16 bytes start at varying offsets inside 16
+// bytes (SHIFT).  They repeat every 8 rows at most, and a group's rows are a multiple of 8
+// apart, so each group has its own offset throughout, and cuts its rows into the 8-column
+// pieces that are aligned in memory: only a row's first and last piece are not whole.
+// 5000 rows of 4097 in bf16 take 42 us and 74 backward; by single columns, 112 and 129.
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -162,28 +169,29 @@ struct Row {
   }
 };
 
-// A group's ring of rows in shared memory: `mats` rows of `bytes` (of x, and of dy) a stage,
-// filled by the group's first thread and awaited by all of it.  bars: one mbarrier a stage.
+// A group's ring of rows in shared memory: `mats` rows (of x, and of dy) a stage, filled by
+// the group's first thread and awaited by all of it.  bars: one mbarrier a stage.
 struct Ring {
   uint32_t base, bars;
-  int bytes, mats, stages;
+  int slot, mats, stages;    // slot: bytes of a row's place
   int stage = 0, next = 0;   // being read; to be filled
   uint32_t parity = 0;       // of the stage being read
 
   __device__ __forceinline__ uint32_t at(int st, int mat) const {
-    return base + (uint32_t)((st * mats + mat) * bytes);
+    return base + (uint32_t)((st * mats + mat) * slot);
   }
-  __device__ __forceinline__ void fill(const void* x, const void* dy) {
+  // n bytes of each row, from 16-byte boundaries.
+  __device__ __forceinline__ void fill(const void* x, const void* dy, int n) {
     const uint32_t bar = bars + 8 * next;
-    tc::mbar_arrive_expect_tx(bar, (uint32_t)(bytes * mats));
-    copy(at(next, 0), x, bar);
-    if (mats == 2) copy(at(next, 1), dy, bar);
+    tc::mbar_arrive_expect_tx(bar, (uint32_t)(n * mats));
+    copy(at(next, 0), x, n, bar);
+    if (mats == 2) copy(at(next, 1), dy, n, bar);
     if (++next == stages) next = 0;
   }
-  __device__ __forceinline__ void copy(uint32_t dst, const void* src, uint32_t bar) const {
+  __device__ __forceinline__ void copy(uint32_t dst, const void* src, int n, uint32_t bar) const {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-        "r"(bytes), "r"(bar)
+        "r"(n), "r"(bar)
         : "memory");
   }
   __device__ __forceinline__ bool wait() const { return tc::mbar_wait(bars + 8 * stage, parity, nullptr); }
@@ -194,6 +202,28 @@ struct Ring {
     }
   }
 };
+
+// How a group's rows lie: sh elements past a 16-byte boundary.  A copy starts at that boundary
+// (before a row's start only where other rows precede it: row 0 has no offset) and ends at
+// the one after the row, but for the last row of the tensors at the one before.
+template <typename T, bool SHIFT>
+struct Placing {
+  int D, last, sh;
+  __device__ __forceinline__ Placing(int D_, int T_, int64_t t0)
+      : D(D_), last(T_ - 1), sh(SHIFT ? (int)(t0 * D_ * (int)sizeof(T) & 15) / (int)sizeof(T) : 0) {}
+  __device__ __forceinline__ int bytes(int64_t t) const {
+    const int n = (D + sh) * (int)sizeof(T);
+    return !SHIFT || t == last ? n & ~15 : (n + 15) & ~15;
+  }
+  // First column of piece `piece` (may be negative), whether it has any column of the row, all 8.
+  __device__ __forceinline__ int column(int piece) const { return piece * 8 - sh; }
+  __device__ __forceinline__ bool any(int d) const { return d < D; }  // (sh < 8)
+  __device__ __forceinline__ bool whole(int d) const { return !SHIFT || (d >= 0 && d + 8 <= D); }
+};
+template <typename T>
+__host__ __device__ __forceinline__ int slot_bytes(int D, bool shift) {
+  return (shift ? (D + 14) / 8 * 8 : D) * (int)sizeof(T);  // whole pieces
+}
 
 constexpr int kMaxStages = 6;
 
@@ -232,9 +262,27 @@ __device__ __forceinline__ bool group_agrees(bool ok, int group, int R) {
   return all != 0;
 }
 
-// The weights of a row in shared memory as fp32, the first four of each 8 columns,
-// then the last four (16-byte accesses of neighbouring threads are then contiguous).
+// The weights of a row in shared memory as fp32.  Whole pieces: the first four of each 8
+// columns, then the last four (16-byte accesses of neighbouring threads are then contiguous).
+// SHIFT: one by one with 8 zeros on either side and a gap every 32 (neighbouring threads'
+// pieces, 8 apart, then lie in different banks).
+template <bool SHIFT>
+__host__ __device__ __forceinline__ int weight_floats(int D) {
+  return SHIFT ? ((D + 16) + (D + 16) / 32 + 4) / 4 * 4 : D;
+}
+template <bool SHIFT>
 __device__ __forceinline__ void stage_weights(float* s, const void* w, int dtype, int D) {
+  if constexpr (SHIFT) {
+    for (int i = threadIdx.x; i < D + 16; i += blockDim.x) {
+      const int d = i - 8;
+      float v = 0.0f;
+      if (w && d >= 0 && d < D)
+        v = dtype == MOE_DTYPE_F32 ? __ldg(static_cast<const float*>(w) + d)
+                                   : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + d));
+      s[i + (i >> 5)] = v;
+    }
+    return;
+  }
   for (int c = threadIdx.x; c < D / 8; c += blockDim.x) {
     float v[8] = {};
     if (w) {
@@ -254,14 +302,23 @@ __device__ __forceinline__ void stage_weights(float* s, const void* w, int dtype
     reinterpret_cast<float4*>(s + D / 2)[c] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
-// Pairs 0 .. 3 of the 8 weights from column d.
+// Pairs 0 .. 3 of the 8 weights from column d (SHIFT: -7 .. D - 1; 0 outside the row).
+template <bool SHIFT>
 __device__ __forceinline__ void shared_weights(const float* s, int d, int D, f2* w) {
-  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s + (d >> 1));
-  const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(s + D / 2 + (d >> 1));
-  w[0] = a.x;
-  w[1] = a.y;
-  w[2] = b.x;
-  w[3] = b.y;
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = d + 8 + 2 * j;
+      w[j] = pack(s[i + (i >> 5)], s[i + 1 + ((i + 1) >> 5)]);
+    }
+  } else {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s + (d >> 1));
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(s + D / 2 + (d >> 1));
+    w[0] = a.x;
+    w[1] = a.y;
+    w[2] = b.x;
+    w[3] = b.y;
+  }
 }
 
 template <typename T>
@@ -281,9 +338,43 @@ __device__ __forceinline__ void store_piece(T* p, const f2* v) {
   Piece<T, 8>::store(p, o);
 }
 
-// The barriers of all rings of the block, and this group's ring behind `reserved` bytes.
+// Of a piece that is not whole: zeros outside the row; its values where the copy of the
+// tensors' last row left them out; its stores.
+__device__ __forceinline__ f2 masked_pair(f2 v, int d, int D) {
+  const float2 u = unpack(v);
+  return pack(d >= 0 && d < D ? u.x : 0.0f, d + 1 >= 0 && d + 1 < D ? u.y : 0.0f);
+}
 template <typename T>
-__device__ __forceinline__ Ring make_ring(uint8_t* rows, uint64_t* bars, int mats, int stages, int D, int groups,
+__device__ __forceinline__ f2 direct_pair(const T* row, int d, int D) {
+  return pack(d >= 0 && d < D ? to_f32(__ldg(row + d)) : 0.0f,
+              d + 1 >= 0 && d + 1 < D ? to_f32(__ldg(row + d + 1)) : 0.0f);
+}
+template <typename T>
+__device__ __forceinline__ void store_part(T* row, int d, int D, const f2* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 u = unpack(v[j]);
+    const int k = d + 2 * j;
+    if (k >= 0 && k < D) put(row + k, u.x);
+    if (k + 1 >= 0 && k + 1 < D) put(row + k + 1, u.y);
+  }
+}
+// The pairs of a row's piece in shared memory from column d, `piece` 8 values in.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void row_piece(const Placing<T, SHIFT>& at, uint32_t slot, int piece, int d, const T* row,
+                                          bool last, f2* v) {
+  const Piece<T, 8> p = shared_piece<T>(slot, piece * 8);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = piece_pair(p, j);
+  if (!at.whole(d)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = last ? direct_pair(row, d + 2 * j, at.D) : masked_pair(v[j], d + 2 * j, at.D);
+  }
+}
+
+// The barriers of all rings of the block, and this group's ring.
+__device__ __forceinline__ Ring make_ring(uint8_t* rows, uint64_t* bars, int mats, int stages, int slot, int groups,
                                           int group) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < groups; ++i)
@@ -292,10 +383,10 @@ __device__ __forceinline__ Ring make_ring(uint8_t* rows, uint64_t* bars, int mat
     tc::fence_proxy_async_shared();
   }
   Ring r;
-  r.bytes = D * (int)sizeof(T);
+  r.slot = slot;
   r.mats = mats;
   r.stages = stages;
-  r.base = tc::smem_u32(rows) + (uint32_t)(group * stages * mats * r.bytes);
+  r.base = tc::smem_u32(rows) + (uint32_t)(group * stages * mats * slot);
   r.bars = tc::smem_u32(bars + group * kMaxStages);
   return r;
 }
@@ -328,7 +419,7 @@ __device__ __forceinline__ float2 ring_sum(float2 v, float2* s, int group, int R
   return v;
 }
 
-template <typename T, int THREADS>
+template <typename T, bool SHIFT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const NormArgs g, int R, float inv_d, int stages) {
   extern __shared__ __align__(128) uint8_t s_mem[];  // gamma, beta, the rings
   __shared__ float2 s_sum[2][2][THREADS / 32];       // by turns, two sums of each warp
@@ -338,29 +429,30 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const NormArgs g,
   const int64_t stride = (int64_t)gridDim.x * groups;
   int64_t t = (int64_t)blockIdx.x * groups + group, ahead = t;  // the next row to fill a stage with
   const T* x0 = static_cast<const T*>(g.x);
+  const Placing<T, SHIFT> at(D, g.T, t);
   float* gamma = reinterpret_cast<float*>(s_mem);
-  float* beta = gamma + D;
-  Ring ring = make_ring<T>(s_mem + 8 * D, s_bars, 1, stages, D, groups, group);
+  float* beta = gamma + weight_floats<SHIFT>(D);
+  Ring ring = make_ring(reinterpret_cast<uint8_t*>(beta + weight_floats<SHIFT>(D)), s_bars, 1, stages,
+                        slot_bytes<T>(D, SHIFT), groups, group);
+  auto fill = [&] { ring.fill(x0 + ahead * g.ldx - at.sh, nullptr, at.bytes(ahead)); };
   __syncthreads();
   if (gt == 0)
-    for (int st = 0; st < stages - 1 && ahead < n; ++st, ahead += stride) ring.fill(x0 + ahead * g.ldx, nullptr);
-  stage_weights(gamma, g.gamma, g.weight_dtype, D);
-  stage_weights(beta, g.beta, g.weight_dtype, D);
+    for (int st = 0; st < stages - 1 && ahead < n; ++st, ahead += stride) fill();
+  stage_weights<SHIFT>(gamma, g.gamma, g.weight_dtype, D);
+  stage_weights<SHIFT>(beta, g.beta, g.weight_dtype, D);
   __syncthreads();
   bool ok = true;
   for (int turn = 0; t < n; t += stride, turn ^= 1) {
     ok = ring.wait();
+    const T* row = x0 + t * g.ldx;
     f2 v[kRingValues / 2], s = both(0.0f);
 #pragma unroll
     for (int c = 0; c < kRingValues / 8; ++c) {
-      const int d = (c * R + gt) * 8;
-      if (d < D) {
-        const Piece<T, 8> p = shared_piece<T>(ring.at(ring.stage, 0), d);
+      const int d = at.column(c * R + gt);
+      if (at.any(d)) {
+        row_piece(at, ring.at(ring.stage, 0), c * R + gt, d, row, t == at.last, v + 4 * c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[4 * c + j] = piece_pair(p, j);
-          s = add2(s, v[4 * c + j]);
-        }
+        for (int j = 4 * c; j < 4 * c + 4; ++j) s = add2(s, v[j]);
       }
     }
     const float mean = ring_sum(make_float2(sum2(s), 0.0f), s_sum[turn][0], group, R, &ok).x * inv_d;
@@ -368,32 +460,39 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const NormArgs g,
     // the group has read this row and those before: refill the stage of the last
     if (gt == 0 && ahead < n) {
       tc::fence_proxy_async_shared();
-      ring.fill(x0 + ahead * g.ldx, nullptr);
+      fill();
     }
     ahead += stride;
     ring.advance();
     s = both(0.0f);
 #pragma unroll
-    for (int c = 0; c < kRingValues / 8; ++c)
-      if ((c * R + gt) * 8 < D)
+    for (int c = 0; c < kRingValues / 8; ++c) {
+      const int d = at.column(c * R + gt);
+      if (at.any(d)) {
 #pragma unroll
-        for (int j = 4 * c; j < 4 * c + 4; ++j) {
-          v[j] = add2(v[j], both(-mean));
-          s = fma2(v[j], v[j], s);
+        for (int j = 4 * c; j < 4 * c + 4; ++j) v[j] = add2(v[j], both(-mean));
+        if (!at.whole(d)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * c + j] = masked_pair(v[4 * c + j], d + 2 * j, D);
         }
+#pragma unroll
+        for (int j = 4 * c; j < 4 * c + 4; ++j) s = fma2(v[j], v[j], s);
+      }
+    }
     const float rstd =
         rsqrtf(ring_sum(make_float2(sum2(s), 0.0f), s_sum[turn][1], group, R, &ok).x * inv_d + g.eps);
     T* y = static_cast<T*>(g.y) + t * D;
 #pragma unroll
     for (int c = 0; c < kRingValues / 8; ++c) {
-      const int d = (c * R + gt) * 8;
-      if (d < D) {
+      const int d = at.column(c * R + gt);
+      if (at.any(d)) {
         f2 w[4], b[4];
-        shared_weights(gamma, d, D, w);
-        shared_weights(beta, d, D, b);
+        shared_weights<SHIFT>(gamma, d, D, w);
+        shared_weights<SHIFT>(beta, d, D, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = fma2(mul2(v[4 * c + j], both(rstd)), w[j], b[j]);
-        store_piece(y + d, w);
+        if (at.whole(d)) store_piece(y + d, w);
+        else store_part(y, d, D, w);
       }
     }
     if (gt == 0) {
@@ -406,8 +505,8 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const NormArgs g,
 
 // This block's row of partial [blocks][2][D]: each group's sums into s [groups][2][D], whose
 // columns are then added over the groups in order.  A thread's piece c of VEC values begins
-// at column col(c).
-template <int VEC, int C, typename F>
+// at column col(c); WHOLE: no piece reaches past the row.
+template <int VEC, int C, bool WHOLE, typename F>
 __device__ __forceinline__ void store_partial(float* partial, float* s, const f2* dg, const f2* db, int group,
                                               int groups, int D, F col) {
   __syncthreads();  // s is free
@@ -416,7 +515,21 @@ __device__ __forceinline__ void store_partial(float* partial, float* s, const f2
   for (int c = 0; c < C; ++c) {
     const int d = col(c);
     if (d >= D) continue;
-    if constexpr (VEC == 8) {
+    if constexpr (VEC == 8 && !WHOLE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = unpack(dg[4 * c + j]), b = unpack(db[4 * c + j]);
+        const int k = d + 2 * j;
+        if (k >= 0 && k < D) {
+          mine[k] = a.x;
+          mine[D + k] = b.x;
+        }
+        if (k + 1 >= 0 && k + 1 < D) {
+          mine[k + 1] = a.y;
+          mine[D + k + 1] = b.y;
+        }
+      }
+    } else if constexpr (VEC == 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         *reinterpret_cast<ulonglong2*>(mine + d + 4 * h) = make_ulonglong2(dg[4 * c + 2 * h], dg[4 * c + 2 * h + 1]);
@@ -437,7 +550,7 @@ __device__ __forceinline__ void store_partial(float* partial, float* s, const f2
   }
 }
 
-template <typename T, int THREADS>
+template <typename T, bool SHIFT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_grad_ring_kernel(const NormArgs g, int R, float inv_d, int stages, float* partial) {
   extern __shared__ __align__(128) uint8_t s_mem[];  // gamma, the rings; then the groups' sums
@@ -450,13 +563,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   int64_t t = (int64_t)blockIdx.x * groups + group, ahead = t;
   const T* x0 = static_cast<const T*>(g.x);
   const T* dy0 = static_cast<const T*>(g.dy);
+  const Placing<T, SHIFT> at(D, g.T, t);
   float* gamma = reinterpret_cast<float*>(s_mem);
-  Ring ring = make_ring<T>(s_mem + 4 * D, s_bars, 2, stages, D, groups, group);
+  Ring ring = make_ring(reinterpret_cast<uint8_t*>(gamma + weight_floats<SHIFT>(D)), s_bars, 2, stages,
+                        slot_bytes<T>(D, SHIFT), groups, group);
+  auto fill = [&] { ring.fill(x0 + ahead * g.ldx - at.sh, dy0 + ahead * D - at.sh, at.bytes(ahead)); };
   __syncthreads();
   if (gt == 0)
-    for (int st = 0; st < stages - 1 && ahead < n; ++st, ahead += stride)
-      ring.fill(x0 + ahead * g.ldx, dy0 + ahead * D);
-  stage_weights(gamma, g.gamma, g.weight_dtype, D);
+    for (int st = 0; st < stages - 1 && ahead < n; ++st, ahead += stride) fill();
+  stage_weights<SHIFT>(gamma, g.gamma, g.weight_dtype, D);
   __syncthreads();
   f2 dg[kRingValues / 2], db[kRingValues / 2];
 #pragma unroll
@@ -476,19 +591,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     ok = ring.wait();
     const uint32_t xr = ring.at(ring.stage, 0), dyr = ring.at(ring.stage, 1);
+    const T* x = x0 + t * g.ldx;
+    const T* dy = dy0 + t * D;
     f2 s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
     for (int c = 0; c < kRingValues / 8; ++c) {
-      const int d = (c * R + gt) * 8;
-      if (d < D) {
-        const Piece<T, 8> px = shared_piece<T>(xr, d), py = shared_piece<T>(dyr, d);
-        f2 w[4];
-        shared_weights(gamma, d, D, w);
+      const int d = at.column(c * R + gt);
+      if (at.any(d)) {
+        f2 px[4], py[4], w[4];
+        row_piece(at, xr, c * R + gt, d, x, t == at.last, px);
+        row_piece(at, dyr, c * R + gt, d, dy, t == at.last, py);
+        shared_weights<SHIFT>(gamma, d, D, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f2 y = piece_pair(py, j), xc = add2(piece_pair(px, j), m2), gd = mul2(y, w[j]);
-          dg[4 * c + j] = fma2(mul2(y, r2), xc, dg[4 * c + j]);
-          db[4 * c + j] = add2(db[4 * c + j], y);
+          const f2 xc = add2(px[j], m2), gd = mul2(py[j], w[j]);
+          dg[4 * c + j] = fma2(mul2(py[j], r2), xc, dg[4 * c + j]);
+          db[4 * c + j] = add2(db[4 * c + j], py[j]);
           s0 = add2(s0, gd);
           s1 = fma2(gd, xc, s1);
         }
@@ -499,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the group is past the row before this one: refill its stage
     if (gt == 0 && ahead < n) {
       tc::fence_proxy_async_shared();
-      ring.fill(x0 + ahead * g.ldx, dy0 + ahead * D);
+      fill();
     }
     ahead += stride;
     // dx = r gd - r m0 - (x - mean) r^2 m1 with m0 = (1/D) sum gd, m1 = (1/D) sum gd r (x - mean)
@@ -508,28 +626,36 @@ __global__ void __launch_bounds__(THREADS, 1)
     const T* res = g.residual ? static_cast<const T*>(g.residual) + t * D : nullptr;
 #pragma unroll
     for (int c = 0; c < kRingValues / 8; ++c) {
-      const int d = (c * R + gt) * 8;
-      if (d < D) {
-        const Piece<T, 8> px = shared_piece<T>(xr, d), py = shared_piece<T>(dyr, d);
-        f2 w[4];
-        shared_weights(gamma, d, D, w);
+      const int d = at.column(c * R + gt);
+      if (at.any(d)) {
+        f2 px[4], py[4], w[4];
+        row_piece(at, xr, c * R + gt, d, x, t == at.last, px);
+        row_piece(at, dyr, c * R + gt, d, dy, t == at.last, py);
+        shared_weights<SHIFT>(gamma, d, D, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = fma2(mul2(piece_pair(py, j), w[j]), r2, fma2(add2(piece_pair(px, j), m2), k1, k0));
-        if (res) {
-          Piece<T, 8> pr;
-          pr.load(res + d);
+        for (int j = 0; j < 4; ++j) w[j] = fma2(mul2(py[j], w[j]), r2, fma2(add2(px[j], m2), k1, k0));
+        if (at.whole(d)) {
+          if (res) {
+            Piece<T, 8> pr;
+            pr.load(res + d);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = add2(w[j], piece_pair(pr, j));
+            for (int j = 0; j < 4; ++j) w[j] = add2(w[j], piece_pair(pr, j));
+          }
+          store_piece(dx + d, w);
+        } else {
+          if (res) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = add2(w[j], direct_pair(res, d + 2 * j, D));
+          }
+          store_part(dx, d, D, w);
         }
-        store_piece(dx + d, w);
       }
     }
     ring.advance();
   }
   if (t < n && gt == 0) drain_ring(g.err);
-  store_partial<8, kRingValues / 8>(partial, reinterpret_cast<float*>(s_mem), dg, db, group, groups, D,
-                                    [&](int c) { return (c * R + gt) * 8; });
+  store_partial<8, kRingValues / 8, !SHIFT>(partial, reinterpret_cast<float*>(s_mem), dg, db, group, groups, D,
+                                            [&](int c) { return at.column(c * R + gt); });
 }
 
 // Rows straight into registers.
@@ -629,8 +755,8 @@ __global__ void __launch_bounds__(THREADS, VEC == 1 && THREADS <= 512 ? 2 : 1) n
       Row<T, VEC, N>::store(dx, R, gt, D, grad);
     }
   }
-  store_partial<VEC, N / VEC>(partial, reinterpret_cast<float*>(s_mem), dg, db, group, groups, D,
-                              [&](int c) { return (c * R + gt) * VEC; });
+  store_partial<VEC, N / VEC, true>(partial, reinterpret_cast<float*>(s_mem), dg, db, group, groups, D,
+                                    [&](int c) { return (c * R + gt) * VEC; });
 }
 
 // dgamma and dbeta: a block of 32 columns of the 2 D and 32 lanes of rows, each adding every
@@ -668,16 +794,27 @@ struct Int {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// f(x element, weight element, VEC)
+// How the rows lie: in whole 16-byte pieces (kWide); at offsets that are the same for all of a
+// row's tensors (kShifted); or neither.
+enum Layout { kWide, kShifted, kSingle };
+
+Layout layout_of(const NormArgs& g) {
+  const int es = g.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (!aligned16(g.x) || !aligned16(g.y) || !aligned16(g.dy) || !aligned16(g.residual)) return kSingle;
+  if (g.D % 8 == 0 && g.ldx * es % 16 == 0 && aligned16(g.gamma) && aligned16(g.beta)) return kWide;
+  return (g.ldx - g.D) * es % 16 == 0 ? kShifted : kSingle;
+}
+
+// f(x element, weight element, layout)
 template <typename F>
 cudaError_t by_types(const NormArgs& g, F f) {
   const bool xf = g.dtype == MOE_DTYPE_F32, wf = g.weight_dtype == MOE_DTYPE_F32;
-  const int per16 = xf ? 4 : 8;
-  const bool wide = g.D % 8 == 0 && g.ldx % per16 == 0 && aligned16(g.x) && aligned16(g.y) && aligned16(g.gamma) &&
-                    aligned16(g.beta) && aligned16(g.dy) && aligned16(g.residual);
-  auto with_vec = [&](auto x, auto w) { return wide ? f(x, w, Int<8>{}) : f(x, w, Int<1>{}); };
-  if (xf) return wf ? with_vec(float{}, float{}) : with_vec(float{}, __nv_bfloat16{});
-  return wf ? with_vec(__nv_bfloat16{}, float{}) : with_vec(__nv_bfloat16{}, __nv_bfloat16{});
+  const Layout layout = layout_of(g);
+  auto with_layout = [&](auto x, auto w) {
+    return layout == kWide ? f(x, w, Int<kWide>{}) : layout == kShifted ? f(x, w, Int<kShifted>{}) : f(x, w, Int<kSingle>{});
+  };
+  if (xf) return wf ? with_layout(float{}, float{}) : with_layout(float{}, __nv_bfloat16{});
+  return wf ? with_layout(__nv_bfloat16{}, float{}) : with_layout(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
 // How a row of D columns is held: values a thread, threads of its group, groups of a block
@@ -691,10 +828,17 @@ Shape shape(int D, int n, int most) {
 }
 
 constexpr int kWarpColumns = 512;     // rows up to this are a warp's (8 or 16 values a thread)
-constexpr int kForwardThreads = 768;  // of a ring kernel's block, in whole groups
-constexpr int kBackwardThreads = 512;
+// Of a ring kernel's block, in whole groups; fewer where the pieces at a row's ends cost registers.
+constexpr int forward_threads(bool shift) { return shift ? 640 : 768; }
+constexpr int backward_threads(bool shift) { return shift ? 384 : 512; }
 constexpr int kRingBytes = 216 * 1024;
 
+// Rows without whole pieces up to here are held 8 columns a thread, and that is faster than
+// their ring: forward, 2400 rows of 1001 in bf16 take 9 us and 13 through the ring, rows of
+// 2051 28 and 17; backward, 2400 rows of 2051 take 23 and 25, rows of 4097 68 and 45.
+constexpr int kSingleForward = 8 * 256, kSingleBackward = 8 * 320;
+
+static_assert(kNumSmsGB300 % 8 == 0, "a group's rows are a multiple of 8 apart");
 // The backward's grid: up to `each` blocks for each SM, fewer for few rows.
 int grad_blocks(int T, const Shape& sh, int each) {
   const int64_t need = ((int64_t)T + sh.groups - 1) / sh.groups, most = (int64_t)kNumSmsGB300 * each;
@@ -704,8 +848,10 @@ constexpr int kMaxGradEach = 2;
 
 // The ring kernels' shape: the most groups that leave two stages or more for each beside
 // `fixed` bytes; stages 0: none do.
-Shape ring_shape(int D, int most, int64_t fixed, int64_t stage_bytes, int* stages) {
-  Shape sh = shape(D, kRingValues, most);
+Shape ring_shape(int D, bool shift, int most, int64_t fixed, int64_t stage_bytes, int* stages) {
+  Shape sh = shape(shift ? D + 7 : D, kRingValues, most);
+  *stages = 0;
+  if (sh.R > most) return sh;
   for (;; --sh.groups) {
     const int64_t n = (kRingBytes - fixed) / (sh.groups * stage_bytes);
     *stages = n < 2 ? 0 : n > kMaxStages ? kMaxStages : (int)n;
@@ -713,13 +859,14 @@ Shape ring_shape(int D, int most, int64_t fixed, int64_t stage_bytes, int* stage
   }
 }
 
-template <typename T, int THREADS>
+template <typename T, bool SHIFT>
 cudaError_t forward_ring(const NormArgs& g, const Shape& sh, int stages, cudaStream_t s) {
-  auto kern = norm_ring_kernel<T, THREADS>;
-  const size_t smem = (size_t)8 * g.D + (size_t)sh.groups * stages * g.D * sizeof(T);
+  auto kern = norm_ring_kernel<T, SHIFT, forward_threads(SHIFT)>;
+  const size_t smem = (size_t)8 * weight_floats<SHIFT>(g.D) + (size_t)sh.groups * stages * slot_bytes<T>(g.D, SHIFT);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t need = ((int64_t)g.T + sh.groups - 1) / sh.groups, most = device_sm_count();
+  const int64_t need = ((int64_t)g.T + sh.groups - 1) / sh.groups;
+  const int64_t most = (device_sm_count() + 7) / 8 * 8;  // a group's rows are a multiple of 8 apart, or it has one
   kern<<<(int)(need < most ? need : most), sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, stages);
   return cudaGetLastError();
 }
@@ -733,10 +880,10 @@ cudaError_t forward(const NormArgs& g, const Shape& sh, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool SHIFT>
 cudaError_t backward_ring(const NormArgs& g, const Shape& sh, int stages, int* blocks, cudaStream_t s) {
-  auto kern = norm_grad_ring_kernel<T, kBackwardThreads>;
-  size_t smem = (size_t)4 * g.D + (size_t)sh.groups * stages * 2 * g.D * sizeof(T);
+  auto kern = norm_grad_ring_kernel<T, SHIFT, backward_threads(SHIFT)>;
+  size_t smem = (size_t)4 * weight_floats<SHIFT>(g.D) + (size_t)sh.groups * stages * 2 * slot_bytes<T>(g.D, SHIFT);
   if (smem < (size_t)sh.groups * 8 * g.D) smem = (size_t)sh.groups * 8 * g.D;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -759,22 +906,25 @@ cudaError_t backward(const NormArgs& g, const Shape& sh, int* blocks, cudaStream
 }  // namespace
 
 cudaError_t launch_layer_norm(const NormArgs& g, cudaStream_t s) {
-  return by_types(g, [&](auto x, auto w, auto vec) {
+  return by_types(g, [&](auto x, auto w, auto layout) {
     using T = decltype(x);
     using W = decltype(w);
-    constexpr int VEC = decltype(vec)::v;
+    constexpr int L = decltype(layout)::v, VEC = L == kWide ? 8 : 1;
+    constexpr bool SHIFT = L == kShifted;
     const int D = g.D;
+    // few rows: a block each, with nothing to fill a ring with (16 rows of 5120: 2.6 us, 7.3 through the ring)
+    if (L != kSingle && D > (SHIFT ? kSingleForward : kWarpColumns) && g.T > 2 * device_sm_count()) {
+      int stages;
+      const Shape sh = ring_shape(D, SHIFT, forward_threads(SHIFT), (int64_t)8 * weight_floats<SHIFT>(D),
+                                  slot_bytes<T>(D, SHIFT), &stages);
+      if (stages) return forward_ring<T, SHIFT>(g, sh, stages, s);
+    }
     if constexpr (VEC == 8) {
       if (D <= 8 * 32) return forward<T, W, VEC, 8, 256>(g, shape(D, 8, 256), s);
       if (D <= kWarpColumns) return forward<T, W, VEC, 16, 256>(g, shape(D, 16, 256), s);
-      // few rows: a block each, with nothing to fill a ring with (16 rows of 5120: 2.7 us, 7.3 through the ring)
-      if (g.T <= 2 * device_sm_count()) return forward<T, W, VEC, 32, 512>(g, shape(D, 32, 1), s);
-      int stages;
-      const Shape sh = ring_shape(D, kForwardThreads, (int64_t)8 * D, (int64_t)D * sizeof(T), &stages);
-      if (stages) return forward_ring<T, kForwardThreads>(g, sh, stages, s);
-      return forward<T, W, VEC, 32, 512>(g, sh, s);
+      return forward<T, W, VEC, 32, 512>(g, shape(D, 32, 1), s);
     } else {
-      if (D <= 8 * 256) return forward<T, W, VEC, 8, 256>(g, shape(D, 8, 256), s);
+      if (D <= kSingleForward) return forward<T, W, VEC, 8, 256>(g, shape(D, 8, 256), s);
       if (D <= 16 * 512) return forward<T, W, VEC, 16, 512>(g, shape(D, 16, 512), s);
       return forward<T, W, VEC, 32, 512>(g, shape(D, 32, 512), s);
     }
@@ -791,20 +941,24 @@ size_t layer_norm_backward_workspace_bytes(int T, int D) {
 cudaError_t launch_layer_norm_backward(const NormArgs& g, cudaStream_t s) {
   int blocks = 0;
   if (g.T > 0) {
-    cudaError_t e = by_types(g, [&](auto x, auto w, auto vec) {
+    cudaError_t e = by_types(g, [&](auto x, auto w, auto layout) {
       using T = decltype(x);
       using W = decltype(w);
-      constexpr int VEC = decltype(vec)::v;
+      constexpr int L = decltype(layout)::v, VEC = L == kWide ? 8 : 1;
+      constexpr bool SHIFT = L == kShifted;
       const int D = g.D;
+      if (L != kSingle && D > (SHIFT ? kSingleBackward : kWarpColumns)) {
+        int stages;
+        const Shape sh = ring_shape(D, SHIFT, backward_threads(SHIFT), (int64_t)4 * weight_floats<SHIFT>(D),
+                                    2 * slot_bytes<T>(D, SHIFT), &stages);
+        if (stages) return backward_ring<T, SHIFT>(g, sh, stages, &blocks, s);
+      }
       if constexpr (VEC == 8) {
         if (D <= 8 * 32) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
         if (D <= kWarpColumns) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
-        int stages;
-        const Shape sh = ring_shape(D, kBackwardThreads, (int64_t)4 * D, (int64_t)2 * D * sizeof(T), &stages);
-        if (stages) return backward_ring<T>(g, sh, stages, &blocks, s);
-        return backward<T, W, VEC, 32, 512>(g, sh, &blocks, s);
+        return backward<T, W, VEC, 32, 512>(g, shape(D, 32, 1), &blocks, s);
       } else {
-        if (D <= 8 * 320) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
+        if (D <= kSingleBackward) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
         if (D <= 16 * 320) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
         return backward<T, W, VEC, 16, 1024>(g, shape(D, 16, 1), &blocks, s);
       }

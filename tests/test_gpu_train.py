@@ -154,6 +154,58 @@ def test_layer_norm_strided_rows_and_valid_tokens(dtype):
     assert mb.device_error() == 0
 
 
+# rows that start inside 16 bytes: widths on both sides of the pieces', one row a group to many
+ODD_ROWS = [(305, 513), (1217, 519), (2000, 521), (310, 1001), (900, 2051), (2000, 2055), (700, 2601), (1300, 4097),
+            (306, 5121), (305, 16383)]
+
+
+@pytest.mark.parametrize("T,D", ODD_ROWS)
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+def test_layer_norm_many_odd_rows(T, D, dtype, wdtype):
+    test_layer_norm(T, D, dtype, wdtype)
+    test_layer_norm_backward(T, D, dtype, wdtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D,gap,valid", [(640, 1003, 0, 640), (640, 1003, 8, 640), (1300, 515, 40, 1299),
+                                           (1300, 2050, 8, 700), (1300, 2602, 8, 700), (400, 4097, 16, 0),
+                                           (311, 777, 3, 310)])
+def test_layer_norm_odd_rows_stay_in_their_memory(T, D, gap, valid, dtype):
+    """Rows with gaps and NaN around them, outputs in the middle of a larger buffer that keeps its bytes."""
+    mb = _mb()
+    g = ref.gen(T + D + gap)
+    wide = torch.full((T + 2, D + gap), float("nan")).to(dtype)
+    wide[1:-1, :D] = torch.randn(T, D, generator=g).to(dtype)
+    wide[1 + valid:] = float("nan")
+    flat = torch.full((8 + T * (D + gap) + 8,), float("nan")).to(dtype)
+    flat[8:-8] = wide[1:-1].reshape(-1)
+    fc = flat.cuda()
+    xc = fc[8:-8].view(T, D + gap)[:, :D]
+    x = wide[1:1 + valid, :D]
+    gamma, beta = torch.randn(D, generator=g), torch.randn(D, generator=g)
+    dy = torch.full((8 + T * D + 8,), float("inf")).to(dtype)
+    dy[8:8 + valid * D] = torch.randn(valid * D, generator=g).to(dtype)
+    dyc, dy = dy.cuda()[8:-8].view(T, D), dy[8:8 + valid * D].view(valid, D)
+    ys, dxs = sentinel_like((16 + T * D,), dtype), sentinel_like((16 + T * D,), dtype)
+    y, dx = ys[8:-8].view(T, D), dxs[8:-8].view(T, D)
+    _, m, r = mb.moe_layer_norm(xc, gamma.cuda(), beta.cuda(), _i32(valid), out=y)
+    want, mean, rstd = ref.layer_norm(x, gamma, beta, 1e-5)
+    _close(y[:valid], want, _norm_bound(x, gamma, beta, mean, rstd, dtype, want), "y")
+    _, dgamma, dbeta = mb.moe_layer_norm_backward(dyc, xc, gamma.cuda(), m, r, _i32(valid), out=dx)
+    for buf in (ys, dxs):
+        assert is_sentinel(buf[:8]) and is_sentinel(buf[8 + valid * D:])
+    wdx, wg, wb = ref.layer_norm_backward(dy, x, gamma, mean, rstd)
+    xh = ((x.double() - mean[:, None]) * rstd[:, None]).abs()
+    gg = (dy.double() * gamma.double()).abs()
+    # the kernel's own mean and rstd: their errors enter xh
+    err = 4 * ROW * rstd[:, None] * (gg + gg.mean(1, keepdim=True) + (2 * xh + 1) * (gg * (xh + 1)).mean(1, keepdim=True))
+    _close(dx[:valid], wdx, _step(wdx, dtype) + err, "dx")
+    n = (T + 64) * 2.0 ** -24 + ROW
+    _close(dgamma, wg, n * (dy.double().abs() * (xh + 1)).sum(0) + 1e-30, "dgamma")
+    _close(dbeta, wb, n * dy.double().abs().sum(0) + 1e-30, "dbeta")
+    assert mb.device_error() == 0
+
+
 def test_layer_norm_empty_constant_and_non_finite_rows():
     mb = _mb()
     gamma, beta = torch.full((48,), 2.0).cuda(), torch.full((48,), 0.5).cuda()
