@@ -1,18 +1,24 @@
 // The router's load-balance loss, per-expert counts and its gradient
 // (include/moe_train.h).
 //
-// LANES lanes of a warp own a token, V neighbouring experts each (4 in 4 lanes for 16
-// experts up to 32 in 32 for 1024), so a lane's experts stay the same from token to token
-// and their sums of p and counts stay in registers.  Blocks leave partial sums; one block
-// adds them in order.  A batch that one block gets through is a single launch.
+// LANES lanes of a warp own a token, V experts each (4 in 4 lanes for 16 experts up to 32 in
+// 32 for 1024), so a lane's experts stay the same from token to token and their sums of p
+// and counts stay in registers.  Blocks leave partial sums; one block adds them in order.
+// A batch that one block gets through is a single launch.
 //
-// The top_k largest of a token: each lane sorts its values, and top_k rounds take the
-// largest of the lanes' heads, whose lanes move on; the last one taken is the threshold.
-// Of bf16 inputs the key carries the expert below the value, so that keys differ and ties
-// fall to the lower expert; fp32 inputs that tie across lanes are noticed by the count
-// above the threshold and selected again one by one.  The rounds bind the forward, not
-// memory: looking for the next smaller value of each lane's four in every round, 65536
-// tokens of 128 experts in fp32, top 8, took 33.6 us, with the integer pipe 75% busy.
+// The top_k largest of a token: up to 8 from 8 or more values a lane come from sorted lists of
+// 8 that are merged in a lane and across lanes (largest_8).  Otherwise each lane sorts its
+// values, and top_k rounds take the largest of the lanes' heads, whose lanes move on.  The
+// last one is the threshold.  Of bf16 inputs the key carries the expert below the value, so
+// that keys differ and ties fall to the lower expert; fp32 inputs that tie are noticed by
+// the count above the threshold and selected again one by one.
+//
+// The selection binds the forward, not memory.  65536 tokens of 128 experts in fp32, top 8:
+// 33.6 us looking for the next smaller value in every round, 28.3 with sorted lanes, 25.4 with
+// merged lists, 23.0 without a test of each expert against E, 19.9 with the next token's
+// values loaded under this one's work; the integer pipe is then the busiest.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "train_launch.h"
@@ -22,6 +28,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kMaxWarps = 32;
+constexpr int warps_of(int V) { return V <= 8 ? kMaxWarps : V <= 16 ? 16 : 8; }  // of a forward block
 constexpr int kOneBlockTurns = 4;  // turns of a block's tokens up to which it does a batch alone
 
 // How the selection is made: the counts are given, or by keys of bf16 or fp32 inputs.
@@ -64,42 +71,68 @@ __device__ __forceinline__ int group_count(int v) {
   }
 }
 
-// A lane's V values of token t from expert e0 on (0 past E).  wide: its experts are whole
-// 8- or 16-byte pieces of a dense row.
-template <int V>
-__device__ __forceinline__ void load_values(const BalanceArgs& g, int64_t t, int e0, bool wide, float* a) {
+// The expert of a lane's value i; e0: that of value 0.  A lane has 4 neighbouring experts of
+// every 4 LANES, so that neighbouring lanes read neighbouring pieces of a row.
+template <int LANES>
+__device__ __forceinline__ int expert(int e0, int i) {
+  return e0 + i % 4 + i / 4 * (4 * LANES);
+}
+
+// A lane's V values of token t as they lie in memory: nothing waits for them before
+// values_of.  wide: they are whole 8- or 16-byte pieces of a dense row.
+// Past E, and where the token is not live: -inf, whose weight is 0 and whose key is the least
+// (a NaN's is the largest), so that such values are chosen after all others, by ties
+// going to the lower expert.
+constexpr uint32_t kMinusInf = 0xff800000u, kMinusInf2 = 0xff80ff80u;
+template <int V, int LANES>
+__device__ __forceinline__ void load_raw(const BalanceArgs& g, int dtype, int64_t t, bool live, int e0, bool wide,
+                                         uint32_t* raw) {
+  const int E = live ? g.E : 0;
   if (wide) {
-    if (e0 >= g.E) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) a[i] = 0.0f;
-    } else if (g.dtype == MOE_DTYPE_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g.scores) + t * g.stride_t + e0);
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 v = __ldg(p + i);
-        a[4 * i] = v.x;
-        a[4 * i + 1] = v.y;
-        a[4 * i + 2] = v.z;
-        a[4 * i + 3] = v.w;
-      }
-    } else {
-      const uint2* p =
-          reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g.scores) + t * g.stride_t + e0);
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const uint2 v = __ldg(p + i);
-        const float2 lo = bf16x2_bits_to_f32(v.x), hi = bf16x2_bits_to_f32(v.y);
-        a[4 * i] = lo.x;
-        a[4 * i + 1] = lo.y;
-        a[4 * i + 2] = hi.x;
-        a[4 * i + 3] = hi.y;
+    for (int i = 0; i < V; i += 4) {
+      const int64_t at = t * g.stride_t + expert<LANES>(e0, i);
+      const bool in = expert<LANES>(e0, i) < E;
+      if (dtype == MOE_DTYPE_F32) {
+        uint4 v = make_uint4(kMinusInf, kMinusInf, kMinusInf, kMinusInf);
+        if (in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(g.scores) + at));
+        raw[i] = v.x;
+        raw[i + 1] = v.y;
+        raw[i + 2] = v.z;
+        raw[i + 3] = v.w;
+      } else {
+        uint2 v = make_uint2(kMinusInf2, kMinusInf2);
+        if (in) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g.scores) + at));
+        raw[i] = v.x;
+        raw[i + 1] = v.y;
       }
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    a[i] = e0 + i < g.E ? load_score(g.scores, g.dtype, t * g.stride_t + (e0 + i) * g.stride_e) : 0.0f;
+  for (int i = 0; i < V; ++i) {
+    const int e = expert<LANES>(e0, i);
+    const int64_t at = t * g.stride_t + e * g.stride_e;
+    if (dtype == MOE_DTYPE_F32) raw[i] = e < E ? __ldg(static_cast<const uint32_t*>(g.scores) + at) : kMinusInf;
+    else raw[i] = e < E ? __ldg(static_cast<const uint16_t*>(g.scores) + at) : kMinusInf2;
+  }
+}
+template <int V>
+__device__ __forceinline__ void values_of(const uint32_t* raw, int dtype, bool wide, float* a) {
+  if (dtype == MOE_DTYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = __uint_as_float(raw[i]);
+  } else if (wide) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = bf16x2_bits_to_f32(raw[i / 4 * 4 + i % 4 / 2]);
+      a[i] = v.x;
+      a[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = __uint_as_float(raw[i] << 16);
+  }
 }
 
 // sigmoid(a) and 1 - sigmoid(a) = sigmoid(-a), each to full relative precision: from
@@ -108,6 +141,14 @@ __device__ __forceinline__ void sigmoid_both(float a, float* s, float* rest) {
   const float e = __expf(-fabsf(a)), r = __fdividef(1.0f, 1.0f + e), er = e * r;
   *s = a >= 0.0f ? r : er;
   *rest = a >= 0.0f ? er : r;
+}
+
+// 2^x, 0 below the normal numbers: next to the largest weight of a row, which is 1.
+constexpr float kLog2E = 1.44269504088896340736f;
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The order of scores as in routing (route_order_key), -0 folded onto +0 by an addition.
@@ -127,13 +168,14 @@ __device__ __forceinline__ float weights(float* a, float* rest, int kind, int E,
   if (kind == MOE_BALANCE_SOFTMAX) {
     if (top == -INFINITY) top = 0.0f;  // every expert masked: all weights are 0
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = e0 + i < E ? __expf(a[i] - top) : 0.0f;
+    for (int i = 0; i < V; ++i) a[i] = exp2_ftz((a[i] - top) * kLog2E);
   } else if (kind == MOE_BALANCE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      sigmoid_both(a[i], a + i, rest + i);
-      if (e0 + i >= E) a[i] = 0.0f;
-    }
+    for (int i = 0; i < V; ++i) sigmoid_both(a[i], a + i, rest + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert<LANES>(e0, i) >= E) a[i] = 0.0f;
   }
   float s = 0.0f;
 #pragma unroll
@@ -143,11 +185,10 @@ __device__ __forceinline__ float weights(float* a, float* rest, int kind, int E,
 }
 
 template <int V, int LANES>
-__device__ __forceinline__ float largest(const float* a, int E, int e0) {
+__device__ __forceinline__ float largest(const float* a) {
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (e0 + i < E) m = fmaxf(m, a[i]);
+  for (int i = 0; i < V; ++i) m = fmaxf(m, a[i]);
   return group_max<LANES>(m);
 }
 
@@ -169,6 +210,43 @@ __device__ __forceinline__ void sort_descending(uint32_t* k) {
           }
 }
 
+// Of two descending lists of 8, the larger of h[i] and the other's [7 - i] are the 8 largest of
+// both, rising and falling once: this sorts them.
+__device__ __forceinline__ void sort_merged(uint32_t* h) {
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const uint32_t a = h[i], b = h[i + d];
+        h[i] = max(a, b);
+        h[i + d] = min(a, b);
+      }
+}
+// The 8 largest keys of the group's lanes, descending.
+template <int V, int LANES>
+__device__ __forceinline__ void largest_8(const uint32_t* key, uint32_t* h) {
+#pragma unroll
+  for (int b = 0; b < V; b += 8) {
+    uint32_t own[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] = key[b + i];
+    sort_descending<8>(own);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = b ? max(h[i], own[7 - i]) : own[i];
+    if (b) sort_merged(h);
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    uint32_t other[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, h[7 - i], o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = max(h[i], other[i]);
+    sort_merged(h);
+  }
+}
+
 // Adds 1 to the counts cs[V] of the lane's values that are among the token's k largest, where
 // the token is live; *top: the largest value.
 template <int V, int LANES, int SELECT>
@@ -178,11 +256,16 @@ __device__ __forceinline__ void choose(const float* a, int k, int E, int e0, boo
   for (int i = 0; i < V; ++i) {
     key[i] = order_key(a[i]);
     // a bf16 value's order is in the upper half of its key; the lower expert is the larger key
-    if (SELECT == kBf16Keys) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - (e0 + i));
-    if (e0 + i >= E) key[i] = 0u;
+    if (SELECT == kBf16Keys) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - expert<LANES>(e0, i));
   }
   uint32_t limit = 0u;
-  if constexpr (V <= 16) {
+  if (V >= 8 && k <= 8) {
+    uint32_t h[8];
+    largest_8<V < 8 ? 8 : V, LANES>(key, h);
+    *top = key_value(h[0]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) limit = max(limit, k <= i + 1 ? h[i] : 0u);
+  } else if constexpr (V <= 16) {
     uint32_t head[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) head[i] = key[i];
@@ -206,13 +289,20 @@ __device__ __forceinline__ void choose(const float* a, int k, int E, int e0, boo
       if (r == 0) *top = key_value(limit);
     }
   }
-  limit = max(limit, 1u);  // (0: past E)
+  limit = live ? limit : kAll;
   if (SELECT == kBf16Keys) *top = __uint_as_float(__float_as_uint(*top) & 0xffff0000u);
-  if (SELECT == kF32Keys) {
-    int n = 0;
+  int n = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) n += key[i] >= limit ? 1 : 0;
-    if (__any_sync(kAll, group_count<LANES>(n) != k)) {
+  for (int i = 0; i < V; ++i) {
+    const int in = key[i] >= limit ? 1 : 0;
+    cs[i] += in;
+    n += in;
+  }
+  if (SELECT == kF32Keys) {
+    n = group_count<LANES>(n);
+    if (__any_sync(kAll, live && n != k)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) cs[i] -= key[i] >= limit ? 1 : 0;
       // equal values among them: one at a time, the lowest expert of the largest value
       for (int r = 0; r < k; ++r) {
         uint32_t m = 0u;
@@ -222,21 +312,17 @@ __device__ __forceinline__ void choose(const float* a, int k, int E, int e0, boo
         uint32_t at = kAll;
 #pragma unroll
         for (int i = V - 1; i >= 0; --i)
-          if (key[i] == m && e0 + i < E) at = (uint32_t)(e0 + i);
+          if (key[i] == m && expert<LANES>(e0, i) < E) at = (uint32_t)expert<LANES>(e0, i);
         at = group_min<LANES>(at);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (at == (uint32_t)(e0 + i)) {
+          if (at == (uint32_t)expert<LANES>(e0, i)) {
             key[i] = 0u;
             cs[i] += live ? 1 : 0;
           }
       }
-      return;
     }
   }
-  if (!live) limit = kAll;
-#pragma unroll
-  for (int i = 0; i < V; ++i) cs[i] += key[i] >= limit ? 1 : 0;
 }
 
 // The loss, mean_probs and counts from each expert's sum of p and count: threads e < E hold
@@ -264,13 +350,13 @@ __device__ __forceinline__ void finish(const BalanceArgs& g, int n, int e, float
 
 // partial: [blocks][2][E], p sums and (as int) counts; unused by a single block.
 template <int V, int LANES, int SELECT>
-__global__ void __launch_bounds__(V <= 8 ? 1024 : V <= 16 ? 512 : 256)
+__global__ void __launch_bounds__(32 * warps_of(V))
     balance_kernel(const BalanceArgs g, bool wide, float* partial) {
   extern __shared__ float sh[];  // [warps][E] p sums, then [warps][E] counts
   pdl_launch_dependents();
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
-  const int e0 = (lane & (LANES - 1)) * V;
+  const int e0 = (lane & (LANES - 1)) * 4;
   const int n = read_count(g.valid, g.T, g.err);
   float ps[V];
   int cs[V];
@@ -279,19 +365,23 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : V <= 16 ? 512 : 256)
     ps[i] = 0.0f;
     cs[i] = 0;
   }
+  const int dtype = SELECT == kGiven ? g.dtype : SELECT == kBf16Keys ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
   const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
-  for (int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS; t0 < n; t0 += stride) {
-    const int64_t t = t0 + lane / LANES;
+  int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS, t = t0 + lane / LANES;
+  uint32_t raw[V];
+  load_raw<V, LANES>(g, dtype, t, t < n, e0, wide, raw);
+  for (; t0 < n; t0 += stride, t += stride) {
     const bool live = t < n;
     float a[V], rest[V];
-    load_values<V>(g, live ? t : t0, e0, wide, a);
+    values_of<V>(raw, dtype, wide, a);
+    load_raw<V, LANES>(g, dtype, t + stride, t + stride < n, e0, wide, raw);  // the next token's, under this one's work
     float top = 0.0f;
     if (SELECT != kGiven) choose<V, LANES, SELECT>(a, g.top_k, E, e0, live, cs, &top);
-    else if (g.kind == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a, E, e0);
+    else if (g.kind == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a);
     const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (live) ps[i] += a[i] * inv;  // (a row past the count may hold anything)
+      if (live) ps[i] += a[i] * inv;
   }
   // the warp's groups, then the block's warps, in order
   int* shc = reinterpret_cast<int*>(sh + warps * E);
@@ -302,9 +392,10 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : V <= 16 ? 512 : 256)
       ps[i] += __shfl_xor_sync(kAll, ps[i], o);
       if (SELECT != kGiven) cs[i] += __shfl_xor_sync(kAll, cs[i], o);
     }
-    if (lane < LANES && e0 + i < E) {
-      sh[warp * E + e0 + i] = ps[i];
-      if (SELECT != kGiven) shc[warp * E + e0 + i] = cs[i];
+    const int e = expert<LANES>(e0, i);
+    if (lane < LANES && e < E) {
+      sh[warp * E + e] = ps[i];
+      if (SELECT != kGiven) shc[warp * E + e] = cs[i];
     }
   }
   __syncthreads();
@@ -369,7 +460,7 @@ template <int V, int LANES>
 __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
-  const int e0 = (lane & (LANES - 1)) * V;
+  const int e0 = (lane & (LANES - 1)) * 4;
   const int n = read_count(g.valid, g.T, g.err);
   if (n == 0) return;
   const float w = g.coefficient / n * (g.dloss ? __ldg(g.dloss) : 1.0f);
@@ -378,15 +469,19 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, 
   float f[V];
   const int64_t kt = (int64_t)g.top_k * n;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    f[i] = e0 + i < E ? (float)((int64_t)__ldg(g.counts_in + e0 + i) * E - kt) / (float)kt : 0.0f;
+  for (int i = 0; i < V; ++i) {
+    const int e = expert<LANES>(e0, i);
+    f[i] = e < E ? (float)((int64_t)__ldg(g.counts_in + e) * E - kt) / (float)kt : 0.0f;
+  }
   const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
   for (int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS; t0 < n; t0 += stride) {
     const int64_t t = t0 + lane / LANES;
     const bool live = t < n;
     float a[V], rest[V];
-    load_values<V>(g, live ? t : t0, e0, wide, a);
-    const float top = g.kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a, E, e0) : 0.0f;
+    uint32_t raw[V];
+    load_raw<V, LANES>(g, g.dtype, t, live, e0, wide, raw);
+    values_of<V>(raw, g.dtype, wide, a);
+    const float top = g.kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
     const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
     float q = 0.0f;
 #pragma unroll
@@ -400,27 +495,24 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, 
       if (g.kind == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
     }
     if (!live) continue;
-    const int64_t at = t * E + e0;
     if (wide_out) {
-      if (e0 >= E) continue;
-      if (g.dtype == MOE_DTYPE_F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.dscores) + at);
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          float4 v = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+      for (int i = 0; i < V; i += 4) {
+        if (expert<LANES>(e0, i) >= E) continue;
+        const int64_t at = t * E + expert<LANES>(e0, i);
+        if (g.dtype == MOE_DTYPE_F32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.dscores) + at);
+          float4 v = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
           if (g.accumulate) {
-            const float4 b = o[i];
+            const float4 b = *o;
             v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
           }
-          o[i] = v;
-        }
-      } else {
-        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.dscores) + at);
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          float v[4] = {d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
+          *o = v;
+        } else {
+          uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.dscores) + at);
+          float v[4] = {d[i], d[i + 1], d[i + 2], d[i + 3]};
           if (g.accumulate) {
-            const uint2 b = o[i];
+            const uint2 b = *o;
             const float2 lo = bf16x2_bits_to_f32(b.x), hi = bf16x2_bits_to_f32(b.y);
             v[0] += lo.x;
             v[1] += lo.y;
@@ -428,18 +520,20 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, 
             v[3] += hi.y;
           }
           const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-          o[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          *o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (e0 + i >= E) continue;
+        const int e = expert<LANES>(e0, i);
+        if (e >= E) continue;
+        const int64_t at = t * E + e;
         if (g.dtype == MOE_DTYPE_F32) {
-          float* o = static_cast<float*>(g.dscores) + at + i;
+          float* o = static_cast<float*>(g.dscores) + at;
           *o = g.accumulate ? *o + d[i] : d[i];
         } else {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.dscores) + at + i;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.dscores) + at;
           *o = __float2bfloat16_rn(g.accumulate ? __bfloat162float(*o) + d[i] : d[i]);
         }
       }
@@ -452,64 +546,76 @@ struct Layout {
   static constexpr int V = V_, LANES = LANES_;
 };
 
-// f(Layout) for E experts: 4 a lane while they fit a warp, which keeps small batches short
-// (500 tokens of 128 experts: 6.1 us; 7.7 with 8 in 16 lanes, which takes 27.1 us for 65536
-// against 29.6), then 8 and more in a whole one.
-template <typename F>
-void by_experts(int E, F f) {
+// f(Layout) for E experts.  4 experts a lane keep small batches short and 16 take fewer
+// instructions a token.  fp32, top 8: of 61 experts 4096 tokens take 6.6 us with 4 in 16
+// lanes and 7.8 with 16 in 4, 65536 17.5 and 14.8; of 128 experts 500 tokens 5.8 and 6.9,
+// 65536 21.6 and 19.9; of 32 experts 1024 tokens 5.5 and 9.1, 65536 10.5 and 9.1; of 256
+// experts 1024 tokens 9.1 with 8 in 32 lanes and 7.7 with 16 in 16, 65536 46 and 36.  The
+// gradient has nothing to select: 65536 tokens of 256 experts 30 with 8, 39 with 16.
+constexpr int kManyTokens = 8192;
+template <bool FORWARD, typename F>
+void by_experts(int E, int T, F f) {
+  if constexpr (FORWARD) {
+    if (E > 32 && E <= 128 && T > kManyTokens) return E <= 64 ? f(Layout<16, 4>{}) : f(Layout<16, 8>{});
+  }
   if (E <= 16) f(Layout<4, 4>{});
   else if (E <= 32) f(Layout<4, 8>{});
   else if (E <= 64) f(Layout<4, 16>{});
   else if (E <= 128) f(Layout<4, 32>{});
-  else if (E <= 256) f(Layout<8, 32>{});
+  else if (E <= 256) f(std::conditional_t<FORWARD, Layout<16, 16>, Layout<8, 32>>{});
   else if (E <= 512) f(Layout<16, 32>{});
   else f(Layout<32, 32>{});
 }
 
-int values_of(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
-int lanes_of(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32; }
-int warps_of(int E) { return E <= 256 ? kMaxWarps : E <= 512 ? 16 : 8; }  // of a forward block
-
-// Forward blocks: one while it gets through the tokens in a few turns and has a thread for
-// each expert, which then finishes by itself; else up to one a SM.
-int forward_blocks(int T, int E) {
-  const int64_t turn = (int64_t)warps_of(E) * (32 / lanes_of(E));
-  if (T <= kOneBlockTurns * turn && E <= warps_of(E) * 32) return 1;
-  const int64_t need = (T + turn - 1) / turn;
-  return (int)(need < kNumSmsGB300 ? need : kNumSmsGB300);
+// A forward launch: whether a single block does it all; warps of a block; blocks.
+struct Plan {
+  bool alone;
+  int warps, blocks;
+};
+// One block while it gets through the tokens in a few turns and has a thread for each expert,
+// which then finishes by itself; else up to one a SM.
+Plan plan(int T, int E) {
+  Plan p = {};
+  by_experts<true>(E, T, [&](auto l) {
+    p.warps = warps_of(l.V);
+    const int64_t turn = (int64_t)p.warps * (32 / l.LANES);
+    p.alone = T <= kOneBlockTurns * turn && E <= p.warps * 32;
+    const int64_t need = (T + turn - 1) / turn;
+    p.blocks = p.alone ? 1 : (int)(need < kNumSmsGB300 ? need : kNumSmsGB300);
+  });
+  return p;
 }
-bool finishes_alone(int blocks, int E) { return blocks <= 1 && E <= warps_of(E) * 32; }
 
-// Whether rows of `stride` elements hold each lane's V values as whole aligned pieces.
+// Whether rows of `stride` elements hold experts by fours as whole aligned pieces.
 bool whole_pieces(const void* base, int dtype, int64_t stride, int E) {
   const int piece = dtype == MOE_DTYPE_F32 ? 16 : 8;  // 4 values
-  return E % values_of(E) == 0 && stride % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & (piece - 1)) == 0;
+  return E % 4 == 0 && stride % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & (piece - 1)) == 0;
 }
 
 }  // namespace
 
 size_t balance_loss_workspace_bytes(int T, int E) {
-  const int blocks = forward_blocks(T, E);
-  return finishes_alone(blocks, E) ? 0 : (size_t)blocks * 2 * E * sizeof(float);
+  const Plan p = plan(T, E);
+  return p.alone ? 0 : (size_t)p.blocks * 2 * E * sizeof(float);
 }
 
 cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
-  const int blocks = forward_blocks(g.T, g.E), warps = warps_of(g.E);
-  const size_t smem = (size_t)warps * g.E * 8;  // at most 64 KB
+  const Plan p = plan(g.T, g.E);
+  const size_t smem = (size_t)p.warps * g.E * 8;  // at most 64 KB
   const bool wide = g.stride_e == 1 && whole_pieces(g.scores, g.dtype, g.stride_t, g.E);
   float* partial = static_cast<float*>(g.ws);
   cudaError_t e = cudaSuccess;
-  if (blocks > 0) by_experts(g.E, [&](auto l) {
+  if (p.blocks > 0) by_experts<true>(g.E, g.T, [&](auto l) {
     constexpr int V = decltype(l)::V, LANES = decltype(l)::LANES;
     auto kern = g.counts_in ? balance_kernel<V, LANES, kGiven>
                 : g.dtype == MOE_DTYPE_BF16 ? balance_kernel<V, LANES, kBf16Keys>
                                             : balance_kernel<V, LANES, kF32Keys>;
     if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return;
-    kern<<<blocks, warps * 32, smem, s>>>(g, wide, partial);
+    kern<<<p.blocks, p.warps * 32, smem, s>>>(g, wide, partial);
     e = cudaGetLastError();
   });
-  if (e != cudaSuccess || finishes_alone(blocks, g.E)) return e;
+  if (e != cudaSuccess || p.alone) return e;
   int width = 32;
   while (width < g.E) width *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -519,7 +625,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, balance_finish_kernel, g, (const float*)partial, blocks, width);
+  e = cudaLaunchKernelEx(&cfg, balance_finish_kernel, g, (const float*)partial, p.blocks, width);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -527,8 +633,9 @@ cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
 cudaError_t launch_balance_loss_backward(const BalanceArgs& g, cudaStream_t s) {
   const bool wide = g.stride_e == 1 && whole_pieces(g.scores, g.dtype, g.stride_t, g.E);
   const bool wide_out = whole_pieces(g.dscores, g.dtype, g.E, g.E);
-  const int64_t turn = 8 * (32 / lanes_of(g.E)), b = (g.T + turn - 1) / turn, most = (int64_t)device_sm_count() * 8;
-  by_experts(g.E, [&](auto l) {
+  const int64_t most = (int64_t)device_sm_count() * 8;
+  by_experts<false>(g.E, g.T, [&](auto l) {
+    const int64_t turn = 8 * (32 / l.LANES), b = (g.T + turn - 1) / turn;
     balance_grad_kernel<decltype(l)::V, decltype(l)::LANES>
         <<<(int)(b < most ? b : most), 256, 0, s>>>(g, wide, wide_out);
   });

@@ -301,6 +301,35 @@ def test_balance_loss_strides_valid_counts(kind, dtype):
         _check_balance(mb, a, a.cuda(), kind, k, valid, counts_in=counts)
 
 
+@pytest.mark.parametrize("T,E,k,valid", [(8193, 33, 8, 8193), (9001, 61, 8, 9000), (8200, 128, 9, 8200),
+                                         (12001, 128, 8, 11999), (8300, 100, 1, 8299)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_balance_loss_of_many_tokens(T, E, k, valid, kind, dtype):
+    """Every third row of few different values, so that equal ones straddle the choice; masked experts
+    in every fifth; NaN past the count."""
+    mb = _mb()
+    a = _router(T, E, kind, dtype, seed=6)
+    a[::3] = (a[::3] * 4).round() / 4
+    a[::5, E - 3:] = 0 if kind == "scores" else float("-inf")
+    a[valid:] = float("nan")
+    _check_balance(mb, a, a.cuda(), kind, k, valid)
+    wide = torch.full((T, E + 3), float("nan")).to(dtype)
+    wide[:, 1:1 + E] = a
+    _check_balance(mb, a, wide.cuda()[:, 1:1 + E], kind, k, valid)
+
+
+@pytest.mark.parametrize("T,E,k", [(700, 256, 8), (700, 255, 7), (300, 512, 8), (200, 700, 5), (100, 1024, 8),
+                                   (64, 1024, 9)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_balance_counts_of_equal_scores(T, E, k, dtype):
+    mb = _mb()
+    a = (_router(T, E, "softmax", F32, seed=12) * 2).round().to(dtype)
+    a[7] = float("-inf")
+    a[9, 5:] = float("-inf")
+    _check_balance(mb, a, a.cuda(), "softmax", k, T)
+
+
 def test_balance_counts_are_the_routers():
     mb = _mb()
     for T, E, k in ((513, 128, 8), (64, 8, 1), (4096, 16, 2)):
