@@ -117,6 +117,7 @@ def _ptr(t):
 
 # The current stream's handle without a Stream object around it, which costs a call 2.6 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None):
@@ -124,7 +125,7 @@ def _stream(stream=None):
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -138,7 +139,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
     """dtype, device and layout checks of a matrix argument: the C ABI reads it as a
     dense row-major array (contiguous=False: only the last dimension must be dense)."""
-    if t.dtype == dtype and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -590,6 +591,8 @@ def _output(t, shape, dtype, device, name: str) -> torch.Tensor:
     """A caller's output tensor, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t
     _need(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
@@ -602,9 +605,9 @@ def _norm_inputs(x, gamma, beta=None) -> int:
         raise ValueError(f"x must be [T, D], got {tuple(x.shape)}")
     _need(x, x.dtype, "x", contiguous=False)
     D = x.shape[1]
-    _output(gamma, (D,), gamma.dtype, x.device, "gamma")
+    _output(gamma, (D,), gamma.dtype, None, "gamma")
     if beta is not None:
-        _output(beta, (D,), gamma.dtype, x.device, "beta")
+        _output(beta, (D,), gamma.dtype, None, "beta")
     return D
 
 
@@ -613,10 +616,10 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
     """Layer norm of x[T, D] (bf16 or fp32, rows of any stride) with gamma, beta [D]: returns
     (y, mean, rstd), mean and rstd [T] in fp32 for the backward pass."""
     D = _norm_inputs(x, gamma, beta)
-    T = x.shape[0]
-    out = _output(out, (T, D), x.dtype, x.device, "out")
-    mean = _output(mean, (T,), torch.float32, x.device, "mean")
-    rstd = _output(rstd, (T,), torch.float32, x.device, "rstd")
+    T, dev = x.shape[0], x.device
+    out = _output(out, (T, D), x.dtype, dev, "out")
+    mean = _output(mean, (T,), torch.float32, dev, "mean")
+    rstd = _output(rstd, (T,), torch.float32, dev, "rstd")
     st = _lib.moe_layer_norm(_ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta), _dtype_code(gamma),
                              eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out), _ptr(mean), _ptr(rstd),
                              _stream(stream))
@@ -637,16 +640,17 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
     """The gradient of moe_layer_norm: returns (dx [T, D], dgamma [D], dbeta [D]), the last two in
     fp32 (dbeta None without with_beta).  residual_grad [T, D] is added to dx before its rounding."""
     D = _norm_inputs(x, gamma)
-    T = x.shape[0]
-    for t, dt, shape, name in ((dy, x.dtype, (T, D), "dy"), (residual_grad, x.dtype, (T, D), "residual_grad"),
-                               (mean, torch.float32, (T,), "mean"), (rstd, torch.float32, (T,), "rstd")):
-        if t is not None:
-            _output(t, shape, dt, x.device, name)
-    out = _output(out, (T, D), x.dtype, x.device, "out")
-    dgamma = _output(dgamma, (D,), torch.float32, x.device, "dgamma")
-    dbeta = _output(dbeta, (D,), torch.float32, x.device, "dbeta") if with_beta else None
+    T, dt, dev = x.shape[0], x.dtype, x.device
+    _output(dy, (T, D), dt, None, "dy")
+    _output(mean, (T,), torch.float32, None, "mean")
+    _output(rstd, (T,), torch.float32, None, "rstd")
+    if residual_grad is not None:
+        _output(residual_grad, (T, D), dt, None, "residual_grad")
+    out = _output(out, (T, D), dt, dev, "out")
+    dgamma = _output(dgamma, (D,), torch.float32, dev, "dgamma")
+    dbeta = _output(dbeta, (D,), torch.float32, dev, "dbeta") if with_beta else None
     if workspace is None:
-        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, D), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, D), dtype=torch.uint8, device=dev)
     st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma),
                                       _dtype_code(gamma), _ptr(mean), _ptr(rstd),
                                       _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(residual_grad),

@@ -281,25 +281,25 @@ __device__ __forceinline__ void stage_weights(float* s, const void* w, int dtype
                                    : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + d));
       s[i + (i >> 5)] = v;
     }
-    return;
-  }
-  for (int c = threadIdx.x; c < D / 8; c += blockDim.x) {
-    float v[8] = {};
-    if (w) {
-      if (dtype == MOE_DTYPE_F32) {
-        Piece<float, 8> p;
-        p.load(static_cast<const float*>(w) + 8 * c);
+  } else {
+    for (int c = threadIdx.x; c < D / 8; c += blockDim.x) {
+      float v[8] = {};
+      if (w) {
+        if (dtype == MOE_DTYPE_F32) {
+          Piece<float, 8> p;
+          p.load(static_cast<const float*>(w) + 8 * c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = p.get(i);
-      } else {
-        Piece<__nv_bfloat16, 8> p;
-        p.load(static_cast<const __nv_bfloat16*>(w) + 8 * c);
+          for (int i = 0; i < 8; ++i) v[i] = p.get(i);
+        } else {
+          Piece<__nv_bfloat16, 8> p;
+          p.load(static_cast<const __nv_bfloat16*>(w) + 8 * c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = p.get(i);
+          for (int i = 0; i < 8; ++i) v[i] = p.get(i);
+        }
       }
+      reinterpret_cast<float4*>(s)[c] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(s + D / 2)[c] = make_float4(v[4], v[5], v[6], v[7]);
     }
-    reinterpret_cast<float4*>(s)[c] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(s + D / 2)[c] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
 // Pairs 0 .. 3 of the 8 weights from column d (SHIFT: -7 .. D - 1; 0 outside the row).
@@ -896,7 +896,8 @@ template <typename T, typename W, int VEC, int N, int THREADS>
 cudaError_t backward(const NormArgs& g, const Shape& sh, int* blocks, cudaStream_t s) {
   auto kern = norm_grad_kernel<T, W, VEC, N, THREADS>;
   const size_t smem = (size_t)sh.groups * 8 * g.D;  // at most 128 KB: one group of 16384 columns
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   *blocks = grad_blocks(g.T, sh, VEC == 1 ? kMaxGradEach : 1);
   kern<<<*blocks, sh.groups * sh.R, smem, s>>>(g, sh.R, 1.0f / g.D, static_cast<float*>(g.ws));
@@ -956,7 +957,9 @@ cudaError_t launch_layer_norm_backward(const NormArgs& g, cudaStream_t s) {
       if constexpr (VEC == 8) {
         if (D <= 8 * 32) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
         if (D <= kWarpColumns) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
-        return backward<T, W, VEC, 32, 512>(g, shape(D, 32, 1), &blocks, s);
+        // fp32 rows of more than 11000 columns (every bf16 row fits the ring)
+        if constexpr (sizeof(T) == 4) return backward<T, W, VEC, 32, 512>(g, shape(D, 32, 1), &blocks, s);
+        return cudaErrorInvalidValue;
       } else {
         if (D <= kSingleBackward) return backward<T, W, VEC, 8, 320>(g, shape(D, 8, 320), &blocks, s);
         if (D <= 16 * 320) return backward<T, W, VEC, 16, 320>(g, shape(D, 16, 320), &blocks, s);
