@@ -357,7 +357,12 @@ __global__ void __launch_bounds__(32 * warps_of(V))
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
   const int e0 = (lane & (LANES - 1)) * 4;
+  const int dtype = SELECT == kGiven ? g.dtype : SELECT == kBf16Keys ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
+  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
+  int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS, t = t0 + lane / LANES;
+  uint32_t raw[V];
   const int n = read_count(g.valid, g.T, g.err);
+  load_raw<V, LANES>(g, dtype, t, t < n, e0, wide, raw);
   float ps[V];
   int cs[V];
 #pragma unroll
@@ -365,11 +370,6 @@ __global__ void __launch_bounds__(32 * warps_of(V))
     ps[i] = 0.0f;
     cs[i] = 0;
   }
-  const int dtype = SELECT == kGiven ? g.dtype : SELECT == kBf16Keys ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
-  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
-  int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS, t = t0 + lane / LANES;
-  uint32_t raw[V];
-  load_raw<V, LANES>(g, dtype, t, t < n, e0, wide, raw);
   for (; t0 < n; t0 += stride, t += stride) {
     const bool live = t < n;
     float a[V], rest[V];
@@ -456,31 +456,38 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
   finish(g, n, part == 0 ? e : E, p, c);
 }
 
+// The gradient's blocks of an SM, all of them resident, with the next tokens' values on their
+// way.  Of 4 values a lane three: 11000 tokens of 128 experts in bf16 take 5.15 us, with four
+// 5.4, with up to eight and nothing on the way 6.6.  Of 8 four: 65536 tokens of 256 in
+// fp32 24.9 us, with three 26.6.
+constexpr int grad_each(int V) { return V <= 4 ? 3 : V <= 8 ? 4 : V <= 16 ? 2 : 1; }
 template <int V, int LANES>
-__global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
+__global__ void __launch_bounds__(256, grad_each(V)) balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
   const int e0 = (lane & (LANES - 1)) * 4;
+  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
+  int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS, t = t0 + lane / LANES;
+  int count[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) count[i] = expert<LANES>(e0, i) < E ? __ldg(g.counts_in + expert<LANES>(e0, i)) : 0;
   const int n = read_count(g.valid, g.T, g.err);
   if (n == 0) return;
+  uint32_t raw[V];
+  load_raw<V, LANES>(g, g.dtype, t, t < n, e0, wide, raw);
   const float w = g.coefficient / n * (g.dloss ? __ldg(g.dloss) : 1.0f);
   // f_e - 1 for f_e: the p of a token add up to 1, so the differences f_e - q are the
   // same, and near balance they keep their digits (c E - k Tv is exact in integers)
   float f[V];
   const int64_t kt = (int64_t)g.top_k * n;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = expert<LANES>(e0, i);
-    f[i] = e < E ? (float)((int64_t)__ldg(g.counts_in + e) * E - kt) / (float)kt : 0.0f;
-  }
-  const int64_t stride = (int64_t)gridDim.x * warps * TOKENS;
-  for (int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * TOKENS; t0 < n; t0 += stride) {
-    const int64_t t = t0 + lane / LANES;
+  for (int i = 0; i < V; ++i)
+    f[i] = expert<LANES>(e0, i) < E ? (float)((int64_t)count[i] * E - kt) / (float)kt : 0.0f;
+  for (; t0 < n; t0 += stride, t += stride) {
     const bool live = t < n;
     float a[V], rest[V];
-    uint32_t raw[V];
-    load_raw<V, LANES>(g, g.dtype, t, live, e0, wide, raw);
     values_of<V>(raw, g.dtype, wide, a);
+    load_raw<V, LANES>(g, g.dtype, t + stride, t + stride < n, e0, wide, raw);
     const float top = g.kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
     const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
     float q = 0.0f;
@@ -551,7 +558,7 @@ struct Layout {
 // lanes and 7.8 with 16 in 4, 65536 17.5 and 14.8; of 128 experts 500 tokens 5.8 and 6.9,
 // 65536 21.6 and 19.9; of 32 experts 1024 tokens 5.5 and 9.1, 65536 10.5 and 9.1; of 256
 // experts 1024 tokens 9.1 with 8 in 32 lanes and 7.7 with 16 in 16, 65536 46 and 36.  The
-// gradient has nothing to select: 65536 tokens of 256 experts 30 with 8, 39 with 16.
+// gradient has nothing to select: 65536 tokens of 256 experts 25 with 8, 39 with 16.
 constexpr int kManyTokens = 8192;
 template <bool FORWARD, typename F>
 void by_experts(int E, int T, F f) {
@@ -633,8 +640,8 @@ cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
 cudaError_t launch_balance_loss_backward(const BalanceArgs& g, cudaStream_t s) {
   const bool wide = g.stride_e == 1 && whole_pieces(g.scores, g.dtype, g.stride_t, g.E);
   const bool wide_out = whole_pieces(g.dscores, g.dtype, g.E, g.E);
-  const int64_t most = (int64_t)device_sm_count() * 8;
   by_experts<false>(g.E, g.T, [&](auto l) {
+    const int64_t most = (int64_t)device_sm_count() * grad_each(l.V);
     const int64_t turn = 8 * (32 / l.LANES), b = (g.T + turn - 1) / turn;
     balance_grad_kernel<decltype(l)::V, decltype(l)::LANES>
         <<<(int)(b < most ? b : most), 256, 0, s>>>(g, wide, wide_out);

@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Rows straight into registers.
 // Blocks of a direct kernel that share an SM's registers: with single columns one row in
-// flight does not hide its loads (5000 rows of 4097 in bf16 took 110 us so).
+// flight does not hide its loads.
 constexpr int direct_blocks(int vec, int threads) { return vec == 1 ? (threads <= 320 ? 3 : 2) : 1; }
 
 template <typename T, typename W, int VEC, int N, int THREADS>
