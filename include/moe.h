@@ -21,6 +21,8 @@
  *   moe_topk_finalize         routing weights applied to the expert outputs
  *   moe_quantize_rows         per-row FP8 quantisation of a weight matrix
  *
+ * moe_train.h adds the operators that training a layer needs.
+ *
  * Conventions (every entry point):
  *  - Pointers are DEVICE pointers unless stated; the caller owns all memory.
  *    No entry point allocates device memory; scratch comes from the caller

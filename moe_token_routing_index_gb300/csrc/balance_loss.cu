@@ -558,7 +558,8 @@ struct Layout {
 // lanes and 7.8 with 16 in 4, 65536 17.5 and 14.8; of 128 experts 500 tokens 5.8 and 6.9,
 // 65536 21.6 and 19.9; of 32 experts 1024 tokens 5.5 and 9.1, 65536 10.5 and 9.1; of 256
 // experts 1024 tokens 9.1 with 8 in 32 lanes and 7.7 with 16 in 16, 65536 46 and 36.  The
-// gradient has nothing to select: 65536 tokens of 256 experts 25 with 8, 39 with 16.
+// gradient has nothing to select: 65536 tokens of 256 experts 30 with 8, 39 with 16
+// (25 with 8 since loads run ahead).
 constexpr int kManyTokens = 8192;
 template <bool FORWARD, typename F>
 void by_experts(int E, int T, F f) {
