@@ -189,10 +189,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 // not loaded: what they leave stale reaches only accumulator rows and columns that are not stored.
 __device__ __forceinline__ int boxes(int cols) { return max(0, min(kBoxes, (cols + kBoxCols - 1) / kBoxCols)); }
 
-// Whether the rows of an expert end inside a step of 16 rows, and the rows of that step to
-// zero.
-__device__ __forceinline__ bool ragged(int rows) { return (rows & 15) != 0; }
-__device__ __forceinline__ int zero_rows(int rows) { return 16 - (rows & 15); }
+// Whether a unit's last block, of `left` rows, ends inside a step of 16, and the rows that
+// are zeroed behind it: 16, in one copy, where they fit the box (a copy costs as much time
+// as it takes to issue, whatever its rows), else to the end of the box.
+__device__ __forceinline__ bool ragged(int left) { return (left & 15) != 0; }
+__device__ __forceinline__ int zero_rows(int left) { return min(16, kBR - left); }
+constexpr int kHeights = 5;  // copies of 1, 2, 4, 8 and 16 rows
+struct ZeroMaps {
+  CUtensorMap rows[kHeights];
+};
 
 // Arrival on the leader's barrier by a warp that has read its accumulator rows (tcgen05.wait::ld):
 // nothing it wrote has to be seen, so no release at cluster scope, whose fence would wait.
@@ -373,8 +378,8 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
 template <bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
-                       const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_zero4,
-                       const __grid_constant__ CUtensorMap map_zero1, const __grid_constant__ CUtensorMap map_part,
+                       const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_part,
+                       const __grid_constant__ ZeroMaps map_zero,
                        const int32_t* __restrict__ counts, const Shape p, int* cut, unsigned int* err) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -534,9 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t dst = sbase + Smem::stage + s * kStageBytes;
-          if (t.rows - r <= kBR && ragged(t.rows)) {
+          if (t.rows - r < kBR && ragged(t.rows - r)) {
             if (leader) {  // the zeros of both CTAs
-              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)(both * zero_rows(t.rows)) * 128);
+              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)(both * zero_rows(t.rows - r)) * 128);
               mbar_arrive(bar_ready(s));
             }
             mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * kBoxBytes);
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c.count == 0) continue;
         const int mine = (s + c.count - 1) % kStages, left = t.rows - (c.blocks - 1) * kBR;
         s = mine + 1 == kStages ? 0 : mine + 1;
-        if (c.first + c.count < c.blocks || !ragged(t.rows)) continue;
+        if (c.first + c.count < c.blocks || !ragged(left)) continue;
         ok = mbar_wait(bar_full(mine), (parity >> mine) & 1u, s_abort);
         if (!ok) break;
         parity ^= 1u << mine;
@@ -599,9 +604,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2 * kBoxes; ++b) {
           if (b < kBoxes ? b >= na : b - kBoxes >= nb) continue;
           // 128-byte lines: the operand's swizzle stays inside them
-          uint32_t at = st + b * kBoxBytes + left * 128, end = at + zero_rows(t.rows) * 128;
-          for (; at + 512 <= end; at += 512) tma_load_2d_pair(at, &map_zero4, ready, 0, p.a_max);
-          for (; at < end; at += 128) tma_load_2d_pair(at, &map_zero1, ready, 0, p.a_max);
+          uint32_t at = st + b * kBoxBytes + left * 128;
+          for (int n = zero_rows(left); n > 0; n &= n - 1) {
+            const int h = __ffs(n) - 1;
+            tma_load_2d_pair(at, &map_zero.rows[h], ready, 0, p.a_max);
+            at += 128 << h;
+          }
         }
       }
       if (!ok) {
@@ -862,15 +870,19 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   p.blocks = !p.part && g.E <= kTwoBlocksMaxE ? 2 : 1;
   int* cut = reinterpret_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(ws + cut_bytes(g.E));
-  CUtensorMap dw, dy, mx, z4, z1, mp;
+  CUtensorMap dw, dy, mx, mp;
+  ZeroMaps zero;
   if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
-  mp = dy = mx = z4 = z1 = dw;  // without rows nothing is loaded, without parts none are stored
+  mp = dy = mx = dw;  // without rows nothing is loaded, without parts none are stored
   if (p.part && !make_dw_map(&mp, parts, (int)most_slots(g.a_max, p.part), g.N, g.K, true))
     return cudaErrorInvalidValue;
   if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
-                      !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR) ||
-                      !make_zero_map(&z4, g.dy, g.a_max, g.N, 4) || !make_zero_map(&z1, g.dy, g.a_max, g.N, 1)))
+                      !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR)))
     return cudaErrorInvalidValue;
+  for (int h = 0; h < kHeights; ++h) {
+    zero.rows[h] = dw;
+    if (g.a_max > 0 && !make_zero_map(&zero.rows[h], g.dy, g.a_max, g.N, 1 << h)) return cudaErrorInvalidValue;
+  }
   const int smem = Smem::bytes_for(p.units, p.part != 0, p.blocks) + 1024;
   auto kern = p.part ? (f32 ? weight_grad_kernel<true, true> : weight_grad_kernel<false, true>)
                      : (f32 ? weight_grad_kernel<true, false> : weight_grad_kernel<false, false>);
@@ -894,7 +906,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   if (pairs < 1) return cudaErrorNotSupported;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, z4, z1, mp, g.counts, p, cut, g.err);
+  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, mp, zero, g.counts, p, cut, g.err);
   if (e != cudaSuccess) return e;
   if (!p.part) return cudaGetLastError();
   const int64_t n4 = (int64_t)g.N * g.K / 4, want = n4 / 32 * g.E, most = 8 * (int64_t)device_sm_count();
