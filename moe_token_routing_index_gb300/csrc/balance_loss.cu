@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
 // fp32 24.9 us, with three 26.6.
 constexpr int grad_each(int V) { return V <= 4 ? 3 : V <= 8 ? 4 : V <= 16 ? 2 : 1; }
 template <int V, int LANES>
-__global__ void __launch_bounds__(256, grad_each(V)) balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
+__global__ void __launch_bounds__(256, grad_each(V))
+    balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
   const int e0 = (lane & (LANES - 1)) * 4;

@@ -664,7 +664,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 constexpr int direct_blocks(int vec, int threads) { return vec == 1 ? (threads <= 320 ? 3 : 2) : 1; }
 
 template <typename T, typename W, int VEC, int N, int THREADS>
-__global__ void __launch_bounds__(THREADS, direct_blocks(VEC, THREADS)) norm_kernel(const NormArgs g, int R, float inv_d) {
+__global__ void __launch_bounds__(THREADS, direct_blocks(VEC, THREADS))
+    norm_kernel(const NormArgs g, int R, float inv_d) {
   __shared__ float2 s_sum[2][2][THREADS / 32];  // by turns, two sums of each warp
   const int groups = blockDim.x / R, group = threadIdx.x / R, gt = threadIdx.x - group * R;
   const int n = read_count(g.valid, g.T, g.err), D = g.D;
@@ -708,7 +709,8 @@ __global__ void __launch_bounds__(THREADS, direct_blocks(VEC, THREADS)) norm_ker
 }
 
 template <typename T, typename W, int VEC, int N, int THREADS>
-__global__ void __launch_bounds__(THREADS, VEC == 1 && THREADS <= 512 ? 2 : 1) norm_grad_kernel(const NormArgs g, int R, float inv_d, float* partial) {
+__global__ void __launch_bounds__(THREADS, VEC == 1 && THREADS <= 512 ? 2 : 1)
+    norm_grad_kernel(const NormArgs g, int R, float inv_d, float* partial) {
   extern __shared__ __align__(128) uint8_t s_mem[];  // the groups' sums
   __shared__ float2 s_sum[2][THREADS / 32];
   pdl_launch_dependents();
@@ -811,7 +813,9 @@ cudaError_t by_types(const NormArgs& g, F f) {
   const bool xf = g.dtype == MOE_DTYPE_F32, wf = g.weight_dtype == MOE_DTYPE_F32;
   const Layout layout = layout_of(g);
   auto with_layout = [&](auto x, auto w) {
-    return layout == kWide ? f(x, w, Int<kWide>{}) : layout == kShifted ? f(x, w, Int<kShifted>{}) : f(x, w, Int<kSingle>{});
+    return layout == kWide      ? f(x, w, Int<kWide>{})
+           : layout == kShifted ? f(x, w, Int<kShifted>{})
+                                : f(x, w, Int<kSingle>{});
   };
   if (xf) return wf ? with_layout(float{}, float{}) : with_layout(float{}, __nv_bfloat16{});
   return wf ? with_layout(__nv_bfloat16{}, float{}) : with_layout(__nv_bfloat16{}, __nv_bfloat16{});

@@ -2,15 +2,18 @@
 // 5th-generation tensor cores.
 //
 // Both operands are row-major with the reduction (the expert's rows) as their outer
-// dimension, so a TMA box of 64 rows x 128 bytes lands in shared memory as an
+// dimension, so a TMA box of 96 rows x 128 bytes lands in shared memory as an
 // MN-major, 128B-swizzled operand and nothing is transposed.
 //
 // A cluster of two CTAs (two SMs) computes one tile of 256 columns of dY x 256 columns of
 // X of an expert with tcgen05.mma.cta_group::2: CTA r loads 128 columns of each operand,
 // the MMAs of the leader (rank 0) read both CTAs' shared memory, and each CTA's tensor
 // memory receives its 128 rows of the tile.  Persistent, 7 warps per CTA:
-//   warp 0     TMA producer: 64 rows of this CTA's columns per stage (16 + 16 KB) into a
-//              6-stage ring guarded by mbarriers.
+//   warp 0     TMA producer: 96 rows of this CTA's columns per stage (24 + 24 KB) into a
+//              4-stage ring guarded by mbarriers.  What a box costs besides its bytes
+//              binds: one expert of 8192 rows, N = K = 8192, takes 611 us (1800 TFLOP/s),
+//              with 6 stages of 64 rows 688, with 12 of 32 1239; 16 of about 512 rows, N = 16384,
+//              K = 5120, 957, 997 and 1656, and 1008 with 3 of 128.
 //              Both CTAs' copies complete on the leader's barrier.  Where an expert's rows
 //              end inside a step of 16, the rest of that step holds rows of the next expert,
 //              or of none, which may be anything: those copies complete on the CTA's own
@@ -49,16 +52,16 @@ using namespace tc;
 
 constexpr int kTile = 256;                // columns of dY and of X of a pair's tile
 constexpr int kHalf = kTile / 2;          // ... that one CTA loads, and rows of the tile it stores
-constexpr int kBR = 64;                   // rows per stage
+constexpr int kBR = 96;                   // rows per stage
 constexpr int kBoxCols = 64, kBoxBytes = kBR * 128;
 constexpr int kBoxes = kHalf / kBoxCols;  // of each operand
-constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 32 KB
-constexpr int kStages = 6, kAccBufs = 2;
+constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 48 KB
+constexpr int kStages = 4, kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kThreads = 224;
 constexpr int kMaxSorted = 384;           // experts (or parts) up to which the rank sort is run
 constexpr int kPairsGB300 = kNumSmsGB300 / 2;
-constexpr int kMinPart = 1024;            // rows
+constexpr int kMinPart = 960;             // rows
 constexpr int kWhole = 0xffff;            // the slot of an expert that is not cut
 constexpr int kEpiBlockBytes = 32 * 128;  // staging block of an epilogue warp: 32 rows x 128 bytes
 // Staging blocks of an epilogue warp: two, which short experts' tiles need to write at 6.3
@@ -195,8 +198,15 @@ __device__ __forceinline__ int boxes(int cols) { return max(0, min(kBoxes, (cols
 __device__ __forceinline__ bool ragged(int left) { return (left & 15) != 0; }
 __device__ __forceinline__ int zero_rows(int left) { return min(16, kBR - left); }
 constexpr int kHeights = 5;  // copies of 1, 2, 4, 8 and 16 rows
-struct ZeroMaps {
-  CUtensorMap rows[kHeights];
+// Of a block that few rows are left for, lower boxes are loaded (w13 of 16 experts from 8-bit
+// rows: 972 us with whole ones, 957).
+constexpr int kLoadHeights = 4;  // 16, 32, 64 and 96 rows
+__host__ __device__ constexpr int load_rows(int h) { return h == 3 ? kBR : 16 << h; }
+__device__ __forceinline__ int load_height(int left) { return left > 64 ? 3 : left > 32 ? 2 : left > 16 ? 1 : 0; }
+struct Maps {
+  CUtensorMap dy[kLoadHeights], x[kLoadHeights];
+  CUtensorMap zero[kHeights];
+  CUtensorMap dw, part;
 };
 
 // Arrival on the leader's barrier by a warp that has read its accumulator rows (tcgen05.wait::ld):
@@ -243,8 +253,8 @@ __device__ __forceinline__ Tile locate(const Shape& p, int tile, const Units& un
 // of the one from the front kChunk blocks follow each time, the time that storing a tile
 // takes, or all that is left when that is no more than twice as many.  Tiles of one length
 // so alternate between the accumulators.  On 128 experts of Zipf-like load, N = 7168,
-// K = 2048, taking whole tiles from the two ends in turn took 990 us.
-constexpr int kChunk = 6;
+// K = 2048, taking whole tiles from the two ends in turn took 990 us, this 976.
+constexpr int kChunk = 4;
 
 struct Schedule {
   int pair, pairs, front, back;  // the next tile of this pair from either end
@@ -377,10 +387,8 @@ __device__ __forceinline__ void store_tile(const Shape& p, const Tile& t, int ro
 // first slot and number of parts.
 template <bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
-                       const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ CUtensorMap map_part,
-                       const __grid_constant__ ZeroMaps map_zero,
-                       const int32_t* __restrict__ counts, const Shape p, int* cut, unsigned int* err) {
+    weight_grad_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ counts, const Shape p, int* cut,
+                       unsigned int* err) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -421,9 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    tma_prefetch_desc(&map_dy);
-    tma_prefetch_desc(&map_x);
-    tma_prefetch_desc(&map_dw);
+    tma_prefetch_desc(&maps.dy[kLoadHeights - 1]);
+    tma_prefetch_desc(&maps.x[kLoadHeights - 1]);
+    tma_prefetch_desc(&maps.dw);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
@@ -539,27 +547,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t dst = sbase + Smem::stage + s * kStageBytes;
-          if (t.rows - r < kBR && ragged(t.rows - r)) {
+          const int left = t.rows - r;
+          const uint32_t bytes = 128u * (uint32_t)load_rows(load_height(left));  // of a box
+          const bool end = left < kBR && ragged(left);
+          uint32_t bar = ready0 + (uint32_t)(s * 8);
+          if (end) {
             if (leader) {  // the zeros of both CTAs
-              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)(both * zero_rows(t.rows - r)) * 128);
+              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)(both * zero_rows(left)) * 128);
               mbar_arrive(bar_ready(s));
             }
-            mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * kBoxBytes);
-            for (int b = 0; b < na; ++b)
-              tma_load_2d(dst + b * kBoxBytes, &map_dy, bar_full(s), n0 + b * kBoxCols, t.row0 + r);
-            for (int b = 0; b < nb; ++b)
-              tma_load_2d(dst + (kBoxes + b) * kBoxBytes, &map_x, bar_full(s), k0 + b * kBoxCols, t.row0 + r);
-          } else {
-            const uint32_t ready = ready0 + (uint32_t)(s * 8);
-            if (leader) {
-              mbar_arrive_expect_tx(bar_ready(s), (uint32_t)both * kBoxBytes);
-              mbar_arrive(bar_ready(s));
-            }
-            for (int b = 0; b < na; ++b)
-              tma_load_2d_pair(dst + b * kBoxBytes, &map_dy, ready, n0 + b * kBoxCols, t.row0 + r);
-            for (int b = 0; b < nb; ++b)
-              tma_load_2d_pair(dst + (kBoxes + b) * kBoxBytes, &map_x, ready, k0 + b * kBoxCols, t.row0 + r);
+            if (na + nb > 0) mbar_arrive_expect_tx(bar_full(s), (uint32_t)(na + nb) * bytes);
+            bar = map_to_rank(bar_full(s), rank);  // this CTA's own
+          } else if (leader) {
+            mbar_arrive_expect_tx(bar_ready(s), (uint32_t)both * bytes);
+            mbar_arrive(bar_ready(s));
           }
+          // (each height's loads by themselves: a map chosen by an index slows all of them)
+          auto load = [&](const CUtensorMap* dy, const CUtensorMap* x) {
+            for (int b = 0; b < na; ++b)
+              tma_load_2d_pair(dst + b * kBoxBytes, dy, bar, n0 + b * kBoxCols, t.row0 + r);
+            for (int b = 0; b < nb; ++b)
+              tma_load_2d_pair(dst + (kBoxes + b) * kBoxBytes, x, bar, k0 + b * kBoxCols, t.row0 + r);
+          };
+          if (left > 64) load(&maps.dy[3], &maps.x[3]);
+          else if (left > 32) load(&maps.dy[2], &maps.x[2]);
+          else if (left > 16) load(&maps.dy[1], &maps.x[1]);
+          else load(&maps.dy[0], &maps.x[0]);
           issued_mask |= 1u << s;
           issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
           if (++s == kStages) {
@@ -596,10 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int mine = (s + c.count - 1) % kStages, left = t.rows - (c.blocks - 1) * kBR;
         s = mine + 1 == kStages ? 0 : mine + 1;
         if (c.first + c.count < c.blocks || !ragged(left)) continue;
+        const int na = boxes(p.N - t.n0 - (int)rank * kHalf), nb = boxes(p.K - t.k0 - (int)rank * kHalf);
+        if (na + nb == 0) continue;  // (else the stage is not used again before its zeros)
         ok = mbar_wait(bar_full(mine), (parity >> mine) & 1u, s_abort);
         if (!ok) break;
         parity ^= 1u << mine;
-        const int na = boxes(p.N - t.n0 - (int)rank * kHalf), nb = boxes(p.K - t.k0 - (int)rank * kHalf);
         const uint32_t st = sbase + Smem::stage + mine * kStageBytes, ready = ready0 + (uint32_t)(mine * 8);
         for (int b = 0; b < 2 * kBoxes; ++b) {
           if (b < kBoxes ? b >= na : b - kBoxes >= nb) continue;
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t at = st + b * kBoxBytes + left * 128;
           for (int n = zero_rows(left); n > 0; n &= n - 1) {
             const int h = __ffs(n) - 1;
-            tma_load_2d_pair(at, &map_zero.rows[h], ready, 0, p.a_max);
+            tma_load_2d_pair(at, &maps.zero[h], ready, 0, p.a_max);
             at += 128 << h;
           }
         }
@@ -690,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = SPLIT ? units.slot[c.t.unit] : kWhole;
       const int expert = SPLIT ? units.owner[c.t.unit] : c.t.unit;
       if (c.t.rows == 0) {
-        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &map_dw, expert, false, [] {});
+        if (!p.accumulate) store_tile<F32>(p, c.t, row, lane, 0, true, stage, &blk, &maps.dw, expert, false, [] {});
         continue;
       }
       if (!warp_wait(bar_tfull(c.acc), (acc_parity >> c.acc) & 1u, s_abort)) {
@@ -707,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(c.acc * 8));
       };
       if (SPLIT && slot != kWhole)
-        store_tile<true>(p, c.t, row, lane, tbase, false, stage, &blk, &map_part, slot, false, release);
+        store_tile<true>(p, c.t, row, lane, tbase, false, stage, &blk, &maps.part, slot, false, release);
       else
-        store_tile<F32>(p, c.t, row, lane, tbase, false, stage, &blk, &map_dw, expert, p.accumulate, release);
+        store_tile<F32>(p, c.t, row, lane, tbase, false, stage, &blk, &maps.dw, expert, p.accumulate, release);
     }
     if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the block exits
   }
@@ -870,18 +884,20 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   p.blocks = !p.part && g.E <= kTwoBlocksMaxE ? 2 : 1;
   int* cut = reinterpret_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(ws + cut_bytes(g.E));
-  CUtensorMap dw, dy, mx, mp;
-  ZeroMaps zero;
-  if (!make_dw_map(&dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
-  mp = dy = mx = dw;  // without rows nothing is loaded, without parts none are stored
-  if (p.part && !make_dw_map(&mp, parts, (int)most_slots(g.a_max, p.part), g.N, g.K, true))
+  Maps maps;
+  if (!make_dw_map(&maps.dw, g.dw, g.E, g.N, g.K, f32)) return cudaErrorInvalidValue;
+  maps.part = maps.dw;  // without parts none are stored, without rows nothing is loaded
+  if (p.part && !make_dw_map(&maps.part, parts, (int)most_slots(g.a_max, p.part), g.N, g.K, true))
     return cudaErrorInvalidValue;
-  if (g.a_max > 0 && (!make_map_sw128(&dy, g.dy, g.a_max, g.N, false, kBR) ||
-                      !make_map_sw128(&mx, x, g.a_max, g.K, false, kBR)))
-    return cudaErrorInvalidValue;
+  for (int h = 0; h < kLoadHeights; ++h) {
+    maps.dy[h] = maps.x[h] = maps.dw;
+    if (g.a_max > 0 && (!make_map_sw128(&maps.dy[h], g.dy, g.a_max, g.N, false, load_rows(h)) ||
+                        !make_map_sw128(&maps.x[h], x, g.a_max, g.K, false, load_rows(h))))
+      return cudaErrorInvalidValue;
+  }
   for (int h = 0; h < kHeights; ++h) {
-    zero.rows[h] = dw;
-    if (g.a_max > 0 && !make_zero_map(&zero.rows[h], g.dy, g.a_max, g.N, 1 << h)) return cudaErrorInvalidValue;
+    maps.zero[h] = maps.dw;
+    if (g.a_max > 0 && !make_zero_map(&maps.zero[h], g.dy, g.a_max, g.N, 1 << h)) return cudaErrorInvalidValue;
   }
   const int smem = Smem::bytes_for(p.units, p.part != 0, p.blocks) + 1024;
   auto kern = p.part ? (f32 ? weight_grad_kernel<true, true> : weight_grad_kernel<false, true>)
@@ -906,7 +922,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& g, cudaStream_t s) {
   if (pairs < 1) return cudaErrorNotSupported;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, dy, mx, dw, mp, zero, g.counts, p, cut, g.err);
+  e = cudaLaunchKernelEx(&cfg, kern, maps, g.counts, p, cut, g.err);
   if (e != cudaSuccess) return e;
   if (!p.part) return cudaGetLastError();
   const int64_t n4 = (int64_t)g.N * g.K / 4, want = n4 / 32 * g.E, most = 8 * (int64_t)device_sm_count();

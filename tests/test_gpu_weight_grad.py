@@ -97,6 +97,27 @@ def test_weight_grad_keeps_experts_apart():
     assert torch.allclose(got[clean].cpu().double(), want[clean], atol=1e-4)
 
 
+@pytest.mark.parametrize("counts", [list(range(1, 200)), [1, 16, 31, 32, 33, 47, 63, 65, 79, 81, 95, 96, 97, 113, 7],
+                                    [3, 5, 190, 2, 191, 4, 192, 6, 193]])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_weight_grad_of_every_length_between_poisoned_rows(counts, odd):
+    """Every other expert's rows are NaN and infinite: wherever the others end, nothing of them comes in."""
+    mb = _mb()
+    dy, x, c = _data(counts, 144, 272, spare=3)
+    clean = torch.zeros(sum(counts) + 3, dtype=torch.bool)
+    row = 0
+    for e, n in enumerate(counts):
+        clean[row:row + n] = e % 2 == odd
+        row += n
+    pdy, px = dy.clone(), x.clone()
+    pdy[~clean], px[~clean] = float("nan"), float("inf")
+    got = mb.moe_grouped_weight_grad(pdy.cuda(), px.cuda(), c, dtype=F32)
+    keep = list(range(odd, len(counts), 2))
+    dy[~clean], x[~clean] = 0, 0
+    _check(got[keep], dy[clean], x[clean], [counts[e] for e in keep])
+    assert mb.device_error() == 0
+
+
 def test_weight_grad_counts_on_the_device():
     """More counts than experts (counts[E] of the router), a negative count, a sum past the rows, no rows."""
     mb = _mb()
