@@ -68,9 +68,10 @@ constexpr int kEpiBlockBytes = 32 * 128;  // staging block of an epilogue warp: 
 // TB/s (6.1 with one); one where the tables of experts or parts want the room.
 constexpr int kTwoBlocksMaxE = 256;
 // Tiles with more rows than this use one block whatever there is: their stores then spread
-// over the products of the next tile.  In bursts they delay its loads: 16 experts of 512
-// rows, N = K = 8192: 800 us with three blocks in flight, 740 us with one.
-constexpr int kBurstRows = 128;
+// over the products of the next tile, whose loads a burst delays.  16 experts of 519
+// rows, N = K = 4096: 198.6 us, 218.7 with both blocks.  64 of 100 rows: 349 us with
+// both, 400 with one.
+constexpr int kBurstRows = 256;
 
 struct Smem {
   static constexpr int stage = 0;
