@@ -1,9 +1,11 @@
 """ctypes binding of libmoe_gb300 (include/moe.h, include/moe_train.h), with the same entry-point names.
 
 Argument marshalling only: tensors become device pointers and sizes, the
-current PyTorch stream becomes the cudaStream_t, and a non-zero status raises
-MoEError.  Output tensors may be passed in (pre-allocated, e.g. to keep rows
-past the valid count untouched) or are allocated here with torch.empty.
+stream given (else PyTorch's current one) becomes the cudaStream_t, and a
+non-zero status raises MoEError.  Output tensors may be passed in (pre-allocated,
+e.g. to keep rows past the valid count untouched) or are allocated here with
+torch.empty, on the stream that the call runs on.  A caller who gives another
+stream orders it after what writes the inputs, and keeps them while it runs.
 Every computation runs in the library's CUDA kernels; loading fails loudly if
 the library has not been built.
 """
@@ -128,6 +130,37 @@ def _stream(stream=None):
     return _raw_stream(_current_device())
 
 
+def _call_on(fn, args: dict):
+    """A wrapper's call with its arguments (its locals() on entry), on the stream among them.
+
+    What the call allocates comes from that stream's memory: the caching allocator reuses a block
+    in the order of the stream it was allocated on, so a workspace of the current stream's would be
+    written while that stream still reads what lay there, and handed out again under the kernel.
+    The caller's stream is recorded on the results, which are used there."""
+    stream = args.pop("stream")
+    if stream.cuda_stream == _stream():
+        return fn(**args)
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = fn(**args)
+    _record(result, caller)
+    return result
+
+
+def _record(result, stream):
+    if isinstance(result, torch.Tensor):
+        result.record_stream(stream)
+    elif isinstance(result, Checkpoint):
+        _record((result.codes, result.exponents), stream)
+    elif isinstance(result, PackedWeights):
+        _record(result.data, stream)
+    elif isinstance(result, dict):
+        _record(tuple(result.values()), stream)
+    elif isinstance(result, tuple):
+        for r in result:
+            _record(r, stream)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return MOE_DTYPE_BF16
@@ -169,6 +202,8 @@ def moe_router_workspace_size(T: int, D: int, E: int) -> int:
 def moe_router_scores(x: torch.Tensor, w_router: torch.Tensor, num_valid_tokens: torch.Tensor | None = None, *,
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """scores[T, E] = bf16(sigmoid(bf16(x @ w_router.T))) for x[T, D] and w_router[E, D] (bf16)."""
+    if stream is not None:
+        return _call_on(moe_router_scores, locals())
     T, D = x.shape
     E = w_router.shape[0]
     _need(x, torch.bfloat16, "x")
@@ -182,7 +217,7 @@ def moe_router_scores(x: torch.Tensor, w_router: torch.Tensor, num_valid_tokens:
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=x.device)
     st = _lib.moe_router_scores(_ptr(x), T, D, _ptr(w_router), E, _ptr(num_valid_tokens), _ptr(out),
-                                _ptr(workspace), workspace.numel(), _stream(stream))
+                                _ptr(workspace), workspace.numel(), _stream())
     _check("moe_router_scores", st)
     return out
 
@@ -198,6 +233,8 @@ def moe_router_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, num_va
                      workspace: torch.Tensor | None = None, stream=None):
     """Router scores and routing in two kernels (the top-k selection in the router's
     epilogue).  Returns (scores[T, E] bf16, the dict of moe_route)."""
+    if stream is not None:
+        return _call_on(moe_router_route, locals())
     T, D = x.shape
     E = w_router.shape[0]
     _need(x, torch.bfloat16, "x")
@@ -225,7 +262,7 @@ def moe_router_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, num_va
     st = _lib.moe_router_route(_ptr(x), T, D, _ptr(w_router), E, top_k, _ptr(num_valid_tokens), _ptr(scores),
                                _ptr(o["counts"]), _ptr(o["expert_offsets"]), _ptr(o["expert_indices"]),
                                _ptr(o["token_indices"]), _ptr(o["inv_rows"]), _ptr(o["topk_weights"]),
-                               _ptr(workspace), workspace.numel(), _stream(stream))
+                               _ptr(workspace), workspace.numel(), _stream())
     _check("moe_router_route", st)
     return scores, o
 
@@ -242,6 +279,8 @@ def moe_route(scores: torch.Tensor, top_k: int, num_valid_tokens: torch.Tensor |
     """Route scores[T, E]; returns dict(counts, expert_offsets, expert_indices,
     token_indices, inv_rows) of int32 device tensors (index arrays of T * top_k),
     plus topk_weights (fp32 [T * top_k], in inv_rows order) when with_weights."""
+    if stream is not None:
+        return _call_on(moe_route, locals())
     T, E = scores.shape
     dev = scores.device
     o = dict(out or {})
@@ -266,7 +305,7 @@ def moe_route(scores: torch.Tensor, top_k: int, num_valid_tokens: torch.Tensor |
     st = _lib.moe_route(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E, top_k,
                         _ptr(num_valid_tokens), _ptr(o["counts"]), _ptr(o["expert_offsets"]),
                         _ptr(o["expert_indices"]), _ptr(o["token_indices"]), _ptr(o["inv_rows"]),
-                        _ptr(o["topk_weights"]), _ptr(workspace), workspace.numel(), _stream(stream))
+                        _ptr(o["topk_weights"]), _ptr(workspace), workspace.numel(), _stream())
     _check("moe_route", st)
     return o
 
@@ -282,6 +321,8 @@ def _scores_args(scores):
 
 def moe_gather_scale(x, token_indices, expert_indices, scores, valid_token_count=None, *, inv_rows=None,
                      top_k: int = 1, out=None, stream=None):
+    if stream is not None:
+        return _call_on(moe_gather_scale, locals())
     T, D = x.shape
     a = token_indices.shape[0]
     _need(x, torch.bfloat16, "x")
@@ -289,13 +330,15 @@ def moe_gather_scale(x, token_indices, expert_indices, scores, valid_token_count
         out = torch.empty(a, D, dtype=x.dtype, device=x.device)
     _need(out, out.dtype, "out")
     st = _lib.moe_gather_scale(_ptr(x), T, D, _ptr(token_indices), _ptr(expert_indices), a, *_scores_args(scores),
-                               _ptr(valid_token_count), _ptr(inv_rows), top_k, _ptr(out), _stream(stream))
+                               _ptr(valid_token_count), _ptr(inv_rows), top_k, _ptr(out), _stream())
     _check("moe_gather_scale", st)
     return out
 
 
 def moe_gather_scale_quant(x, token_indices, expert_indices, scores, scale_ub=None, valid_token_count=None, *,
                            inv_rows=None, top_k: int = 1, out=None, out_scale=None, stream=None):
+    if stream is not None:
+        return _call_on(moe_gather_scale_quant, locals())
     T, D = x.shape
     a = token_indices.shape[0]
     _need(x, torch.bfloat16, "x")
@@ -308,13 +351,15 @@ def moe_gather_scale_quant(x, token_indices, expert_indices, scores, scale_ub=No
     st = _lib.moe_gather_scale_quant(_ptr(x), T, D, _ptr(token_indices), _ptr(expert_indices), a,
                                      *_scores_args(scores),
                                      _ptr(valid_token_count), _ptr(inv_rows), top_k, _ptr(scale_ub), _ptr(out),
-                                     _ptr(out_scale), _stream(stream))
+                                     _ptr(out_scale), _stream())
     _check("moe_gather_scale_quant", st)
     return out, out_scale
 
 
 def moe_quantize_rows(w: torch.Tensor, scale_ub=None, *, out=None, out_scale=None, stream=None):
     """Per-row FP8 quantisation over the last dim of an fp32 tensor."""
+    if stream is not None:
+        return _call_on(moe_quantize_rows, locals())
     _need(w, torch.float32, "w")
     cols = w.shape[-1]
     rows = w.numel() // cols if cols else 0
@@ -324,7 +369,7 @@ def moe_quantize_rows(w: torch.Tensor, scale_ub=None, *, out=None, out_scale=Non
     if out_scale is None:
         out_scale = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
     _need(out_scale, out_scale.dtype, "out_scale")
-    st = _lib.moe_quantize_rows(_ptr(w), rows, cols, _ptr(scale_ub), _ptr(out), _ptr(out_scale), _stream(stream))
+    st = _lib.moe_quantize_rows(_ptr(w), rows, cols, _ptr(scale_ub), _ptr(out), _ptr(out_scale), _stream())
     _check("moe_quantize_rows", st)
     return out, out_scale
 
@@ -360,13 +405,15 @@ def moe_pack_weights_size(E: int, N: int, K: int, dtype: int) -> int:
 
 def moe_pack_weights(w: torch.Tensor, stream=None) -> PackedWeights:
     """Tile-packed copy of w [E, N, K] bf16 or e4m3 (every 128-row x 128-byte box contiguous)."""
+    if stream is not None:
+        return _call_on(moe_pack_weights, locals())
     E, N, K = w.shape
     if w.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise TypeError(f"w must be bf16 or e4m3, got {w.dtype}")
     _need(w, w.dtype, "w")
     dt = MOE_DTYPE_E4M3 if w.dtype == torch.float8_e4m3fn else MOE_DTYPE_BF16
     data = torch.empty(moe_pack_weights_size(E, N, K, dt), dtype=torch.uint8, device=w.device)
-    _check("moe_pack_weights", _lib.moe_pack_weights(_ptr(w), E, N, K, dt, _ptr(data), _stream(stream)))
+    _check("moe_pack_weights", _lib.moe_pack_weights(_ptr(w), E, N, K, dt, _ptr(data), _stream()))
     return PackedWeights(data, (E, N, K), w.dtype)
 
 
@@ -408,6 +455,8 @@ def moe_grouped_gemm(x, w, counts, *, epilogue: int = MOE_EPILOGUE_NONE, out=Non
     With scatter_indices (top_k = 1), routed row r lands in out[scatter_indices[r]].
     With MOE_EPILOGUE_SILU_MUL_QUANT, out receives the bf16 z and the call returns
     (z_out e4m3 [a_max, N/2], z_scale fp32 [a_max]) instead."""
+    if stream is not None:
+        return _call_on(moe_grouped_gemm, locals())
     a_max, K = x.shape
     E, N, K2 = w.shape
     assert K == K2
@@ -416,7 +465,7 @@ def moe_grouped_gemm(x, w, counts, *, epilogue: int = MOE_EPILOGUE_NONE, out=Non
     si, t_out, acc = _scatter_args(scatter_indices, out, accumulate)
     out, z_out, z_scale = _gemm_outputs(x, N, epilogue, out, z_out, z_scale)
     st = _lib.moe_grouped_gemm(_ptr(x), w_ptr, _ptr(counts), E, a_max, N, K, _ptr(out), epilogue, _ptr(si),
-                               t_out, acc, _ptr(scale_ub), _ptr(z_out), _ptr(z_scale), _stream(stream))
+                               t_out, acc, _ptr(scale_ub), _ptr(z_out), _ptr(z_scale), _stream())
     _check("moe_grouped_gemm", st)
     return out if z_out is None else (z_out, z_scale)
 
@@ -426,6 +475,8 @@ def moe_grouped_gemm_fp8_rowwise(x, w, counts, x_scale, w_scale, *, epilogue: in
                                  z_scale=None, stream=None):
     """As moe_grouped_gemm on e4m3 x[a_max, K] and w[E, N, K] with fp32 row scales
     x_scale[a_max] and w_scale[E, N]."""
+    if stream is not None:
+        return _call_on(moe_grouped_gemm_fp8_rowwise, locals())
     a_max, K = x.shape
     E, N, K2 = w.shape
     assert K == K2
@@ -435,7 +486,7 @@ def moe_grouped_gemm_fp8_rowwise(x, w, counts, x_scale, w_scale, *, epilogue: in
     out, z_out, z_scale = _gemm_outputs(x, N, epilogue, out, z_out, z_scale)
     st = _lib.moe_grouped_gemm_fp8_rowwise(_ptr(x), w_ptr, _ptr(counts), _ptr(x_scale), _ptr(w_scale), E, a_max,
                                            N, K, _ptr(out), epilogue, _ptr(si), t_out, acc, _ptr(scale_ub),
-                                           _ptr(z_out), _ptr(z_scale), _stream(stream))
+                                           _ptr(z_out), _ptr(z_scale), _stream())
     _check("moe_grouped_gemm_fp8_rowwise", st)
     return out if z_out is None else (z_out, z_scale)
 
@@ -450,6 +501,8 @@ def moe_expert_mlp(x, w13, w2, counts, *, z=None, out=None, scatter_indices=None
                    workspace=None, stream=None):
     """Both bf16 grouped GEMMs in one launch: z = silu_mul(x w13^T), out = z w2^T per expert
     (with scatter_indices, top_k = 1: row r lands in out[scatter_indices[r]])."""
+    if stream is not None:
+        return _call_on(moe_expert_mlp, locals())
     a_max, D = x.shape
     E, n2, D2 = w13.shape
     H = n2 // 2
@@ -469,7 +522,7 @@ def moe_expert_mlp(x, w13, w2, counts, *, z=None, out=None, scatter_indices=None
     if workspace is None:   # zero on first use; each call leaves it zero
         workspace = torch.zeros(moe_expert_mlp_workspace_size(E), dtype=torch.uint8, device=x.device)
     st = _lib.moe_expert_mlp(_ptr(x), w13_ptr, w2_ptr, _ptr(counts), E, a_max, D, H, _ptr(z), _ptr(out),
-                             _ptr(si), t_out, acc, _ptr(workspace), workspace.numel(), flags, _stream(stream))
+                             _ptr(si), t_out, acc, _ptr(workspace), workspace.numel(), flags, _stream())
     _check("moe_expert_mlp", st)
     return out
 
@@ -478,6 +531,8 @@ def moe_expert_mlp(x, w13, w2, counts, *, z=None, out=None, scatter_indices=None
 
 def moe_silu_mul(y, H: int | None = None, valid_rows=None, *, out=None, stream=None):
     """y[a, 2H] bf16 -> z[a, H] = silu(y[:, :H]) * y[:, H:]."""
+    if stream is not None:
+        return _call_on(moe_silu_mul, locals())
     a, n2 = y.shape
     H = n2 // 2 if H is None else H
     _need(y, torch.bfloat16, "y", contiguous=False)
@@ -485,13 +540,15 @@ def moe_silu_mul(y, H: int | None = None, valid_rows=None, *, out=None, stream=N
         out = torch.empty(a, H, dtype=torch.bfloat16, device=y.device)
     _need(out, out.dtype, "out")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul(_ptr(y), x1, y.stride(0), a, H, _ptr(valid_rows), _ptr(out), _stream(stream))
+    st = _lib.moe_silu_mul(_ptr(y), x1, y.stride(0), a, H, _ptr(valid_rows), _ptr(out), _stream())
     _check("moe_silu_mul", st)
     return out
 
 
 def moe_silu_mul_quant(y, H: int | None = None, scale_ub=None, valid_rows=None, *, out=None, out_scale=None,
                        stream=None):
+    if stream is not None:
+        return _call_on(moe_silu_mul_quant, locals())
     a, n2 = y.shape
     H = n2 // 2 if H is None else H
     _need(y, torch.bfloat16, "y", contiguous=False)
@@ -503,7 +560,7 @@ def moe_silu_mul_quant(y, H: int | None = None, scale_ub=None, valid_rows=None, 
     _need(out_scale, out_scale.dtype, "out_scale")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
     st = _lib.moe_silu_mul_quant(_ptr(y), x1, y.stride(0), a, H, _ptr(valid_rows), _ptr(scale_ub), _ptr(out),
-                                 _ptr(out_scale), _stream(stream))
+                                 _ptr(out_scale), _stream())
     _check("moe_silu_mul_quant", st)
     return out, out_scale
 
@@ -544,6 +601,8 @@ def moe_topk_finalize(rows, expert_weights, expanded_idx_to_permuted_idx, shared
                       valid_token_count=None, *, out=None, stream=None):
     """out[M, D] = bf16(sum_j w[t, j] * rows[idx[t, j]]) (-0 -> +0), plus the shared
     output (one more rounding); rows[n, D] bf16, weights fp32 or bf16 [M, k], idx int32 [M, k]."""
+    if stream is not None:
+        return _call_on(moe_topk_finalize, locals())
     n_rows, D = rows.shape
     M, k = expanded_idx_to_permuted_idx.shape
     _need(rows, torch.bfloat16, "rows")
@@ -555,7 +614,7 @@ def moe_topk_finalize(rows, expert_weights, expanded_idx_to_permuted_idx, shared
     _need(out, out.dtype, "out")
     st = _lib.moe_topk_finalize(_ptr(rows), n_rows, D, _ptr(expert_weights), _dtype_code(expert_weights),
                                 _ptr(expanded_idx_to_permuted_idx), M, k, _ptr(valid_token_count),
-                                _ptr(shared_output), _ptr(out), _stream(stream))
+                                _ptr(shared_output), _ptr(out), _stream())
     _check("moe_topk_finalize", st)
     return out
 
@@ -563,6 +622,8 @@ def moe_topk_finalize(rows, expert_weights, expanded_idx_to_permuted_idx, shared
 def moe_dense_gemm(x, w, valid_rows=None, *, epilogue: int = MOE_EPILOGUE_NONE, out=None, stream=None):
     """y = x[M, K] @ w[N, K]^T (bf16, split-K over a cluster); with the SiLU*mul
     epilogue y[M, N/2] = silu_mul of the two halves."""
+    if stream is not None:
+        return _call_on(moe_dense_gemm, locals())
     M, K = x.shape
     N, K2 = w.shape
     assert K == K2
@@ -574,7 +635,7 @@ def moe_dense_gemm(x, w, valid_rows=None, *, epilogue: int = MOE_EPILOGUE_NONE, 
     if out is None:
         out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, "out")
-    st = _lib.moe_dense_gemm(_ptr(x), M, K, _ptr(w), N, _ptr(valid_rows), _ptr(out), epilogue, _stream(stream))
+    st = _lib.moe_dense_gemm(_ptr(x), M, K, _ptr(w), N, _ptr(valid_rows), _ptr(out), epilogue, _stream())
     _check("moe_dense_gemm", st)
     return out
 
@@ -615,6 +676,8 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
                    stream=None):
     """Layer norm of x[T, D] (bf16 or fp32, rows of any stride) with gamma, beta [D]: returns
     (y, mean, rstd), mean and rstd [T] in fp32 for the backward pass."""
+    if stream is not None:
+        return _call_on(moe_layer_norm, locals())
     D = _norm_inputs(x, gamma, beta)
     T, dev = x.shape[0], x.device
     out = _output(out, (T, D), x.dtype, dev, "out")
@@ -622,7 +685,7 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
     rstd = _output(rstd, (T,), torch.float32, dev, "rstd")
     st = _lib.moe_layer_norm(_ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta), _dtype_code(gamma),
                              eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out), _ptr(mean), _ptr(rstd),
-                             _stream(stream))
+                             _stream())
     _check("moe_layer_norm", st)
     return out, mean, rstd
 
@@ -639,6 +702,8 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
                             dgamma=None, dbeta=None, with_beta: bool = True, workspace=None, stream=None):
     """The gradient of moe_layer_norm: returns (dx [T, D], dgamma [D], dbeta [D]), the last two in
     fp32 (dbeta None without with_beta).  residual_grad [T, D] is added to dx before its rounding."""
+    if stream is not None:
+        return _call_on(moe_layer_norm_backward, locals())
     D = _norm_inputs(x, gamma)
     T, dt, dev = x.shape[0], x.dtype, x.device
     _output(dy, (T, D), dt, None, "dy")
@@ -655,7 +720,7 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
                                       _dtype_code(gamma), _ptr(mean), _ptr(rstd),
                                       _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(residual_grad),
                                       _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
-                                      _stream(stream))
+                                      _stream())
     _check("moe_layer_norm_backward", st)
     return out, dgamma, dbeta
 
@@ -686,6 +751,8 @@ def moe_balance_loss(scores, top_k: int, num_valid_tokens=None, *, kind: int = M
     """Load-balance loss of a top_k router from its output scores[T, E] (bf16 or fp32, any strides):
     returns (loss [1] fp32, counts [E + 1] int32, mean_probs [E] fp32).  counts: those of moe_route for
     the same tokens, when there are some (returned as they are); else the selection is made here."""
+    if stream is not None:
+        return _call_on(moe_balance_loss, locals())
     T, E = _balance_inputs(scores, counts)
     dev = scores.device
     loss = torch.empty(1, dtype=torch.float32, device=dev)
@@ -696,7 +763,7 @@ def moe_balance_loss(scores, top_k: int, num_valid_tokens=None, *, kind: int = M
     st = _lib.moe_balance_loss(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E, top_k,
                                kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(counts),
                                _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace),
-                               0 if workspace is None else workspace.numel(), _stream(stream))
+                               0 if workspace is None else workspace.numel(), _stream())
     _check("moe_balance_loss", st)
     return loss, made if counts is None else counts, mean_probs
 
@@ -705,6 +772,8 @@ def moe_balance_loss_backward(scores, counts, top_k: int, num_valid_tokens=None,
                               coefficient: float = 1.0, dloss=None, out=None, accumulate: bool = False, stream=None):
     """The gradient of moe_balance_loss with respect to scores (same dtype, [T, E]); dloss: fp32 [1] on the
     device (None: 1).  With accumulate it is added to out."""
+    if stream is not None:
+        return _call_on(moe_balance_loss_backward, locals())
     T, E = _balance_inputs(scores, counts)
     if dloss is not None:
         _need(dloss, torch.float32, "dloss")
@@ -713,7 +782,7 @@ def moe_balance_loss_backward(scores, counts, top_k: int, num_valid_tokens=None,
     out = _output(out, (T, E), scores.dtype, scores.device, "out")
     st = _lib.moe_balance_loss_backward(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E,
                                         top_k, kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"),
-                                        _ptr(counts), _ptr(dloss), _ptr(out), int(accumulate), _stream(stream))
+                                        _ptr(counts), _ptr(dloss), _ptr(out), int(accumulate), _stream())
     _check("moe_balance_loss_backward", st)
     return out
 
@@ -761,29 +830,35 @@ def _checkpoint_arg(ck, a: int, W: int, halves: int, device) -> Checkpoint:
 
 def moe_checkpoint_pack(x, valid_rows=None, *, checkpoint=None, stream=None) -> Checkpoint:
     """bf16 rows x[a, W] (any row stride) as an 8-bit checkpoint."""
+    if stream is not None:
+        return _call_on(moe_checkpoint_pack, locals())
     a, W = x.shape
     _need(x, torch.bfloat16, "x", contiguous=False)
     ck = _checkpoint_arg(checkpoint, a, W, 1, x.device)
     st = _lib.moe_checkpoint_pack(_ptr(x), x.stride(0), a, W, _valid_arg(valid_rows, "valid_rows"), _ptr(ck.codes),
-                                  _ptr(ck.exponents), _stream(stream))
+                                  _ptr(ck.exponents), _stream())
     _check("moe_checkpoint_pack", st)
     return ck
 
 
 def moe_checkpoint_unpack(checkpoint: Checkpoint, valid_rows=None, *, out=None, stream=None):
     """The bf16 rows [a, W] that a checkpoint (of one half) holds, exactly."""
+    if stream is not None:
+        return _call_on(moe_checkpoint_unpack, locals())
     a, W = checkpoint.shape
     if checkpoint.halves != 1:
         raise ValueError("a checkpoint in two halves is read by moe_silu_mul_backward")
     out = _output(out, (a, W), torch.bfloat16, checkpoint.device, "out")
     st = _lib.moe_checkpoint_unpack(_ptr(checkpoint.codes), _ptr(checkpoint.exponents), a, W,
-                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _stream(stream))
+                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _stream())
     _check("moe_checkpoint_unpack", st)
     return out
 
 
 def moe_silu_mul_checkpoint(y, H: int | None = None, valid_rows=None, *, out=None, checkpoint=None, stream=None):
     """moe_silu_mul of y[a, 2H] (bf16, any row stride) that keeps y in 8 bits: returns (z [a, H], Checkpoint)."""
+    if stream is not None:
+        return _call_on(moe_silu_mul_checkpoint, locals())
     a, n2 = y.shape
     H = n2 // 2 if H is None else H
     if 2 * H > n2:
@@ -793,7 +868,7 @@ def moe_silu_mul_checkpoint(y, H: int | None = None, valid_rows=None, *, out=Non
     ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, y.device)
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
     st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, y.stride(0), a, H, _valid_arg(valid_rows, "valid_rows"),
-                                      _ptr(out), _ptr(ck.codes), _ptr(ck.exponents), _stream(stream))
+                                      _ptr(out), _ptr(ck.codes), _ptr(ck.exponents), _stream())
     _check("moe_silu_mul_checkpoint", st)
     return out, ck
 
@@ -802,13 +877,15 @@ def moe_silu_mul_backward(checkpoint: Checkpoint, dz, valid_rows=None, *, out=No
                           stream=None):
     """The gradient of silu_mul at a checkpoint's values: returns (dy [a, 2H], z [a, H]), z computed again from
     them for the gradient of w2 (None without with_z)."""
+    if stream is not None:
+        return _call_on(moe_silu_mul_backward, locals())
     a, H = dz.shape
     _need(dz, torch.bfloat16, "dz")
     ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, dz.device)
     out = _output(out, (a, 2 * H), torch.bfloat16, dz.device, "out")
     z = _output(z, (a, H), torch.bfloat16, dz.device, "z") if with_z else None
     st = _lib.moe_silu_mul_backward(_ptr(ck.codes), _ptr(ck.exponents), _ptr(dz), a, H,
-                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _ptr(z), _stream(stream))
+                                    _valid_arg(valid_rows, "valid_rows"), _ptr(out), _ptr(z), _stream())
     _check("moe_silu_mul_backward", st)
     return out, z
 
@@ -827,6 +904,8 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
                             accumulate: bool = False, workspace=None, stream=None):
     """dw[e] = dy_e^T x_e over the rows of each expert: dy[a, N] bf16, x[a, K] bf16 or a Checkpoint,
     counts[>= E] int32 (E: len(counts), or out's) -> dw[E, N, K] bf16 or fp32.  accumulate adds to an fp32 out."""
+    if stream is not None:
+        return _call_on(moe_grouped_weight_grad, locals())
     a_max, N = dy.shape
     _need(dy, torch.bfloat16, "dy")
     _need(counts, torch.int32, "counts")
@@ -853,7 +932,7 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
         workspace = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
     st = _lib.moe_grouped_weight_grad(_ptr(dy), x_ptr, exps, _ptr(counts), E, a_max, N, K, _ptr(out),
                                       _dtype_code(out), int(accumulate), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _stream(stream))
+                                      0 if workspace is None else workspace.numel(), _stream())
     _check("moe_grouped_weight_grad", st)
     return out
 
