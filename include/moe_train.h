@@ -72,7 +72,9 @@ int moe_layer_norm_backward(const void* dy, const void* x, int64_t ldx, int T, i
 /* What the router's output a[t, e] is, and how it becomes a distribution p over experts. */
 #define MOE_BALANCE_SCORES 0  /* scores >= 0 (moe_router_scores): p = a / sum_e a, 0 where the sum is 0 */
 #define MOE_BALANCE_SOFTMAX 1 /* logits: p = softmax(a); a row of -inf alone has p = 0 */
-#define MOE_BALANCE_SIGMOID 2 /* logits: s = sigmoid(a), p = s / sum_e s, 0 where the sum is 0 */
+/* logits: s = sigmoid(a), p = s / sum_e s.  The sum may be far below fp32's least number; a row
+ * whose logits are all below -700 (masked by the type's lowest value or -inf) has p = 0. */
+#define MOE_BALANCE_SIGMOID 2
 
 /*
  * The load-balance loss of a top-k router over the valid tokens t < Tv:

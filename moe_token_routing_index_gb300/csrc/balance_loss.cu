@@ -160,18 +160,59 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// Whether any live group's lanes all say so.
+template <int LANES>
+__device__ __forceinline__ bool any_whole_group(bool in) {
+  if constexpr (LANES == 32) {
+    return __all_sync(kAll, in);
+  } else {
+    uint32_t b = __ballot_sync(kAll, in);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) b &= b >> o;  // bit i: lanes i .. i + 2 o - 1
+    constexpr uint32_t first = LANES == 4 ? 0x11111111u : LANES == 8 ? 0x01010101u : 0x00010001u;
+    return (b & first) != 0;
+  }
+}
+
+// Logits below which a sigmoid is its exponential to fp32, and those of a masked row: the
+// sigmoid of one is 0 in 64 bits, too.
+constexpr float kSmallLogit = -32.0f, kMaskedLogit = -700.0f;
+// Sums of scores whose reciprocal fp32 does not hold, or that it does not hold themselves, are
+// taken of scores times a power of two.
+constexpr float kTinySum = 0x1p-100f, kHugeSum = 0x1p+100f;
+
 // The token's values become unnormalised weights in place (0 past E), rest[V] what each
 // sigmoid lacks to 1; returns 1 / the sum of the weights, or 0.  top: their largest value
-// (softmax only).
-template <int V, int LANES>
-__device__ __forceinline__ float weights(float* a, float* rest, int kind, int E, int e0, float top) {
-  if (kind == MOE_BALANCE_SOFTMAX) {
+// (softmax only).  *scale: what the scores were multiplied by.
+//
+// A row of sigmoids may add up to less than fp32 holds although each expert's share is an
+// ordinary number.  Where all of its logits are below kSmallLogit the weights are so taken
+// relative to the largest one's, which is a softmax.
+template <int V, int LANES, int KIND>
+__device__ __forceinline__ float weights(float* a, float* rest, int E, int e0, float top, bool live, float* scale) {
+  *scale = 1.0f;
+  if (KIND == MOE_BALANCE_SOFTMAX) {
     if (top == -INFINITY) top = 0.0f;  // every expert masked: all weights are 0
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = exp2_ftz((a[i] - top) * kLog2E);
-  } else if (kind == MOE_BALANCE_SIGMOID) {
+  } else if (KIND == MOE_BALANCE_SIGMOID) {
+    float most = a[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sigmoid_both(a[i], a + i, rest + i);
+    for (int i = 1; i < V; ++i) most = fmaxf(most, a[i]);
+    if (any_whole_group<LANES>(live && most < kSmallLogit)) {
+      most = group_max<LANES>(most);
+      const bool small = most < kSmallLogit;
+      if (most < kMaskedLogit) most = 0.0f;  // all weights are 0
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float relative = exp2_ftz((a[i] - most) * kLog2E);
+        sigmoid_both(a[i], a + i, rest + i);
+        if (small) a[i] = relative;  // (and rest is 1)
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sigmoid_both(a[i], a + i, rest + i);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -181,6 +222,14 @@ __device__ __forceinline__ float weights(float* a, float* rest, int kind, int E,
 #pragma unroll
   for (int i = 0; i < V; ++i) s += a[i];
   s = group_sum<LANES>(s);
+  if (KIND == MOE_BALANCE_SCORES && __any_sync(kAll, live && ((s > 0.0f && s < kTinySum) || s > kHugeSum))) {
+    if (s < kTinySum) *scale = kHugeSum;
+    if (s > kHugeSum) *scale = kTinySum;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += a[i] *= *scale;
+    s = group_sum<LANES>(s);
+  }
   return s == 0.0f ? 0.0f : 1.0f / s;
 }
 
@@ -349,7 +398,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& g, int n, int e, float
 }
 
 // partial: [blocks][2][E], p sums and (as int) counts; unused by a single block.
-template <int V, int LANES, int SELECT>
+template <int V, int LANES, int SELECT, int KIND>
 __global__ void __launch_bounds__(32 * warps_of(V))
     balance_kernel(const BalanceArgs g, bool wide, float* partial) {
   extern __shared__ float sh[];  // [warps][E] p sums, then [warps][E] counts
@@ -372,13 +421,13 @@ __global__ void __launch_bounds__(32 * warps_of(V))
   }
   for (; t0 < n; t0 += stride, t += stride) {
     const bool live = t < n;
-    float a[V], rest[V];
+    float a[V], rest[V], scale;
     values_of<V>(raw, dtype, wide, a);
     load_raw<V, LANES>(g, dtype, t + stride, t + stride < n, e0, wide, raw);  // the next token's, under this one's work
     float top = 0.0f;
     if (SELECT != kGiven) choose<V, LANES, SELECT>(a, g.top_k, E, e0, live, cs, &top);
-    else if (g.kind == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a);
-    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
+    else if (KIND == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a);
+    const float inv = weights<V, LANES, KIND>(a, rest, E, e0, top, live, &scale);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (live) ps[i] += a[i] * inv;
@@ -461,7 +510,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
 // 5.4, with up to eight and nothing on the way 6.6.  Of 8 four: 65536 tokens of 256 in
 // fp32 24.9 us, with three 26.6.
 constexpr int grad_each(int V) { return V <= 4 ? 3 : V <= 8 ? 4 : V <= 16 ? 2 : 1; }
-template <int V, int LANES>
+template <int V, int LANES, int KIND>
 __global__ void __launch_bounds__(256, grad_each(V))
     balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
   constexpr int TOKENS = 32 / LANES;
@@ -486,11 +535,11 @@ __global__ void __launch_bounds__(256, grad_each(V))
     f[i] = expert<LANES>(e0, i) < E ? (float)((int64_t)count[i] * E - kt) / (float)kt : 0.0f;
   for (; t0 < n; t0 += stride, t += stride) {
     const bool live = t < n;
-    float a[V], rest[V];
+    float a[V], rest[V], scale;
     values_of<V>(raw, g.dtype, wide, a);
     load_raw<V, LANES>(g, g.dtype, t + stride, t + stride < n, e0, wide, raw);
-    const float top = g.kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
-    const float inv = weights<V, LANES>(a, rest, g.kind, E, e0, top);
+    const float top = KIND == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
+    const float inv = weights<V, LANES, KIND>(a, rest, E, e0, top, live, &scale);
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) q += f[i] * a[i];
@@ -498,9 +547,9 @@ __global__ void __launch_bounds__(256, grad_each(V))
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      d[i] = w * (f[i] - q) * inv;
-      if (g.kind == MOE_BALANCE_SOFTMAX) d[i] *= a[i];
-      if (g.kind == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
+      d[i] = w * (f[i] - q) * inv * scale;
+      if (KIND == MOE_BALANCE_SOFTMAX) d[i] *= a[i];
+      if (KIND == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
     }
     if (!live) continue;
     if (wide_out) {
@@ -576,6 +625,15 @@ void by_experts(int E, int T, F f) {
   else f(Layout<32, 32>{});
 }
 
+// f(kind as a type): a kernel for each, without the others' code (65536 tokens of
+// 128 experts in fp32 from L2, softmax: 19.4 us and 15.7 backward with one for all, 18.7 and 13.7).
+template <typename F>
+auto by_kind(int kind, F f) {
+  return kind == MOE_BALANCE_SOFTMAX   ? f(std::integral_constant<int, MOE_BALANCE_SOFTMAX>{})
+         : kind == MOE_BALANCE_SIGMOID ? f(std::integral_constant<int, MOE_BALANCE_SIGMOID>{})
+                                       : f(std::integral_constant<int, MOE_BALANCE_SCORES>{});
+}
+
 // A forward launch: whether a single block does it all; warps of a block; blocks.
 struct Plan {
   bool alone;
@@ -616,9 +674,12 @@ cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.blocks > 0) by_experts<true>(g.E, g.T, [&](auto l) {
     constexpr int V = decltype(l)::V, LANES = decltype(l)::LANES;
-    auto kern = g.counts_in ? balance_kernel<V, LANES, kGiven>
-                : g.dtype == MOE_DTYPE_BF16 ? balance_kernel<V, LANES, kBf16Keys>
-                                            : balance_kernel<V, LANES, kF32Keys>;
+    auto kern = by_kind(g.kind, [&](auto kind) {
+      constexpr int KIND = decltype(kind)::value;
+      return g.counts_in ? balance_kernel<V, LANES, kGiven, KIND>
+             : g.dtype == MOE_DTYPE_BF16 ? balance_kernel<V, LANES, kBf16Keys, KIND>
+                                         : balance_kernel<V, LANES, kF32Keys, KIND>;
+    });
     if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return;
     kern<<<p.blocks, p.warps * 32, smem, s>>>(g, wide, partial);
@@ -645,8 +706,9 @@ cudaError_t launch_balance_loss_backward(const BalanceArgs& g, cudaStream_t s) {
   by_experts<false>(g.E, g.T, [&](auto l) {
     const int64_t most = (int64_t)device_sm_count() * grad_each(l.V);
     const int64_t turn = 8 * (32 / l.LANES), b = (g.T + turn - 1) / turn;
-    balance_grad_kernel<decltype(l)::V, decltype(l)::LANES>
-        <<<(int)(b < most ? b : most), 256, 0, s>>>(g, wide, wide_out);
+    constexpr int V = decltype(l)::V, LANES = decltype(l)::LANES;
+    auto kern = by_kind(g.kind, [&](auto kind) { return balance_grad_kernel<V, LANES, decltype(kind)::value>; });
+    kern<<<(int)(b < most ? b : most), 256, 0, s>>>(g, wide, wide_out);
   });
   return cudaGetLastError();
 }
