@@ -90,10 +90,10 @@ __device__ int row_count(const CheckpointArgs& g) {
   if (!g.sum_counts) return read_count(g.valid, g.a, g.err);
   __shared__ int s_rows;
   if (threadIdx.x < 32) {
-    int v = 0;
-    for (int e = threadIdx.x; e < g.E; e += 32) v = min(v + max(__ldg(g.sum_counts + e), 0), g.a);
+    int v = 0;  // at most a, as is what is added: neither sum passes 31 bits
+    for (int e = threadIdx.x; e < g.E; e += 32) v += min(max(__ldg(g.sum_counts + e), 0), g.a - v);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = min(v + __shfl_xor_sync(0xffffffffu, v, o), g.a);
+    for (int o = 16; o > 0; o >>= 1) v += min(__shfl_xor_sync(0xffffffffu, v, o), g.a - v);
     if (threadIdx.x == 0) s_rows = v;
   }
   __syncthreads();

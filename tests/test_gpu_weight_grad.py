@@ -178,3 +178,21 @@ def test_weight_grad_python_refusals():
         mb.moe_grouped_weight_grad(dy, x, c, out=torch.zeros(1, 32, 32, dtype=BF16, device="cuda"), accumulate=True)
     with pytest.raises(ValueError):
         mb.moe_grouped_weight_grad(dy, x, c, out=torch.empty(1, 32, 16, dtype=BF16, device="cuda"))
+
+
+@pytest.mark.parametrize("counts,rows", [([10] + [0] * 31 + [2**31 - 1], [10] + [0] * 31 + [30]),
+                                         ([2**31 - 1] * 70, [40] + [0] * 69),
+                                         ([3] * 8 + [2**31 - 1] * 2 + [5] * 60, [3] * 8 + [16] + [0] * 61),
+                                         ([7, -2**31] * 20, [7, 0] * 5 + [5, 0] + [0, 0] * 14)])
+def test_weight_grad_from_a_checkpoint_of_oversized_counts(counts, rows):
+    """Counts are cut where their sum passes the rows, however far it goes, for 8-bit rows as for bf16."""
+    mb = _mb()
+    dy, x, _ = _data([40], 32, 48)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    ck = mb.moe_checkpoint_pack(x.cuda())
+    kept = mb.moe_checkpoint_unpack(ck)
+    ws = torch.full((mb.moe_grouped_weight_grad_workspace_size(len(counts), 40, 32, 48, mb.MOE_DTYPE_E4M3),), 0xFF,
+                    dtype=torch.uint8, device="cuda")                   # what was not unpacked is NaN
+    got = mb.moe_grouped_weight_grad(dy.cuda(), ck, c, dtype=F32, workspace=ws)
+    _check(got, dy, kept.cpu(), rows)
+    assert mb.device_error() == mb.MOE_DEVERR_BAD_COUNT
