@@ -17,6 +17,7 @@ backward a routed row so holds D + 2H bytes (and an exponent per 128 of them) in
     dw2  = do^T z,  dw13 = dy^T x                         moe_grouped_weight_grad (x: the checkpoint)
     dxr  = dy w13                                         moe_grouped_gemm, w13 transposed
     scores: the routed rows' part, plus the balance loss  moe_balance_loss_backward (accumulate)
+    logits again, for the sigmoid's slope                 moe_dense_gemm
     router: dlogits^T n and dlogits router                moe_grouped_weight_grad, moe_dense_gemm
     dn   = sum of score * dxr over a token's rows + ...   moe_topk_finalize
     dx, dgamma, dbeta                                     moe_layer_norm_backward (+ dout)
@@ -109,8 +110,9 @@ class MoETrainBlock:
         dscores = self._score_gradient(s, dxr)
         mb.moe_balance_loss_backward(s.scores, counts, k, valid, coefficient=self.balance, dloss=dloss, out=dscores,
                                      accumulate=True)
-        p = s.scores.float()
-        dlogits = (dscores.float() * p * (1 - p)).to(torch.bfloat16)
+        # the sigmoid's slope from the logits: of a score near 1, bf16 holds little of what it leaves to 1
+        logits = mb.moe_dense_gemm(s.n, self.router, valid).float()
+        dlogits = (dscores.float() * torch.sigmoid(logits) * torch.sigmoid(-logits)).to(torch.bfloat16)
         tokens = valid if valid is not None else torch.full((1,), T, dtype=torch.int32, device=s.x.device)
         drouter = mb.moe_grouped_weight_grad(dlogits, s.n, tokens, E=1)[0]
         through_router = mb.moe_dense_gemm(dlogits, self.router_t, valid)

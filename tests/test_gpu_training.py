@@ -83,3 +83,28 @@ def test_block_refuses_what_does_not_fit():
         MoETrainBlock(2, z(8, 64, 32), z(8, 32, 32), z(8, 32), z(32), z(32))          # 8 experts
     with pytest.raises(ValueError):
         MoETrainBlock(2, z(16, 64, 32), z(16, 32, 64), z(16, 32), z(32), z(32))
+
+
+@pytest.mark.parametrize("at", [4.0, 7.0, -7.0])
+def test_gradients_of_confident_scores(at):
+    """Every expert's logit near `at`, where a score leaves little to 1 or to 0: the router's gradient still
+    follows from what it leaves (logits are bf16: 2^-9 of them, below 2% of such a slope)."""
+    E, D, H, k, T = 16, 256, 64, 2, 96
+    block, p = _block(E, D, H, k, seed=3)
+    u = torch.randn(D, generator=ref.gen(4))
+    p["beta"] = u.to(BF16)
+    p["router"] = (at * u / u.square().sum() + 0.3 * torch.randn(E, D, generator=ref.gen(5)) / D ** 0.5).to(BF16)
+    block.beta.copy_(p["beta"])
+    block.router.copy_(p["router"])
+    block.refresh_weights()
+    x = torch.randn(T, D, generator=ref.gen(1)).to(BF16)
+    dout = torch.randn(T, D, generator=ref.gen(2)).to(BF16)
+    out, saved = block.forward(x.cuda())
+    grads = block.backward(saved, dout.cuda(), torch.tensor([1.5], device="cuda"))
+    r = saved.route
+    chosen = torch.zeros(T, E, dtype=torch.bool)
+    chosen[r["token_indices"].cpu().long(), r["expert_indices"].cpu().long()] = True
+    want, _, g = _reference(x, p, chosen, H, k, 0.5, dout, 1.5)
+    _near(out, want, 0.02, "out")
+    for name in ("router", "w13", "w2", "gamma", "beta", "x"):
+        _near(grads[name], g[name], 0.08, name)
