@@ -180,8 +180,13 @@ def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
         raise TypeError(f"{name} must be a CUDA tensor")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.dim() > 0 and t.stride(-1) != 1:
+    if not contiguous and t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
+
+
+def _row_stride(t: torch.Tensor, columns: int) -> int:
+    """The row stride of t[a, >= columns]; of a single row, whose stride may be any number, that of dense rows."""
+    return t.stride(0) if t.shape[0] > 1 else columns
 
 
 def device_error(stream=None) -> int:
@@ -540,7 +545,7 @@ def moe_silu_mul(y, H: int | None = None, valid_rows=None, *, out=None, stream=N
         out = torch.empty(a, H, dtype=torch.bfloat16, device=y.device)
     _need(out, out.dtype, "out")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul(_ptr(y), x1, y.stride(0), a, H, _ptr(valid_rows), _ptr(out), _stream())
+    st = _lib.moe_silu_mul(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _ptr(valid_rows), _ptr(out), _stream())
     _check("moe_silu_mul", st)
     return out
 
@@ -559,7 +564,7 @@ def moe_silu_mul_quant(y, H: int | None = None, scale_ub=None, valid_rows=None, 
         out_scale = torch.empty(a, dtype=torch.float32, device=y.device)
     _need(out_scale, out_scale.dtype, "out_scale")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul_quant(_ptr(y), x1, y.stride(0), a, H, _ptr(valid_rows), _ptr(scale_ub), _ptr(out),
+    st = _lib.moe_silu_mul_quant(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _ptr(valid_rows), _ptr(scale_ub), _ptr(out),
                                  _ptr(out_scale), _stream())
     _check("moe_silu_mul_quant", st)
     return out, out_scale
@@ -683,9 +688,9 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
     out = _output(out, (T, D), x.dtype, dev, "out")
     mean = _output(mean, (T,), torch.float32, dev, "mean")
     rstd = _output(rstd, (T,), torch.float32, dev, "rstd")
-    st = _lib.moe_layer_norm(_ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta), _dtype_code(gamma),
-                             eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out), _ptr(mean), _ptr(rstd),
-                             _stream())
+    st = _lib.moe_layer_norm(_ptr(x), _row_stride(x, D), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta),
+                             _dtype_code(gamma), eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out),
+                             _ptr(mean), _ptr(rstd), _stream())
     _check("moe_layer_norm", st)
     return out, mean, rstd
 
@@ -716,7 +721,7 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
     dbeta = _output(dbeta, (D,), torch.float32, dev, "dbeta") if with_beta else None
     if workspace is None:
         workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, D), dtype=torch.uint8, device=dev)
-    st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), x.stride(0), T, D, _dtype_code(x), _ptr(gamma),
+    st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), _row_stride(x, D), T, D, _dtype_code(x), _ptr(gamma),
                                       _dtype_code(gamma), _ptr(mean), _ptr(rstd),
                                       _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(residual_grad),
                                       _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
@@ -835,8 +840,8 @@ def moe_checkpoint_pack(x, valid_rows=None, *, checkpoint=None, stream=None) -> 
     a, W = x.shape
     _need(x, torch.bfloat16, "x", contiguous=False)
     ck = _checkpoint_arg(checkpoint, a, W, 1, x.device)
-    st = _lib.moe_checkpoint_pack(_ptr(x), x.stride(0), a, W, _valid_arg(valid_rows, "valid_rows"), _ptr(ck.codes),
-                                  _ptr(ck.exponents), _stream())
+    st = _lib.moe_checkpoint_pack(_ptr(x), _row_stride(x, W), a, W, _valid_arg(valid_rows, "valid_rows"),
+                                  _ptr(ck.codes), _ptr(ck.exponents), _stream())
     _check("moe_checkpoint_pack", st)
     return ck
 
@@ -867,7 +872,7 @@ def moe_silu_mul_checkpoint(y, H: int | None = None, valid_rows=None, *, out=Non
     out = _output(out, (a, H), torch.bfloat16, y.device, "out")
     ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, y.device)
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, y.stride(0), a, H, _valid_arg(valid_rows, "valid_rows"),
+    st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _valid_arg(valid_rows, "valid_rows"),
                                       _ptr(out), _ptr(ck.codes), _ptr(ck.exponents), _stream())
     _check("moe_silu_mul_checkpoint", st)
     return out, ck
