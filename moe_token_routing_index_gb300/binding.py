@@ -171,7 +171,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
     """dtype, device and layout checks of a matrix argument: the C ABI reads it as a
-    dense row-major array (contiguous=False: only the last dimension must be dense)."""
+    dense row-major array (contiguous=False: only the last dimension must be dense; the
+    row stride of a single row, which PyTorch may set to any number, is then not passed on)."""
     if t.dtype is dtype and t.is_cuda and t.is_contiguous():
         return
     if t.dtype != dtype:
@@ -182,11 +183,6 @@ def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
         raise ValueError(f"{name} must be contiguous")
     if not contiguous and t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
-
-
-def _row_stride(t: torch.Tensor, columns: int) -> int:
-    """The row stride of t[a, >= columns]; of a single row, whose stride may be any number, that of dense rows."""
-    return t.stride(0) if t.shape[0] > 1 else columns
 
 
 def device_error(stream=None) -> int:
@@ -545,7 +541,7 @@ def moe_silu_mul(y, H: int | None = None, valid_rows=None, *, out=None, stream=N
         out = torch.empty(a, H, dtype=torch.bfloat16, device=y.device)
     _need(out, out.dtype, "out")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _ptr(valid_rows), _ptr(out), _stream())
+    st = _lib.moe_silu_mul(_ptr(y), x1, y.stride(0) if a > 1 else 2 * H, a, H, _ptr(valid_rows), _ptr(out), _stream())
     _check("moe_silu_mul", st)
     return out
 
@@ -564,8 +560,8 @@ def moe_silu_mul_quant(y, H: int | None = None, scale_ub=None, valid_rows=None, 
         out_scale = torch.empty(a, dtype=torch.float32, device=y.device)
     _need(out_scale, out_scale.dtype, "out_scale")
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul_quant(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _ptr(valid_rows), _ptr(scale_ub), _ptr(out),
-                                 _ptr(out_scale), _stream())
+    st = _lib.moe_silu_mul_quant(_ptr(y), x1, y.stride(0) if a > 1 else 2 * H, a, H, _ptr(valid_rows), _ptr(scale_ub),
+                                 _ptr(out), _ptr(out_scale), _stream())
     _check("moe_silu_mul_quant", st)
     return out, out_scale
 
@@ -647,10 +643,25 @@ def moe_dense_gemm(x, w, valid_rows=None, *, epilogue: int = MOE_EPILOGUE_NONE, 
 
 # ----------------------------------------------------------------- layer norm
 
-def _valid_arg(valid, name: str):
-    if valid is not None:
-        _need(valid, torch.int32, name)
-    return _ptr(valid)
+def _no_value(name: str):
+    raise ValueError(f"{name} must hold a value")
+
+
+def _valid_arg(valid, name: str, dtype=torch.int32):
+    """The pointer of a scalar on the device, or none.  (An empty tensor's is null, which would be read as none.)"""
+    if valid is None:
+        return None
+    _need(valid, dtype, name)
+    return valid.data_ptr() or _no_value(name)
+
+
+def _workspace_bytes(workspace) -> int:
+    """The size of a caller's workspace, which must be device memory."""
+    if not workspace.is_cuda:
+        raise TypeError("the workspace must be a CUDA tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _output(t, shape, dtype, device, name: str) -> torch.Tensor:
@@ -688,7 +699,7 @@ def moe_layer_norm(x, gamma, beta=None, num_valid_tokens=None, *, eps: float = 1
     out = _output(out, (T, D), x.dtype, dev, "out")
     mean = _output(mean, (T,), torch.float32, dev, "mean")
     rstd = _output(rstd, (T,), torch.float32, dev, "rstd")
-    st = _lib.moe_layer_norm(_ptr(x), _row_stride(x, D), T, D, _dtype_code(x), _ptr(gamma), _ptr(beta),
+    st = _lib.moe_layer_norm(_ptr(x), x.stride(0) if T > 1 else D, T, D, _dtype_code(x), _ptr(gamma), _ptr(beta),
                              _dtype_code(gamma), eps, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(out),
                              _ptr(mean), _ptr(rstd), _stream())
     _check("moe_layer_norm", st)
@@ -720,12 +731,14 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, num_valid_tokens=None, *, 
     dgamma = _output(dgamma, (D,), torch.float32, dev, "dgamma")
     dbeta = _output(dbeta, (D,), torch.float32, dev, "dbeta") if with_beta else None
     if workspace is None:
-        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, D), dtype=torch.uint8, device=dev)
-    st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), _row_stride(x, D), T, D, _dtype_code(x), _ptr(gamma),
+        ws_bytes = moe_layer_norm_backward_workspace_size(T, D)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        ws_bytes = _workspace_bytes(workspace)
+    st = _lib.moe_layer_norm_backward(_ptr(dy), _ptr(x), x.stride(0) if T > 1 else D, T, D, _dtype_code(x), _ptr(gamma),
                                       _dtype_code(gamma), _ptr(mean), _ptr(rstd),
                                       _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(residual_grad),
-                                      _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
-                                      _stream())
+                                      _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes, _stream())
     _check("moe_layer_norm_backward", st)
     return out, dgamma, dbeta
 
@@ -763,12 +776,13 @@ def moe_balance_loss(scores, top_k: int, num_valid_tokens=None, *, kind: int = M
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     mean_probs = torch.empty(E, dtype=torch.float32, device=dev)
     made = torch.empty(E + 1, dtype=torch.int32, device=dev) if counts is None else None
-    if workspace is None and (ws_bytes := moe_balance_loss_workspace_size(T, E)):
+    if workspace is not None:
+        ws_bytes = _workspace_bytes(workspace)
+    elif ws_bytes := moe_balance_loss_workspace_size(T, E):
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     st = _lib.moe_balance_loss(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E, top_k,
                                kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"), _ptr(counts),
-                               _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace),
-                               0 if workspace is None else workspace.numel(), _stream())
+                               _ptr(made), _ptr(mean_probs), _ptr(loss), _ptr(workspace), ws_bytes, _stream())
     _check("moe_balance_loss", st)
     return loss, made if counts is None else counts, mean_probs
 
@@ -780,14 +794,13 @@ def moe_balance_loss_backward(scores, counts, top_k: int, num_valid_tokens=None,
     if stream is not None:
         return _call_on(moe_balance_loss_backward, locals())
     T, E = _balance_inputs(scores, counts)
-    if dloss is not None:
-        _need(dloss, torch.float32, "dloss")
     if accumulate and out is None:
         raise ValueError("accumulate adds to a caller-provided out[T, E]")
     out = _output(out, (T, E), scores.dtype, scores.device, "out")
     st = _lib.moe_balance_loss_backward(_ptr(scores), _dtype_code(scores), scores.stride(0), scores.stride(1), T, E,
                                         top_k, kind, coefficient, _valid_arg(num_valid_tokens, "num_valid_tokens"),
-                                        _ptr(counts), _ptr(dloss), _ptr(out), int(accumulate), _stream())
+                                        _ptr(counts), _valid_arg(dloss, "dloss", torch.float32), _ptr(out),
+                                        int(accumulate), _stream())
     _check("moe_balance_loss_backward", st)
     return out
 
@@ -824,9 +837,10 @@ class Checkpoint:
         return self.codes.device
 
 
-def _checkpoint_arg(ck, a: int, W: int, halves: int, device) -> Checkpoint:
-    if ck is None:
-        return Checkpoint.empty(a, W, device, halves)
+def _checkpoint_arg(ck, a: int, W: int, halves: int) -> Checkpoint:
+    """A checkpoint to be read, or a caller's to be written, checked."""
+    if not isinstance(ck, Checkpoint):
+        raise TypeError(f"a Checkpoint is needed, got {type(ck).__name__}")
     if tuple(ck.shape) != (a, W) or ck.halves != halves:
         raise ValueError(f"the checkpoint must hold [{a}, {W}] in {halves} half or halves, "
                          f"got {tuple(ck.shape)} in {ck.halves}")
@@ -839,8 +853,8 @@ def moe_checkpoint_pack(x, valid_rows=None, *, checkpoint=None, stream=None) -> 
         return _call_on(moe_checkpoint_pack, locals())
     a, W = x.shape
     _need(x, torch.bfloat16, "x", contiguous=False)
-    ck = _checkpoint_arg(checkpoint, a, W, 1, x.device)
-    st = _lib.moe_checkpoint_pack(_ptr(x), _row_stride(x, W), a, W, _valid_arg(valid_rows, "valid_rows"),
+    ck = Checkpoint.empty(a, W, x.device) if checkpoint is None else _checkpoint_arg(checkpoint, a, W, 1)
+    st = _lib.moe_checkpoint_pack(_ptr(x), x.stride(0) if a > 1 else W, a, W, _valid_arg(valid_rows, "valid_rows"),
                                   _ptr(ck.codes), _ptr(ck.exponents), _stream())
     _check("moe_checkpoint_pack", st)
     return ck
@@ -850,6 +864,8 @@ def moe_checkpoint_unpack(checkpoint: Checkpoint, valid_rows=None, *, out=None, 
     """The bf16 rows [a, W] that a checkpoint (of one half) holds, exactly."""
     if stream is not None:
         return _call_on(moe_checkpoint_unpack, locals())
+    if not isinstance(checkpoint, Checkpoint):
+        raise TypeError(f"a Checkpoint is needed, got {type(checkpoint).__name__}")
     a, W = checkpoint.shape
     if checkpoint.halves != 1:
         raise ValueError("a checkpoint in two halves is read by moe_silu_mul_backward")
@@ -870,10 +886,11 @@ def moe_silu_mul_checkpoint(y, H: int | None = None, valid_rows=None, *, out=Non
         raise ValueError(f"y must hold two halves of {H} columns, got {n2}")
     _need(y, torch.bfloat16, "y", contiguous=False)
     out = _output(out, (a, H), torch.bfloat16, y.device, "out")
-    ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, y.device)
+    ck = Checkpoint.empty(a, 2 * H, y.device, 2) if checkpoint is None else _checkpoint_arg(checkpoint, a, 2 * H, 2)
     x1 = ctypes.c_void_p(y.data_ptr() + H * y.element_size())
-    st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, _row_stride(y, 2 * H), a, H, _valid_arg(valid_rows, "valid_rows"),
-                                      _ptr(out), _ptr(ck.codes), _ptr(ck.exponents), _stream())
+    st = _lib.moe_silu_mul_checkpoint(_ptr(y), x1, y.stride(0) if a > 1 else 2 * H, a, H,
+                                      _valid_arg(valid_rows, "valid_rows"), _ptr(out), _ptr(ck.codes),
+                                      _ptr(ck.exponents), _stream())
     _check("moe_silu_mul_checkpoint", st)
     return out, ck
 
@@ -886,7 +903,7 @@ def moe_silu_mul_backward(checkpoint: Checkpoint, dz, valid_rows=None, *, out=No
         return _call_on(moe_silu_mul_backward, locals())
     a, H = dz.shape
     _need(dz, torch.bfloat16, "dz")
-    ck = _checkpoint_arg(checkpoint, a, 2 * H, 2, dz.device)
+    ck = _checkpoint_arg(checkpoint, a, 2 * H, 2)
     out = _output(out, (a, 2 * H), torch.bfloat16, dz.device, "out")
     z = _output(z, (a, H), torch.bfloat16, dz.device, "z") if with_z else None
     st = _lib.moe_silu_mul_backward(_ptr(ck.codes), _ptr(ck.exponents), _ptr(dz), a, H,
@@ -932,12 +949,13 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
     if accumulate and out is None:
         raise ValueError("accumulate adds to a caller-provided out[E, N, K]")
     out = _output(out, (E, N, K), dtype if out is None else out.dtype, dy.device, "out")
-    if workspace is None:
-        n = moe_grouped_weight_grad_workspace_size(E, a_max, N, K, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+    if workspace is not None:
+        ws_bytes = _workspace_bytes(workspace)
+    elif ws_bytes := moe_grouped_weight_grad_workspace_size(E, a_max, N, K, code):
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dy.device)
     st = _lib.moe_grouped_weight_grad(_ptr(dy), x_ptr, exps, _ptr(counts), E, a_max, N, K, _ptr(out),
                                       _dtype_code(out), int(accumulate), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _stream())
+                                      ws_bytes, _stream())
     _check("moe_grouped_weight_grad", st)
     return out
 
