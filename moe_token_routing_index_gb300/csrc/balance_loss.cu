@@ -33,6 +33,7 @@ constexpr int kOneBlockTurns = 4;  // turns of a block's tokens up to which it d
 
 // How the selection is made: the counts are given, or by keys of bf16 or fp32 inputs.
 enum Select { kGiven, kBf16Keys, kF32Keys };
+constexpr int kAnyKind = -1;  // of a kernel that takes the kind from its arguments
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -188,14 +189,15 @@ constexpr float kTinySum = 0x1p-100f, kHugeSum = 0x1p+100f;
 // A row of sigmoids may add up to less than fp32 holds although each expert's share is an
 // ordinary number.  Where all of its logits are below kSmallLogit the weights are so taken
 // relative to the largest one's, which is a softmax.
-template <int V, int LANES, int KIND>
-__device__ __forceinline__ float weights(float* a, float* rest, int E, int e0, float top, bool live, float* scale) {
+template <int V, int LANES>
+__device__ __forceinline__ float weights(float* a, float* rest, int kind, int E, int e0, float top, bool live,
+                                         float* scale) {
   *scale = 1.0f;
-  if (KIND == MOE_BALANCE_SOFTMAX) {
+  if (kind == MOE_BALANCE_SOFTMAX) {
     if (top == -INFINITY) top = 0.0f;  // every expert masked: all weights are 0
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = exp2_ftz((a[i] - top) * kLog2E);
-  } else if (KIND == MOE_BALANCE_SIGMOID) {
+  } else if (kind == MOE_BALANCE_SIGMOID) {
     float most = a[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) most = fmaxf(most, a[i]);
@@ -222,7 +224,7 @@ __device__ __forceinline__ float weights(float* a, float* rest, int E, int e0, f
 #pragma unroll
   for (int i = 0; i < V; ++i) s += a[i];
   s = group_sum<LANES>(s);
-  if (KIND == MOE_BALANCE_SCORES && __any_sync(kAll, live && ((s > 0.0f && s < kTinySum) || s > kHugeSum))) {
+  if (kind == MOE_BALANCE_SCORES && __any_sync(kAll, live && ((s > 0.0f && s < kTinySum) || s > kHugeSum))) {
     if (s < kTinySum) *scale = kHugeSum;
     if (s > kHugeSum) *scale = kTinySum;
     s = 0.0f;
@@ -401,6 +403,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& g, int n, int e, float
 template <int V, int LANES, int SELECT, int KIND>
 __global__ void __launch_bounds__(32 * warps_of(V))
     balance_kernel(const BalanceArgs g, bool wide, float* partial) {
+  const int kind = KIND == kAnyKind ? g.kind : KIND;
   extern __shared__ float sh[];  // [warps][E] p sums, then [warps][E] counts
   pdl_launch_dependents();
   constexpr int TOKENS = 32 / LANES;
@@ -426,8 +429,8 @@ __global__ void __launch_bounds__(32 * warps_of(V))
     load_raw<V, LANES>(g, dtype, t + stride, t + stride < n, e0, wide, raw);  // the next token's, under this one's work
     float top = 0.0f;
     if (SELECT != kGiven) choose<V, LANES, SELECT>(a, g.top_k, E, e0, live, cs, &top);
-    else if (KIND == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a);
-    const float inv = weights<V, LANES, KIND>(a, rest, E, e0, top, live, &scale);
+    else if (kind == MOE_BALANCE_SOFTMAX) top = largest<V, LANES>(a);
+    const float inv = weights<V, LANES>(a, rest, kind, E, e0, top, live, &scale);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (live) ps[i] += a[i] * inv;
@@ -513,6 +516,7 @@ constexpr int grad_each(int V) { return V <= 4 ? 3 : V <= 8 ? 4 : V <= 16 ? 2 : 
 template <int V, int LANES, int KIND>
 __global__ void __launch_bounds__(256, grad_each(V))
     balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
+  constexpr int kind = KIND;
   constexpr int TOKENS = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32, E = g.E;
   const int e0 = (lane & (LANES - 1)) * 4;
@@ -538,8 +542,8 @@ __global__ void __launch_bounds__(256, grad_each(V))
     float a[V], rest[V], scale;
     values_of<V>(raw, g.dtype, wide, a);
     load_raw<V, LANES>(g, g.dtype, t + stride, t + stride < n, e0, wide, raw);
-    const float top = KIND == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
-    const float inv = weights<V, LANES, KIND>(a, rest, E, e0, top, live, &scale);
+    const float top = kind == MOE_BALANCE_SOFTMAX ? largest<V, LANES>(a) : 0.0f;
+    const float inv = weights<V, LANES>(a, rest, kind, E, e0, top, live, &scale);
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) q += f[i] * a[i];
@@ -548,8 +552,8 @@ __global__ void __launch_bounds__(256, grad_each(V))
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       d[i] = w * (f[i] - q) * inv * scale;
-      if (KIND == MOE_BALANCE_SOFTMAX) d[i] *= a[i];
-      if (KIND == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
+      if (kind == MOE_BALANCE_SOFTMAX) d[i] *= a[i];
+      if (kind == MOE_BALANCE_SIGMOID) d[i] *= a[i] * rest[i];
     }
     if (!live) continue;
     if (wide_out) {
@@ -625,8 +629,9 @@ void by_experts(int E, int T, F f) {
   else f(Layout<32, 32>{});
 }
 
-// f(kind as a type): a kernel for each, without the others' code (65536 tokens of
-// 128 experts in fp32 from L2, softmax: 19.4 us and 15.7 backward with one for all, 18.7 and 13.7).
+// f(kind as a type): a kernel for each, without the others' code (65536 tokens of 128 experts in
+// fp32 from L2, softmax: 19.4 us and 15.7 backward with one for all, 18.7 and 13.7).  Given the
+// counts there is one for all (from HBM 13.9 us, 15.3 with one for each).
 template <typename F>
 auto by_kind(int kind, F f) {
   return kind == MOE_BALANCE_SOFTMAX   ? f(std::integral_constant<int, MOE_BALANCE_SOFTMAX>{})
@@ -676,7 +681,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& g, cudaStream_t s) {
     constexpr int V = decltype(l)::V, LANES = decltype(l)::LANES;
     auto kern = by_kind(g.kind, [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
-      return g.counts_in ? balance_kernel<V, LANES, kGiven, KIND>
+      return g.counts_in ? balance_kernel<V, LANES, kGiven, kAnyKind>
              : g.dtype == MOE_DTYPE_BF16 ? balance_kernel<V, LANES, kBf16Keys, KIND>
                                          : balance_kernel<V, LANES, kF32Keys, KIND>;
     });
