@@ -16,7 +16,8 @@
 // The selection binds the forward, not memory.  65536 tokens of 128 experts in fp32, top 8:
 // 33.6 us looking for the next smaller value in every round, 28.3 with sorted lanes, 25.4 with
 // merged lists, 23.0 without a test of each expert against E, 19.9 with the next token's
-// values loaded under this one's work; the integer pipe is then the busiest.
+// values loaded under this one's work, 19.4 with a kernel for each kind; the integer pipe is
+// then the busiest.
 #include <type_traits>
 
 #include "common.cuh"
@@ -509,10 +510,9 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
 }
 
 // The gradient's blocks of an SM, all of them resident, with the next tokens' values on their
-// way.  Of 4 values a lane three: 11000 tokens of 128 experts in bf16 take 5.15 us, with four
-// 5.4, with up to eight and nothing on the way 6.6.  Of 8 four: 65536 tokens of 256 in
-// fp32 24.9 us, with three 26.6.
-constexpr int grad_each(int V) { return V <= 4 ? 3 : V <= 8 ? 4 : V <= 16 ? 2 : 1; }
+// way.  65536 tokens of 128 experts, softmax in fp32 (4 values a lane): 15.5 us, with three 17.0;
+// 11000 in bf16, sigmoid: 5.4 both.  65536 of 256 (8 values) 24.4 us, with three 25.5.
+constexpr int grad_each(int V) { return V <= 8 ? 4 : V <= 16 ? 2 : 1; }
 template <int V, int LANES, int KIND>
 __global__ void __launch_bounds__(256, grad_each(V))
     balance_grad_kernel(const BalanceArgs g, bool wide, bool wide_out) {
@@ -608,12 +608,11 @@ struct Layout {
 };
 
 // f(Layout) for E experts.  4 experts a lane keep small batches short and 16 take fewer
-// instructions a token.  fp32, top 8: of 61 experts 4096 tokens take 6.6 us with 4 in 16
-// lanes and 7.8 with 16 in 4, 65536 17.5 and 14.8; of 128 experts 500 tokens 5.8 and 6.9,
-// 65536 21.6 and 19.9; of 32 experts 1024 tokens 5.5 and 9.1, 65536 10.5 and 9.1; of 256
-// experts 1024 tokens 9.1 with 8 in 32 lanes and 7.7 with 16 in 16, 65536 46 and 36.  The
-// gradient has nothing to select: 65536 tokens of 256 experts 30 with 8, 39 with 16
-// (25 with 8 since loads run ahead).
+// instructions a token.  Softmax in fp32, top 8: of 61 experts 4096 tokens take 6.3 us with 4 in 16
+// lanes and 7.4 with 16 in 4, 65536 17.0 and 14.3; of 128 experts 500 tokens 5.4 and 6.3,
+// 65536 20.6 and 19.2; of 32 experts 1024 tokens 5.1 and (16 in 2) 8.7, 65536 10.2 and 8.9; of
+// 256 experts 1024 tokens 9.0 with 8 in 32 lanes and 7.4 with 16 in 16, 65536 46 and 35.  The
+// gradient has nothing to select: 65536 tokens of 256 experts 24.2 with 8, 25.7 with 16.
 constexpr int kManyTokens = 8192;
 template <bool FORWARD, typename F>
 void by_experts(int E, int T, F f) {
