@@ -14,8 +14,11 @@
 // Rows wider than a warp's go through a ring of rows in shared memory for each group,
 // filled by bulk copies several rows ahead (Ring), with the weights in fp32 beside it;
 // narrower rows, few rows, very wide fp32 rows and rows whose tensors are aligned apart are
-// loaded straight into registers.  Loaded one row ahead into registers, 11000 rows of 4096
-// took 49 us and the gradient of 8192 rows of 5120 took 106 us (bf16): the values held
+// loaded straight into registers.  Where that is 16 or 32 columns a thread by single accesses, or
+// backward 32 fp32 columns, the registers spill (0.2 to 1.3 KB a thread): 5000 rows of 5120 in
+// bf16 that start 2 bytes past 16 take 121 us and 146 backward, 2000 of 16384 in fp32 75 and 171.
+//
+// Loaded one row ahead into registers, 11000 rows of 4096 took 49 us and the gradient of 8192 rows of 5120 took 106 us (bf16): the values held
 // ahead left too few warps to hide the reductions; through the ring 35 and 54 us, 5.2 and
 // 4.7 TB/s.  Arithmetic is in pairs (fma.rn.f32x2), and 32 values a thread spread a row's
 // fixed cost over enough elements.
@@ -831,7 +834,9 @@ Shape shape(int D, int n, int most) {
   return {n, R, groups < 1 ? 1 : groups > kMaxGroups ? kMaxGroups : groups};
 }
 
-constexpr int kWarpColumns = 512;     // rows up to this are a warp's (8 or 16 values a thread)
+// Rows up to this are a warp's (8 or 16 values a thread).  16384 rows of 512 in bf16 take 12.4 us, 17.8
+// backward, and 15.1, 21.4 through the ring; rows of 640 24.4, 31.7 in two warps, 17.5, 24.8 through it.
+constexpr int kWarpColumns = 512;
 // Of a ring kernel's block, in whole groups; fewer where the pieces at a row's ends cost registers.
 constexpr int forward_threads(bool shift) { return shift ? 640 : 768; }
 constexpr int backward_threads(bool shift) { return shift ? 384 : 512; }
@@ -917,7 +922,8 @@ cudaError_t launch_layer_norm(const NormArgs& g, cudaStream_t s) {
     constexpr int L = decltype(layout)::v, VEC = L == kWide ? 8 : 1;
     constexpr bool SHIFT = L == kShifted;
     const int D = g.D;
-    // few rows: a block each, with nothing to fill a ring with (16 rows of 5120: 2.6 us, 7.3 through the ring)
+    // few rows: a block each, with nothing to fill a ring with (bf16: 304 rows of 5120 4.0 us, 5.8 through the
+    // ring, 1216 11.2 and 9.5; of 1024 columns direct wins longer: 1216 rows 4.4 and 6.7, 16384 25.5 and 20.5)
     if (L != kSingle && D > (SHIFT ? kSingleForward : kWarpColumns) && g.T > 2 * device_sm_count()) {
       int stages;
       const Shape sh = ring_shape(D, SHIFT, forward_threads(SHIFT), (int64_t)8 * weight_floats<SHIFT>(D),

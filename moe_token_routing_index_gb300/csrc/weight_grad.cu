@@ -38,6 +38,9 @@
 // its tiles of that order from both ends at once, a long one in one accumulator and short
 // ones in the other (Schedule).
 //
+// Times in this file are the GPU's, of calls in a graph, those of one comparison of one session.
+// Between boxes they differ by up to 5%.
+//
 // Every mbarrier wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT,
 // all roles stop, copies and MMAs in flight are drained, and tensor memory is freed.
 #include "common.cuh"
@@ -59,7 +62,10 @@ constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // 48 KB
 constexpr int kStages = 4, kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kThreads = 224;
-constexpr int kMaxSorted = 384;           // experts (or parts) up to which the rank sort is run
+// Experts (or parts) up to which the rank sort is run, whose steps grow with their square.  16384
+// rows, Zipf-like, N = 1024, K = 2304, sorted and not: 200 experts 206 and 211 us, 384 366 and 361,
+// 500 470 and 454, 1000 932 and 872.
+constexpr int kMaxSorted = 384;
 constexpr int kPairsGB300 = kNumSmsGB300 / 2;
 constexpr int kMinPart = 960;             // rows
 constexpr int kWhole = 0xffff;            // the slot of an expert that is not cut
