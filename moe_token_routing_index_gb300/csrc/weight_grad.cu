@@ -39,7 +39,7 @@
 // ones in the other (Schedule).
 //
 // Times in this file are the GPU's, of calls in a graph, those of one comparison of one session.
-// Between boxes they differ by up to 5%.
+// Between machines they differ by up to 5%.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT,
 // all roles stop, copies and MMAs in flight are drained, and tensor memory is freed.
