@@ -11,6 +11,10 @@
  *   moe_silu_mul_checkpoint     z = silu(y0) * y1, keeping y0 and y1 as an 8-bit checkpoint
  *   moe_silu_mul_backward       the gradient of silu_mul, read from that checkpoint
  *   moe_grouped_weight_grad     the experts' weight gradients dW[e] = dY_e^T X_e
+ *   moe_gated_mlp               the experts' gated feed-forward block, keeping what its gradient needs
+ *   moe_gated_mlp_backward      ... the gradient of its data path
+ *   moe_orthogonalize           a batch of matrices orthogonalised by Newton-Schulz products
+ *   moe_muon_update             momentum and the weights' update by the orthogonalised momentum
  *
  * The conventions of moe.h hold: device pointers owned by the caller, no
  * allocation, everything asynchronous on `stream`, status codes for argument
@@ -190,6 +194,84 @@ int moe_grouped_weight_grad_workspace_size(int E, int a_max, int N, int K, int x
 int moe_grouped_weight_grad(const void* dy, const void* x, const uint8_t* x_exponents, const int32_t* counts, int E,
                             int a_max, int N, int K, void* dw, int dw_dtype, int accumulate, void* ws,
                             size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------- gated feed-forward block */
+
+/* act(v): v * sigmoid(v), or the tanh form of the GELU, v * sigmoid(sqrt(8 / pi) (v + 0.044715 v^3)). */
+#define MOE_ACT_SILU 0
+#define MOE_ACT_GELU 1
+
+/*
+ * The experts' gated feed-forward block on routed rows, for the rows r of expert e
+ * (as in moe_grouped_gemm: [off_e, off_e + counts[e])):
+ *   y[r, n]   = sum_d x[r, d] w13[e, n, d]               n < 2H
+ *   z[r, j]   = act(y[r, j]) * y[r, H + j]               j < H
+ *   out[r, d] = sum_j z[r, j] w2[e, d, j]
+ * with fp32 accumulation.  z is computed from the fp32 y and rounded to bf16, the operand of the
+ * second product; y and out are rounded once.  (moe_grouped_gemm with MOE_EPILOGUE_SILU_MUL rounds y first.)
+ *
+ * x [a_max, D], w13 [E, 2H, D], w2 [E, D, H], y [a_max, 2H] (nullable: not kept), z [a_max, H],
+ * out [a_max, D], all bf16 and contiguous.  counts [E] device int32: negative entries count as 0
+ * and a sum past a_max is cut there; both are flagged (MOE_DEVERR_BAD_COUNT).  Rows of the
+ * outputs past the sum are not written, whatever x holds there.
+ * D and H multiples of 16, E <= 1024, 16-byte aligned bases (MOE_ERR_UNSUPPORTED).
+ * D == 0 or H == 0 is MOE_ERR_INVALID; a_max == 0 is a no-op.
+ */
+int moe_gated_mlp(const void* x, const void* w13, const void* w2, const int32_t* counts, int E, int a_max, int D, int H,
+                  int activation, void* y, void* z, void* out, cudaStream_t stream);
+
+/*
+ * The gradient of its data path, from dout [a_max, D] bf16 and the kept y:
+ *   dz[r, j]     = sum_d dout[r, d] w2[e, d, j]                 (fp32)
+ *   dy[r, j]     = bf16(dz y1 act'(y0)),  dy[r, H + j] = bf16(dz act(y0))
+ *   z[r, j]      = bf16(act(y0) y1)       (nullable: what the gradient of w2 takes)
+ *   dx[r, d]     = sum_n dy[r, n] w13[e, n, d]
+ * with y0 = y[r, j], y1 = y[r, H + j].  The weights are read as the forward reads them: no transposed copies.
+ * y: [a_max, 2H] bf16 with y_exponents NULL, or the codes of a checkpoint in two halves
+ * (moe_silu_mul_checkpoint) with its exponents.  dy [a_max, 2H], z [a_max, H], dx [a_max, D] bf16.
+ * The weights' gradients are moe_grouped_weight_grad(dy, x) and (dout, z).
+ * counts, sizes and errors: as above.
+ */
+int moe_gated_mlp_backward(const void* dout, const void* y, const uint8_t* y_exponents, const void* w13, const void* w2,
+                           const int32_t* counts, int E, int a_max, int D, int H, int activation, void* dy, void* z,
+                           void* dx, cudaStream_t stream);
+
+/* ----------------------------------------- orthogonalised weight updates */
+
+/*
+ * Each of B matrices G [N, K], driven towards the nearest matrix with orthonormal rows (N <= K)
+ * or columns (N > K) by `steps` Newton-Schulz products:
+ *   X = G / (|G| + eps), |G| the Frobenius norm; then, for the [m, n] view of X with m <= n,
+ *   A = X X^T,  X = a X + (b A + c A A) X     each step;
+ *   out = scale * X
+ * g: element (i, r, c) at g + i * batch_stride + r * row_stride + c, MOE_DTYPE_BF16 or MOE_DTYPE_F32;
+ * out [B, N, K] bf16, contiguous.  1 <= steps <= 16; eps >= 1e-12.
+ * coefficients: host float[3] (a, b, c), or NULL: 3.4445, -4.7750, 2.0315.  The iteration must keep
+ * every singular value in [0, 1] below 4, and |b s^2 + c s^4| below 32 (MOE_ERR_INVALID).
+ * The products' operands are fp16 (scaled by a power of two) with fp32 accumulation, X itself has 22 bits.
+ * A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN in its own result only.
+ * Any 1 <= N, K <= 65536 and B <= 65535 (larger: MOE_ERR_UNSUPPORTED), any element alignment.
+ * B, N or K == 0 is a no-op.
+ * ws: device workspace of moe_orthogonalize_workspace_size bytes, 256-byte aligned; its contents
+ * on entry do not matter.  One workspace serves one call at a time.
+ */
+int moe_orthogonalize_workspace_size(int B, int N, int K, size_t* bytes);
+int moe_orthogonalize(const void* g, int dtype, int64_t batch_stride, int64_t row_stride, int B, int N, int K, int steps,
+                      const float* coefficients, float eps, float scale, void* out, void* ws, size_t ws_bytes,
+                      cudaStream_t stream);
+
+/*
+ * One update of B weight matrices w [N, K], in place:
+ *   momentum = mu * momentum + grad
+ *   u        = grad + mu * momentum (nesterov != 0), or momentum
+ *   w        = (1 - r * weight_decay) * w - r * X,  X as above from u,  r = lr * (lr_scale ? *lr_scale : 1)
+ * w of w_dtype and grad of grad_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), momentum fp32, all
+ * [B, N, K] contiguous; the sums in fp32, w rounded once.  lr_scale: device fp32 scalar, nullable.
+ * lr, weight_decay and mu are finite, mu in [0, 1).  steps, coefficients, eps, sizes and workspace: as above.
+ */
+int moe_muon_update(void* w, int w_dtype, const void* grad, int grad_dtype, float* momentum, int B, int N, int K,
+                    float mu, int nesterov, float lr, const float* lr_scale, float weight_decay, int steps,
+                    const float* coefficients, float eps, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

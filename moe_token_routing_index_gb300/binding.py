@@ -30,6 +30,7 @@ MOE_GEMM_CTA_PAIRS = 0x100
 MOE_WEIGHTS_PACKED = 0x200
 MOE_BALANCE_SCORES, MOE_BALANCE_SOFTMAX, MOE_BALANCE_SIGMOID = 0, 1, 2
 MOE_CHECKPOINT_BLOCK = 128
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
 MOE_DEVERR_BAD_INDEX, MOE_DEVERR_BAD_COUNT, MOE_DEVERR_TIMEOUT = 1, 2, 4
 
 
@@ -88,6 +89,11 @@ def _load() -> ctypes.CDLL:
         "moe_silu_mul_backward": ([P, P, P, I, I, P, P, P, P], I),
         "moe_grouped_weight_grad_workspace_size": ([I, I, I, I, I, ctypes.POINTER(S)], I),
         "moe_grouped_weight_grad": ([P, P, P, P, I, I, I, I, P, I, I, P, S, P], I),
+        "moe_gated_mlp": ([P, P, P, P, I, I, I, I, I, P, P, P, P], I),
+        "moe_gated_mlp_backward": ([P, P, P, P, P, P, I, I, I, I, I, P, P, P, P], I),
+        "moe_orthogonalize_workspace_size": ([I, I, I, ctypes.POINTER(S)], I),
+        "moe_orthogonalize": ([P, I, L, L, I, I, I, I, P, F, F, P, P, S, P], I),
+        "moe_muon_update": ([P, I, P, I, P, I, I, I, F, I, F, P, F, I, P, F, P, S, P], I),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -958,6 +964,148 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
                                       ws_bytes, _stream())
     _check("moe_grouped_weight_grad", st)
     return out
+
+
+# -------------------------------------------------- gated feed-forward block
+
+def _gated_weights(w13, w2, counts):
+    """Checks w13 [E, 2H, D], w2 [E, D, H] and counts [>= E]; returns E, D, H."""
+    if w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w13 must be [E, 2H, D] and w2 [E, D, H]")
+    E, n2, D = w13.shape
+    H = n2 // 2
+    if n2 % 2 or w2.shape != (E, D, H):
+        raise ValueError(f"w13 [E, 2H, D] and w2 [E, D, H] must fit together, got {tuple(w13.shape)} and "
+                         f"{tuple(w2.shape)}")
+    _need(w13, torch.bfloat16, "w13")
+    _need(w2, torch.bfloat16, "w2")
+    _need(counts, torch.int32, "counts")
+    if counts.dim() != 1 or counts.shape[0] < E:
+        raise ValueError(f"counts must hold {E} experts' rows, got {tuple(counts.shape)}")
+    return E, D, H
+
+
+def _gated_rows(t, D: int, name: str) -> int:
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 2 or t.shape[1] != D:
+        raise ValueError(f"{name} must be [rows, {D}], got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def moe_gated_mlp(x, w13, w2, counts, *, activation: int = MOE_ACT_SILU, keep: bool = True, y=None, z=None, out=None,
+                  stream=None):
+    """The experts' gated block: z = act(y0) * y1 with y = x w13_e^T, out = z w2_e^T, for x[a, D], w13[E, 2H, D],
+    w2[E, D, H] (bf16) and counts[>= E] int32.  Returns (out [a, D], y [a, 2H]), y being what the gradient
+    takes (None with keep=False).  Rows past the counts' sum are not written."""
+    if stream is not None:
+        return _call_on(moe_gated_mlp, locals())
+    E, D, H = _gated_weights(w13, w2, counts)
+    a, dev = _gated_rows(x, D, "x"), x.device
+    y = _output(y, (a, 2 * H), torch.bfloat16, dev, "y") if keep else None
+    z = _output(z, (a, H), torch.bfloat16, dev, "z")
+    out = _output(out, (a, D), torch.bfloat16, dev, "out")
+    st = _lib.moe_gated_mlp(_ptr(x), _ptr(w13), _ptr(w2), _ptr(counts), E, a, D, H, activation, _ptr(y), _ptr(z),
+                            _ptr(out), _stream())
+    _check("moe_gated_mlp", st)
+    return out, y
+
+
+def moe_gated_mlp_backward(dout, y, w13, w2, counts, *, activation: int = MOE_ACT_SILU, with_z: bool = True, out=None,
+                           dy=None, z=None, stream=None):
+    """The gradient of moe_gated_mlp's data path for dout[a, D] and the kept y (bf16 [a, 2H], or a Checkpoint in two
+    halves): returns (dx [a, D], dy [a, 2H], z [a, H]).  The weights' gradients are moe_grouped_weight_grad(dy, x,
+    counts) and moe_grouped_weight_grad(dout, z, counts); z is None without with_z."""
+    if stream is not None:
+        return _call_on(moe_gated_mlp_backward, locals())
+    E, D, H = _gated_weights(w13, w2, counts)
+    a, dev = _gated_rows(dout, D, "dout"), dout.device
+    if isinstance(y, Checkpoint):
+        ck = _checkpoint_arg(y, a, 2 * H, 2)
+        y_ptr, exps = _ptr(ck.codes), _ptr(ck.exponents)
+    else:
+        _output(y, (a, 2 * H), torch.bfloat16, None, "y")
+        y_ptr, exps = _ptr(y), None
+    dy = _output(dy, (a, 2 * H), torch.bfloat16, dev, "dy")
+    z = _output(z, (a, H), torch.bfloat16, dev, "z") if with_z else None
+    out = _output(out, (a, D), torch.bfloat16, dev, "out")
+    st = _lib.moe_gated_mlp_backward(_ptr(dout), y_ptr, exps, _ptr(w13), _ptr(w2), _ptr(counts), E, a, D, H,
+                                     activation, _ptr(dy), _ptr(z), _ptr(out), _stream())
+    _check("moe_gated_mlp_backward", st)
+    return out, dy, z
+
+
+# --------------------------------------------------- orthogonalised updates
+
+MOE_ORTHOGONALIZE_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_orthogonalize_workspace_size(B: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_orthogonalize_workspace_size", _lib.moe_orthogonalize_workspace_size(B, N, K, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=64)
+def _coefficients(c: tuple):
+    if len(c) != 3:
+        raise ValueError(f"coefficients must be three numbers, got {len(c)}")
+    return (ctypes.c_float * 3)(*c)
+
+
+def _matrices(t, name: str):
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [N, K] or [B, N, K], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.shape if t.dim() == 3 else (1, *t.shape)
+
+
+def _ortho_workspace(workspace, B: int, N: int, K: int, device):
+    if workspace is not None:
+        return workspace, _workspace_bytes(workspace)
+    n = moe_orthogonalize_workspace_size(B, N, K)
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def moe_orthogonalize(g, *, steps: int = 5, coefficients=MOE_ORTHOGONALIZE_COEFFICIENTS, eps: float = 1e-7,
+                      scale: float = 1.0, out=None, workspace=None, stream=None):
+    """scale times the matrices g [N, K] or [B, N, K] (bf16 or fp32, rows and matrices of any stride) after `steps`
+    Newton-Schulz products X = a X + (b A + c A A) X, A = X X^T, from X = g / (|g| + eps); bf16, of g's shape."""
+    if stream is not None:
+        return _call_on(moe_orthogonalize, locals())
+    B, N, K = _matrices(g, "g")
+    _need(g, g.dtype, "g", contiguous=False)
+    dt = _dtype_code(g)
+    out = _output(out, tuple(g.shape), torch.bfloat16, g.device, "out")
+    workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, g.device)
+    st = _lib.moe_orthogonalize(_ptr(g), dt, g.stride(0) if B > 1 else 0, g.stride(-2) if N > 1 else 0, B, N, K,
+                                steps, _coefficients(tuple(coefficients)), eps, scale, _ptr(out), _ptr(workspace),
+                                ws_bytes, _stream())
+    _check("moe_orthogonalize", st)
+    return out
+
+
+def moe_muon_update(w, grad, momentum, *, lr: float, mu: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                    lr_scale=None, steps: int = 5, coefficients=MOE_ORTHOGONALIZE_COEFFICIENTS, eps: float = 1e-7,
+                    workspace=None, stream=None):
+    """One update, in place, of the weights w [N, K] or [B, N, K] (bf16 or fp32) by their orthogonalised momentum:
+    momentum (fp32) = mu * momentum + grad, u = grad + mu * momentum (nesterov) or momentum,
+    w = (1 - r * weight_decay) * w - r * orthogonalized(u), r = lr * lr_scale (fp32 [1] on the device, None: 1).
+    Returns w."""
+    if stream is not None:
+        return _call_on(moe_muon_update, locals())
+    B, N, K = _matrices(w, "w")
+    _need(w, w.dtype, "w")
+    _output(grad, w.shape, grad.dtype, None, "grad")
+    _output(momentum, w.shape, torch.float32, None, "momentum")
+    wt, gt = _dtype_code(w), _dtype_code(grad)
+    workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, w.device)
+    st = _lib.moe_muon_update(_ptr(w), wt, _ptr(grad), gt, _ptr(momentum), B, N, K, mu, int(nesterov), lr,
+                              _valid_arg(lr_scale, "lr_scale", torch.float32), weight_decay, steps,
+                              _coefficients(tuple(coefficients)), eps, _ptr(workspace), ws_bytes, _stream())
+    _check("moe_muon_update", st)
+    return w
 
 
 def moe_selftest_bounded_wait(which: int, limit_ns: int = 20_000_000, stream=None) -> int:

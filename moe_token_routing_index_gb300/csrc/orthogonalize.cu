@@ -1,0 +1,452 @@
+// Orthogonalisation of a batch of matrices by Newton-Schulz products, and the momentum update
+// of weights that applies it (include/moe_train.h), on the pair GEMM.
+//
+// X = G / (|G| + eps), then for each step, with m the shorter side and X seen as [m, n]:
+//   A = X X^T      P = b A + c A A      X = a X + P X
+// A and P are symmetric: only the tiles on and below the diagonal are computed, and each is
+// stored a second time across it.
+//
+// Operands are fp16 scaled by 2^10.  Singular values stay below 4 (checked on the host for the
+// coefficients), so the entries of X, A and P stay below 2^15 after the scaling, and what a
+// matrix of 10^4 columns holds on average (10^-4 and less) stays above fp16's least normal
+// number.  fp16 rounds eight times finer than bf16 at the same rate: against 64 bits the result
+// of five steps on Gaussian matrices is off by 1.7e-3 of its norm, with bf16 by 1.1e-2.  X itself
+// is kept in two fp16 (its value and what the first leaves): a X is added from both, because
+// the iteration multiplies what lies in small singular values by a at each step, and the
+// rounding of the large ones with it (few strong directions over a weak rest: 1.4e-2 off with
+// one fp16).
+#include "common.cuh"
+#include "launch.h"
+#include "pair_gemm.cuh"
+#include "train_launch.h"
+
+namespace moe {
+namespace {
+
+using namespace pg;
+
+constexpr float kScale = 1024.0f, kUnscale = 1.0f / kScale;
+constexpr int kNormThreads = 256;
+
+// ------------------------------------------------- momentum, norm, first iterate
+
+struct Source {            // u: g itself, or g and the momentum
+  const void* g;
+  int64_t batch, row;      // strides of g, elements
+  int dtype;
+  float* momentum;         // nullable; contiguous
+  float mu;
+  int nesterov;
+  int B, N, K;
+};
+
+__device__ __forceinline__ float load_g(const Source& p, int b, int r, int c) {
+  const int64_t o = b * p.batch + r * p.row + c;
+  return p.dtype == MOE_DTYPE_F32 ? static_cast<const float*>(p.g)[o]
+                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(p.g)[o]);
+}
+
+// Squares whose sum would overflow are summed a second time as multiples of 2^160.
+constexpr float kDown = 0x1p-80f;
+
+struct Squares {
+  float plain = 0.0f, small = 0.0f;
+  __device__ __forceinline__ void add(float u) {
+    plain = fmaf(u, u, plain);
+    const float d = u * kDown;
+    small = fmaf(d, d, small);
+  }
+};
+
+__device__ __forceinline__ float2 block_sum(float2 v) {
+  __shared__ float2 s[kNormThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float2 t = s[0];
+  for (int i = 1; i < kNormThreads / 32; ++i) {
+    t.x += s[i].x;
+    t.y += s[i].y;
+  }
+  return t;
+}
+
+// Block (i, b): rows i, i + gridDim.x, ... of matrix b.  The momentum is updated, and the
+// squares of u are summed: part[b][i].
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Source p, float2* part) {
+  pdl_launch_dependents();
+  const int b = blockIdx.y;
+  Squares q;
+  for (int r = blockIdx.x; r < p.N; r += gridDim.x)
+    for (int c = threadIdx.x; c < p.K; c += kNormThreads) {
+      float u = load_g(p, b, r, c);
+      if (p.momentum) {
+        float* m = p.momentum + ((int64_t)b * p.N + r) * p.K + c;
+        const float v = fmaf(p.mu, *m, u);
+        *m = v;
+        u = p.nesterov ? fmaf(p.mu, v, u) : v;
+      }
+      q.add(u);
+    }
+  const float2 t = block_sum(make_float2(q.plain, q.small));
+  if (threadIdx.x == 0) part[(int64_t)b * gridDim.x + blockIdx.x] = t;
+}
+
+// X = u / (|u| + eps), scaled, in two fp16 with rows ld elements apart.
+__global__ void __launch_bounds__(kNormThreads) first_kernel(const Source p, const float2* part, int parts, float eps,
+                                                             __half* hi, __half* lo, int ld) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.y;
+  float2 t = make_float2(0.0f, 0.0f);
+  for (int i = threadIdx.x; i < parts; i += kNormThreads) {
+    const float2 v = part[(int64_t)b * parts + i];
+    t.x += v.x;
+    t.y += v.y;
+  }
+  t = block_sum(t);
+  // (a sum that overflowed means entries above 2^60: eps is far below the norm)
+  const bool big = isinf(t.x);
+  const float pre = big ? kDown : 1.0f;
+  const float f = kScale / (big ? sqrtf(t.y) : sqrtf(t.x) + eps);
+  for (int r = blockIdx.x; r < p.N; r += gridDim.x)
+    for (int c = threadIdx.x; c < p.K; c += kNormThreads) {
+      float u = load_g(p, b, r, c);
+      if (p.momentum) {
+        const float m = p.momentum[((int64_t)b * p.N + r) * p.K + c];
+        u = p.nesterov ? fmaf(p.mu, m, u) : m;
+      }
+      const float x = u * pre * f;
+      const __half h = __float2half_rn(x);
+      const int64_t o = ((int64_t)b * p.N + r) * ld + c;
+      hi[o] = h;
+      lo[o] = __float2half_rn(x - __half2float(h));
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+// A tile of 256 columns (lanes) x n rows of a [rows, cols] result of one matrix.
+struct MatTile {
+  int n, blocks;
+  int at, col, row;    // the matrix, first column and first row
+  int height;          // of B's boxes where it is K-major
+  bool mirror;         // symmetric results: stored across the diagonal too
+};
+
+constexpr int kHeights = 4;
+__host__ __device__ constexpr int box_rows(int h) { return 16 << h; }
+
+struct Mats {
+  CUtensorMap a, b[kHeights];
+  int count, rows, cols;  // of the result
+  int ct, rt;             // tiles along its columns and rows
+  int per;                // tiles of a matrix
+  int blocks;             // of the reduction
+};
+
+// SYM: the tiles of column block >= row block (cols == rows).
+template <bool SYM>
+__device__ __forceinline__ MatTile locate_mat(const Mats& p, int i) {
+  MatTile t;
+  t.at = i / p.per;
+  const int l = i - t.at * p.per;
+  int r, c;
+  if (SYM) {  // row block r has the column blocks 0 .. r
+    r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > l) --r;
+    while ((r + 1) * (r + 2) / 2 <= l) ++r;
+    c = l - r * (r + 1) / 2;
+    t.mirror = c != r;
+  } else {
+    r = l / p.ct;
+    c = l - r * p.ct;
+    t.mirror = false;
+  }
+  t.col = c * kTileM;
+  t.row = r * kMaxN;
+  t.n = min(kMaxN, (p.rows - t.row + 31) / 32 * 32);
+  t.blocks = p.blocks;
+  const int half = t.n / 2;
+  t.height = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+  return t;
+}
+
+enum Product { kGram, kPolynomial, kNext, kOut, kWeights };
+
+struct Result {
+  __half* sym;          // A or P, rows ldm elements apart
+  const __half* src;    // P: A.  X: its first half
+  __half* next;         // X's next first half
+  __half* lo;           // X's second half, in place
+  void* out;            // bf16 result, or weights
+  int ld;               // of sym and src's matrices; X: of src, next and lo
+  float alpha, beta;    // result = alpha * src + beta * product
+  float scale, keep;    // out = scale * result, or keep * w - scale * result
+  const float* lr;      // nullable: multiplies scale, and what keep takes from 1
+  int w_dtype;
+};
+
+template <bool AMN, bool BMN, Product KIND>
+struct Ns {
+  static constexpr bool kAMN = AMN, kBMN = BMN, kF16 = true;
+  static constexpr bool kSym = KIND == kGram || KIND == kPolynomial;
+  struct Params {
+    Mats m;
+    Result r;
+    unsigned int* err;
+  };
+  using Tile = MatTile;
+  static __device__ int setup(const Params& p, int*, int) { return p.m.count * p.m.per; }
+  static __device__ Tile tile(const Params& p, const int*, int i) { return locate_mat<kSym>(p.m, i); }
+  static __device__ uint32_t stage_bytes(const Params&, const Tile& t) {
+    return 2u * (uint32_t)(kOperandBytes + (BMN ? kOperandBytes : box_rows(t.height) * 128 * (kBK / 64)));
+  }
+  static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
+                              uint32_t bar) {
+    load_half<AMN>(a, &p.m.a, bar, block * kBK, t.col + rank * kHalfM, t.at);
+    const int row = t.row + rank * (t.n / 2);
+    if (BMN || t.height == 3) load_half<BMN>(b, &p.m.b[3], bar, block * kBK, row, t.at);
+    else if (t.height == 2) load_half<BMN>(b, &p.m.b[2], bar, block * kBK, row, t.at);
+    else if (t.height == 1) load_half<BMN>(b, &p.m.b[1], bar, block * kBK, row, t.at);
+    else load_half<BMN>(b, &p.m.b[0], bar, block * kBK, row, t.at);
+  }
+  template <class Release>
+  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int lane, uint32_t tbase,
+                                  Release release) {
+    const Result& g = p.r;
+    const int f = t.col + rank * kHalfM + sub * 32 + lane;
+    const bool keep = f < p.m.cols;
+    const int rows = min(t.n, p.m.rows - t.row);
+    const int64_t ld = g.ld, base = (int64_t)t.at * p.m.rows * ld;
+    const int64_t first = base + (int64_t)t.row * ld + f;
+    float lr = 1.0f;
+    if (KIND == kWeights && g.lr) lr = __ldg(g.lr);
+    const float w_keep = 1.0f - lr * g.keep, w_scale = lr * g.scale;
+    for (int c = 0; c < rows; c += 32) {
+      float x[32], v[32];
+      if (KIND != kGram) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          x[i] = 0.0f;
+          if (keep && c + i < rows) {
+            const int64_t o = first + (int64_t)(c + i) * ld;
+            x[i] = __half2float(g.src[o]);
+            if (KIND != kPolynomial) x[i] += __half2float(g.lo[o]);
+          }
+        }
+      }
+      tmem_ld32(tbase + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] *= g.beta;
+        if (KIND != kGram) v[i] = fmaf(g.alpha, x[i], v[i]);
+        if (!keep || c + i >= rows) continue;
+        if (kSym || KIND == kNext) {
+          const int64_t o = first + (int64_t)(c + i) * ld;
+          const __half h = __float2half_rn(v[i]);
+          if (kSym) {
+            g.sym[o] = h;
+          } else {
+            g.next[o] = h;
+            g.lo[o] = __float2half_rn(v[i] - __half2float(h));
+          }
+        } else {
+          const int64_t o = ((int64_t)t.at * p.m.rows + t.row + c + i) * p.m.cols + f;
+          if (KIND == kOut) {
+            static_cast<__nv_bfloat16*>(g.out)[o] = __float2bfloat16_rn(v[i] * g.scale);
+          } else if (g.w_dtype == MOE_DTYPE_F32) {
+            float* w = static_cast<float*>(g.out) + o;
+            *w = w_keep * *w - w_scale * v[i];
+          } else {
+            __nv_bfloat16* w = static_cast<__nv_bfloat16*>(g.out) + o;
+            *w = __float2bfloat16_rn(w_keep * __bfloat162float(*w) - w_scale * v[i]);
+          }
+        }
+      }
+      if (kSym && t.mirror && keep) {  // this lane's row of the mirrored tile
+        __half* m = g.sym + base + (int64_t)f * ld + t.row + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < rows) m[i] = __float2half_rn(v[i]);
+      }
+    }
+    release();
+  }
+};
+
+// ------------------------------------------------------------------- host
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+int norm_blocks(const OrthoArgs& g) {
+  const int64_t most = (8 * (int64_t)kNumSmsGB300 + g.B - 1) / g.B;
+  const int64_t want = ((int64_t)g.N * g.K + 4095) / 4096;
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n > g.N ? g.N : n);
+}
+
+struct Layout {
+  int m, ldx, ldm;
+  size_t part, x0, x1, lo, gram, poly, total;  // offsets
+};
+
+Layout layout(const OrthoArgs& g) {
+  Layout l;
+  l.m = g.N < g.K ? g.N : g.K;
+  l.ldx = (int)up(g.K, 8);
+  l.ldm = (int)up(l.m, 8);
+  const size_t x = up((int64_t)g.B * g.N * l.ldx * 2, 256), sym = up((int64_t)g.B * l.m * l.ldm * 2, 256);
+  l.part = 0;
+  l.x0 = up((int64_t)g.B * norm_blocks(g) * (int64_t)sizeof(float2), 256);
+  l.x1 = l.x0 + x;
+  l.lo = l.x1 + x;
+  l.gram = l.lo + x;
+  l.poly = l.gram + sym;
+  l.total = l.poly + sym;
+  return l;
+}
+
+// The result [rows, cols] of count matrices; reduction over k.
+bool make_mats(Mats* m, const OrthoArgs& g, int rows, int cols, int k, bool sym) {
+  m->count = g.B;
+  m->rows = rows;
+  m->cols = cols;
+  m->ct = (cols + kTileM - 1) / kTileM;
+  m->rt = (rows + kMaxN - 1) / kMaxN;
+  m->blocks = (k + kBK - 1) / kBK;
+  m->per = sym ? m->rt * (m->rt + 1) / 2 : m->rt * m->ct;
+  return (int64_t)m->per * g.B <= INT32_MAX / 2;
+}
+
+// The operand maps: matrices [rows, cols] with rows ld elements apart.
+bool map_a(Mats* m, bool mn, const void* x, int count, int rows, int cols, int ld) {
+  return make_map_3d(&m->a, x, true, count, rows, cols, ld, mn ? kBK : kHalfM);
+}
+bool map_b(Mats* m, bool mn, const void* x, int count, int rows, int cols, int ld) {
+  for (int h = 0; h < kHeights; ++h)
+    if (!make_map_3d(&m->b[h], x, true, count, rows, cols, ld, mn ? kBK : box_rows(h))) return false;
+  return true;
+}
+
+template <class P>
+cudaError_t launch(const typename P::Params& p, cudaStream_t s) {
+  return launch_pairs<P>(p, (int64_t)p.m.count * p.m.per, 0, true, s);
+}
+
+template <bool TALL, Product KIND>
+cudaError_t multiply(const OrthoArgs& g, const Layout& l, const Result& r, const __half* poly, cudaStream_t s) {
+  // X [N, K] with lanes along K: A is X read along its columns (wide), or P (tall)
+  using P = Ns<!TALL, false, KIND>;
+  typename P::Params p{};
+  if (!make_mats(&p.m, g, g.N, g.K, l.m, false)) return cudaErrorNotSupported;
+  if (TALL ? !(map_a(&p.m, false, poly, g.B, l.m, l.m, l.ldm) && map_b(&p.m, false, r.src, g.B, g.N, g.K, l.ldx))
+           : !(map_a(&p.m, true, r.src, g.B, g.N, g.K, l.ldx) && map_b(&p.m, false, poly, g.B, l.m, l.m, l.ldm)))
+    return cudaErrorInvalidValue;
+  p.r = r;
+  p.err = g.err;
+  return launch<P>(p, s);
+}
+
+template <bool TALL>
+cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s) {
+  __half* x[2] = {reinterpret_cast<__half*>(ws + l.x0), reinterpret_cast<__half*>(ws + l.x1)};
+  __half* gram = reinterpret_cast<__half*>(ws + l.gram);
+  __half* poly = reinterpret_cast<__half*>(ws + l.poly);
+  using Gram = Ns<TALL, TALL, kGram>;
+  using Poly = Ns<false, false, kPolynomial>;
+  for (int step = 0; step < g.steps; ++step) {
+    const __half* cur = x[step & 1];
+    typename Gram::Params a{};
+    if (!make_mats(&a.m, g, l.m, l.m, TALL ? g.N : g.K, true)) return cudaErrorNotSupported;
+    if (!map_a(&a.m, TALL, cur, g.B, g.N, g.K, l.ldx) || !map_b(&a.m, TALL, cur, g.B, g.N, g.K, l.ldx))
+      return cudaErrorInvalidValue;
+    a.r.sym = gram;
+    a.r.ld = l.ldm;
+    a.r.beta = kUnscale;
+    a.err = g.err;
+    cudaError_t e = launch<Gram>(a, s);
+    if (e != cudaSuccess) return e;
+
+    typename Poly::Params q{};
+    if (!make_mats(&q.m, g, l.m, l.m, l.m, true)) return cudaErrorNotSupported;
+    if (!map_a(&q.m, false, gram, g.B, l.m, l.m, l.ldm) || !map_b(&q.m, false, gram, g.B, l.m, l.m, l.ldm))
+      return cudaErrorInvalidValue;
+    q.r.sym = poly;
+    q.r.src = gram;
+    q.r.ld = l.ldm;
+    q.r.alpha = g.coef[1];
+    q.r.beta = g.coef[2] * kUnscale;
+    q.err = g.err;
+    e = launch<Poly>(q, s);
+    if (e != cudaSuccess) return e;
+
+    Result r{};
+    r.src = cur;
+    r.next = x[(step + 1) & 1];
+    r.lo = reinterpret_cast<__half*>(ws + l.lo);
+    r.ld = l.ldx;
+    r.alpha = g.coef[0];
+    r.beta = kUnscale;
+    r.out = g.out;
+    r.scale = kUnscale * g.scale;
+    r.keep = g.decay;
+    r.lr = g.lr;
+    r.w_dtype = g.w_dtype;
+    if (step + 1 < g.steps) e = multiply<TALL, kNext>(g, l, r, poly, s);
+    else if (g.update) e = multiply<TALL, kWeights>(g, l, r, poly, s);
+    else e = multiply<TALL, kOut>(g, l, r, poly, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t orthogonalize_workspace_bytes(int B, int N, int K) {
+  OrthoArgs g{};
+  g.B = B;
+  g.N = N;
+  g.K = K;
+  return layout(g).total;
+}
+
+cudaError_t launch_orthogonalize(const OrthoArgs& g, cudaStream_t s) {
+  const Layout l = layout(g);
+  char* ws = static_cast<char*>(g.ws);
+  Source src{};
+  src.g = g.g;
+  src.batch = g.batch_stride;
+  src.row = g.row_stride;
+  src.dtype = g.dtype;
+  src.momentum = g.momentum;
+  src.mu = g.mu;
+  src.nesterov = g.nesterov;
+  src.B = g.B;
+  src.N = g.N;
+  src.K = g.K;
+  float2* part = reinterpret_cast<float2*>(ws + l.part);
+  const int parts = norm_blocks(g);
+  const dim3 grid(parts, g.B);
+  norm_kernel<<<grid, kNormThreads, 0, s>>>(src, part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, first_kernel, src, (const float2*)part, parts, g.eps,
+                         reinterpret_cast<__half*>(ws + l.x0), reinterpret_cast<__half*>(ws + l.lo), l.ldx);
+  if (e != cudaSuccess) return e;
+  return g.N > g.K ? iterate<true>(g, l, ws, s) : iterate<false>(g, l, ws, s);
+}
+
+}  // namespace moe

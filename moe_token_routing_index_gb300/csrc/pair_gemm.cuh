@@ -1,0 +1,384 @@
+// A persistent GEMM on pairs of SMs for 16-bit operands, whose problem (tile list, operand
+// boxes, epilogue) is a policy class: the gated feed-forward block and the orthogonalisation
+// share it.
+//
+// A cluster of two CTAs computes a tile D[256, n] = A[256, k] B[n, k]^T, n a multiple of 32 up
+// to 256, with tcgen05.mma.cta_group::2 (fp32 accumulation).  CTA r loads 128 rows of A and
+// n / 2 of B, the MMAs of the leader (rank 0) read both CTAs' shared memory, and each CTA's
+// tensor memory receives its 128 rows of the tile: one lane per row, one column per row of B.
+// An operand lies K-major (its rows contiguous along the reduction: boxes of 64 k) or MN-major
+// (rows of the reduction, contiguous along the tile: boxes of 64 columns).  6 warps:
+//   warp 0     TMA producer of this CTA's halves, into a ring of stages of kBK of the
+//              reduction; both CTAs' copies complete on the leader's barrier
+//   warp 1     (leader) MMA issuer, into one of two 256-column accumulators
+//   warps 2-5  the policy's epilogue, each on the 32 lanes of its quarter
+// What an epilogue stores has its lanes as the contiguous dimension, so that a warp's store of a
+// column is 64 contiguous bytes and needs no staging.
+//
+// Every wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT, all roles stop,
+// copies and MMAs in flight are drained, and tensor memory is freed.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace pg {
+
+using namespace tc;
+
+constexpr int kTileM = 256, kHalfM = 128, kMaxN = 256;
+constexpr int kBK = 64;                                  // of the reduction per stage
+constexpr int kOperandBytes = 128 * kBK * 2;             // of a CTA's half of A; room for its half of B
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 192 * 1024 / kStageBytes;
+constexpr int kAccBufs = 2;
+constexpr int kTmemCols = kAccBufs * kMaxN;
+constexpr int kThreads = 192;
+constexpr int kBoxBytes = 64 * 128;                      // of an MN-major box: 64 columns x kBK rows
+
+struct Smem {
+  static constexpr int stage = 0;
+  static constexpr int bars = stage + kStages * kStageBytes;  // full[S], empty[S], tfull[2], tempty[2], drain
+  static constexpr int misc = bars + (2 * kStages + 2 * kAccBufs + 1) * 8;
+  static constexpr int tables = (misc + 16 + 15) / 16 * 16;   // the policy's
+};
+
+// Shared-memory descriptor of an MN-major operand, 128B swizzle: 64-column blocks one box
+// apart, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((64 * kBK * 2) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// The descriptor of the 16 reduction steps from 16 * kk on of an operand's half at addr.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int kk) {
+  if (MN) return desc_mn(addr + kk * 2048);                            // 16 rows of 128 bytes
+  return smem_desc_sw128(addr + (kk >> 2) * (128 * 128) + (kk & 3) * 32);  // 64 k of 128 rows a box
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = global_timer_ns();
+    if ((i & 63) == 63 && (*abort_flag || global_timer_ns() - t0 > kWaitTimeoutNs)) return false;
+  }
+}
+
+__device__ __forceinline__ void mma_issue_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Arrive on the barrier at this shared-memory offset in both CTAs once the leader's MMAs have completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)0x3)
+      : "memory");
+}
+
+// Arrival on the leader's barrier by a warp that has read its accumulator (tcgen05.wait::ld):
+// nothing it wrote has to be seen, so no release at cluster scope, whose fence would wait.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// TMA loads into this CTA's shared memory that complete on the leader's barrier.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                        int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// 128 rows of a K-major operand half, or 128 columns of an MN-major one, at reduction index k
+// of matrix `at` of a 3-D map [at][rows][columns]: kBK of the reduction.
+template <bool MN>
+__device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row, int at) {
+#pragma unroll
+  for (int h = 0; h < (MN ? 2 : kBK / 64); ++h) {
+    if (MN) load_3d(dst + h * kBoxBytes * (kBK / 64), map, bar, row + 64 * h, k, at);
+    else load_3d(dst + h * 128 * 128, map, bar, k + 64 * h, row, at);
+  }
+}
+
+// A policy P has
+//   kAMN, kBMN                       an operand is MN-major
+//   kF16                             fp16 operands (else bf16)
+//   Params                           kernel parameter, with unsigned int* err
+//   Tile                             with int n (rows of B, a multiple of 32) and int blocks (of kBK) > 0
+//   setup(p, tables, lane) -> int    the number of tiles (one warp; it may fill the tables)
+//   tile(p, tables, i) -> Tile
+//   stage_bytes(p, t)                what both CTAs' loads of a stage complete
+//   load(p, t, rank, block, a, b, bar)
+//   epilogue(p, t, rank, sub, lane, tbase, release)   release(): the accumulator has been read
+template <class P>
+__global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(cluster_ctarank() & 1u);
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
+  auto bar_full = [&](int s) { return smem_u32(&bars[s]); };
+  auto bar_empty = [&](int s) { return smem_u32(&bars[kStages + s]); };
+  auto bar_tfull = [&](int b) { return smem_u32(&bars[2 * kStages + b]); };
+  auto bar_tempty = [&](int b) { return smem_u32(&bars[2 * kStages + kAccBufs + b]); };
+  const uint32_t bar_drain = smem_u32(&bars[2 * kStages + 2 * kAccBufs]);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::misc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
+  int* s_total = reinterpret_cast<int*>(smem + Smem::misc + 8);
+  int* tables = reinterpret_cast<int*>(smem + Smem::tables);
+
+  pdl_launch_dependents();
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < kAccBufs; ++b) {
+      mbar_init(bar_tfull(b), 1);
+      mbar_init(bar_tempty(b), 8);  // 4 epilogue warps in each CTA of the pair
+    }
+    mbar_init(bar_drain, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();  // what the previous kernel of the stream wrote
+  if (warp == 2) {
+    const int total = P::setup(p, tables, lane);
+    if (lane == 0) *s_total = total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const int total = *s_total;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      const uint32_t full0 = map_to_rank(bar_full(0), 0);
+      int s = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+      bool ok = true;
+      for (int i = pair; i < total && ok; i += pairs) {
+        const typename P::Tile t = P::tile(p, tables, i);
+        const uint32_t bytes = P::stage_bytes(p, t);
+        for (int kb = 0; kb < t.blocks; ++kb) {
+          if (!mbar_wait(bar_empty(s), phase ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(bar_full(s), bytes);
+          const uint32_t a = sbase + Smem::stage + s * kStageBytes;
+          P::load(p, t, rank, kb, a, a + kOperandBytes, full0 + (uint32_t)(s * 8));
+          issued_mask |= 1u << s;
+          issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (ok) {  // every stage this CTA filled has been read by the pair's MMAs before it exits
+        for (int b = 0; b < kStages; ++b)
+          if ((issued_mask >> b) & 1u && !mbar_wait(bar_empty(b), (issued_parity >> b) & 1u, s_abort)) ok = false;
+      }
+      if (!ok) {
+        flag_error(p.err, MOE_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        const uint64_t t0 = global_timer_ns();  // copies in flight complete on the leader's barrier: let them land
+        while (global_timer_ns() - t0 < kDrainTimeoutNs) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA (leader)
+    if (lane == 0 && leader) {
+      const uint32_t fmt = P::kF16 ? 0u : 1u;
+      const uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((P::kAMN ? 1u : 0u) << 15) |
+                            ((P::kBMN ? 1u : 0u) << 16) | ((uint32_t)(kTileM >> 4) << 24);
+      int s = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, issued_any = false;
+      for (int i = pair; i < total && ok; i += pairs) {
+        const typename P::Tile t = P::tile(p, tables, i);
+        const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
+        if (!mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kMaxN);
+        for (int kb = 0; kb < t.blocks; ++kb) {
+          if (!mbar_wait_cluster(bar_full(s), phase, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = sbase + Smem::stage + s * kStageBytes, b = a + kOperandBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_issue_pair(d, operand_desc<P::kAMN>(a, kk), operand_desc<P::kBMN>(b, kk), idesc, (kb | kk) != 0);
+          issued_any = true;
+          mma_commit_pair(bar_empty(s));
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(bar_tfull(acc));
+        if (++acc == kAccBufs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        flag_error(p.err, MOE_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        if (issued_any) {  // the MMAs in flight finish before tensor memory is freed
+          mma_commit_pair(bar_drain);
+          mbar_wait(bar_drain, 0, nullptr, kDrainTimeoutNs);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------- epilogue (both CTAs)
+    const int sub = warp & 3;  // TMEM lane quarter this warp may access
+    const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = pair; i < total; i += pairs) {
+      const typename P::Tile t = P::tile(p, tables, i);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull(acc), acc_phase, s_abort))) {
+        if (lane == 0) flag_error(p.err, MOE_DEVERR_TIMEOUT);
+        *s_abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kMaxN);
+      P::epilogue(p, t, rank, sub, lane, tbase, [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
+      });
+      if (++acc == kAccBufs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  // the pair meets, then frees its tensor memory together
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------- host
+
+// A map of 16-bit elements with boxes of 64 of them (128 bytes, 128B swizzle) along the first dimension.
+inline bool make_map(CUtensorMap* map, const void* base, bool f16, int nd, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [count][rows][cols], rows ld elements apart: boxes of box_rows rows of one matrix.
+inline bool make_map_3d(CUtensorMap* map, const void* base, bool f16, int64_t count, int64_t rows, int64_t cols,
+                        int64_t ld, int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  return make_map(map, base, f16, 3, dims, strides, box);
+}
+
+// tiles: at most so many.  pdl: the launch may begin before the stream's previous kernel ends.
+template <class P>
+cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int table_ints, bool pdl, cudaStream_t s) {
+  const int smem = Smem::tables + table_ints * 4 + 1024;
+  auto kern = pair_kernel<P>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(device_sm_count() / 2 * 2);
+  int pairs = 0;
+  e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+  if (e != cudaSuccess) return e;
+  if (pairs < 1) return cudaErrorNotSupported;
+  if (tiles < pairs) pairs = (int)tiles;
+  if (pairs < 1) return cudaSuccess;
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace pg
+}  // namespace moe

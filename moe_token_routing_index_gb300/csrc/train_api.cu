@@ -51,6 +51,56 @@ int check_rows(int a, int W) {
   return MOE_OK;
 }
 
+int check_gated(const void* x, const void* y, const void* w13, const void* w2, const int32_t* counts, int E, int a_max,
+                int D, int H, int activation, const void* z, const void* out) {
+  if (E < 1 || a_max < 0 || D < 1 || H < 1) return MOE_ERR_INVALID;
+  if (activation != MOE_ACT_SILU && activation != MOE_ACT_GELU) return MOE_ERR_INVALID;
+  if (E > 1024 || D % 16 != 0 || H % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (!w13 || !w2 || !counts) return MOE_ERR_INVALID;
+  if (a_max > 0 && (!x || !out)) return MOE_ERR_INVALID;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(z, 16) ||
+      !aligned(out, 16))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+constexpr int kMaxOrthoSide = 65536, kMaxOrthoBatch = 65535, kMaxOrthoSteps = 16;
+constexpr float kOrthoDefaults[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// Whether the iteration keeps every singular value of [0, 1] in the range of the kernels' fp16.
+bool coefficients_fit(const float* c, int steps) {
+  for (int i = 0; i < 3; ++i)
+    if (!isfinite(c[i])) return false;
+  for (int i = 0; i <= 1024; ++i) {
+    double s = i / 1024.0;
+    for (int k = 0; k < steps; ++k) {
+      const double p = (c[1] + c[2] * s * s) * s * s;
+      s = fabs((c[0] + p) * s);
+      if (!(fabs(p) < 32.0) || !(s < 4.0)) return false;
+    }
+  }
+  return true;
+}
+
+// Fills what both entry points share; g's sizes are set.
+int check_ortho(moe::OrthoArgs* g, int steps, const float* coefficients, float eps, void* ws, size_t ws_bytes) {
+  size_t need;
+  const int rc = moe_orthogonalize_workspace_size(g->B, g->N, g->K, &need);
+  if (rc != MOE_OK) return rc;
+  if (!float_dtype(g->dtype) || steps < 1 || steps > kMaxOrthoSteps) return MOE_ERR_INVALID;
+  if (!(eps >= 1e-12f) || !isfinite(eps)) return MOE_ERR_INVALID;
+  for (int i = 0; i < 3; ++i) g->coef[i] = coefficients ? coefficients[i] : kOrthoDefaults[i];
+  if (!coefficients_fit(g->coef, steps)) return MOE_ERR_INVALID;
+  g->steps = steps;
+  g->eps = eps;
+  if (need == 0) return MOE_OK;
+  if (!ws) return MOE_ERR_INVALID;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MOE_ERR_INVALID;
+  g->ws = ws;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -314,6 +364,122 @@ int moe_grouped_weight_grad(const void* dy, const void* x, const uint8_t* x_expo
   rc = moe::device_error_address(&g.err);
   if (rc != MOE_OK) return rc;
   return finish(moe::launch_weight_grad(g, stream));
+}
+
+int moe_gated_mlp(const void* x, const void* w13, const void* w2, const int32_t* counts, int E, int a_max, int D, int H,
+                  int activation, void* y, void* z, void* out, cudaStream_t stream) {
+  int rc = check_gated(x, y, w13, w2, counts, E, a_max, D, H, activation, z, out);
+  if (rc != MOE_OK) return rc;
+  if (a_max == 0) return MOE_OK;
+  if (!z) return MOE_ERR_INVALID;
+  moe::GatedArgs g{};
+  g.x = x;
+  g.w13 = w13;
+  g.w2 = w2;
+  g.counts = counts;
+  g.E = E;
+  g.a_max = a_max;
+  g.D = D;
+  g.H = H;
+  g.activation = activation;
+  g.y = y;
+  g.z = z;
+  g.out = out;
+  rc = moe::device_error_address(&g.err);
+  if (rc != MOE_OK) return rc;
+  return finish(moe::launch_gated_mlp(g, stream));
+}
+
+int moe_gated_mlp_backward(const void* dout, const void* y, const uint8_t* y_exponents, const void* w13, const void* w2,
+                           const int32_t* counts, int E, int a_max, int D, int H, int activation, void* dy, void* z,
+                           void* dx, cudaStream_t stream) {
+  int rc = check_gated(dout, y, w13, w2, counts, E, a_max, D, H, activation, z, dx);
+  if (rc != MOE_OK) return rc;
+  if (a_max == 0) return MOE_OK;
+  if (!y || !dy) return MOE_ERR_INVALID;
+  if (!aligned(dy, 16)) return MOE_ERR_UNSUPPORTED;
+  moe::GatedArgs g{};
+  g.x = dout;
+  g.w13 = w13;
+  g.w2 = w2;
+  g.counts = counts;
+  g.E = E;
+  g.a_max = a_max;
+  g.D = D;
+  g.H = H;
+  g.activation = activation;
+  g.y = const_cast<void*>(y);
+  g.exponents = y_exponents;
+  g.dy = dy;
+  g.z = z;
+  g.out = dx;
+  rc = moe::device_error_address(&g.err);
+  if (rc != MOE_OK) return rc;
+  return finish(moe::launch_gated_mlp_backward(g, stream));
+}
+
+int moe_orthogonalize_workspace_size(int B, int N, int K, size_t* bytes) {
+  if (!bytes || B < 0 || N < 0 || K < 0) return MOE_ERR_INVALID;
+  if (B > kMaxOrthoBatch || N > kMaxOrthoSide || K > kMaxOrthoSide) return MOE_ERR_UNSUPPORTED;
+  *bytes = B == 0 || N == 0 || K == 0 ? 0 : moe::orthogonalize_workspace_bytes(B, N, K);
+  return MOE_OK;
+}
+
+int moe_orthogonalize(const void* g, int dtype, int64_t batch_stride, int64_t row_stride, int B, int N, int K, int steps,
+                      const float* coefficients, float eps, float scale, void* out, void* ws, size_t ws_bytes,
+                      cudaStream_t stream) {
+  moe::OrthoArgs a{};
+  a.g = g;
+  a.dtype = dtype;
+  a.batch_stride = batch_stride;
+  a.row_stride = row_stride;
+  a.B = B;
+  a.N = N;
+  a.K = K;
+  int rc = check_ortho(&a, steps, coefficients, eps, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  if (!isfinite(scale)) return MOE_ERR_INVALID;
+  if (B == 0 || N == 0 || K == 0) return MOE_OK;
+  if (!g || !out || row_stride < 0 || batch_stride < 0) return MOE_ERR_INVALID;
+  if (!aligned(g, dtype_bytes(dtype)) || !aligned(out, 2)) return MOE_ERR_UNSUPPORTED;
+  a.out = out;
+  a.scale = scale;
+  rc = moe::device_error_address(&a.err);
+  if (rc != MOE_OK) return rc;
+  return finish(moe::launch_orthogonalize(a, stream));
+}
+
+int moe_muon_update(void* w, int w_dtype, const void* grad, int grad_dtype, float* momentum, int B, int N, int K,
+                    float mu, int nesterov, float lr, const float* lr_scale, float weight_decay, int steps,
+                    const float* coefficients, float eps, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  moe::OrthoArgs a{};
+  a.g = grad;
+  a.dtype = grad_dtype;
+  a.batch_stride = (int64_t)N * K;
+  a.row_stride = K;
+  a.B = B;
+  a.N = N;
+  a.K = K;
+  int rc = check_ortho(&a, steps, coefficients, eps, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  if (!float_dtype(w_dtype) || !isfinite(lr) || !isfinite(weight_decay) || !(mu >= 0.0f && mu < 1.0f))
+    return MOE_ERR_INVALID;
+  if (B == 0 || N == 0 || K == 0) return MOE_OK;
+  if (!w || !grad || !momentum) return MOE_ERR_INVALID;
+  if (!aligned(w, dtype_bytes(w_dtype)) || !aligned(grad, dtype_bytes(grad_dtype)) || !aligned(momentum, 4))
+    return MOE_ERR_UNSUPPORTED;
+  a.momentum = momentum;
+  a.mu = mu;
+  a.nesterov = nesterov != 0;
+  a.update = true;
+  a.out = w;
+  a.w_dtype = w_dtype;
+  a.scale = lr;
+  a.decay = lr * weight_decay;
+  a.lr = lr_scale;
+  rc = moe::device_error_address(&a.err);
+  if (rc != MOE_OK) return rc;
+  return finish(moe::launch_orthogonalize(a, stream));
 }
 
 }  // extern "C"

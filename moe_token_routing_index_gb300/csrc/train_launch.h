@@ -97,4 +97,44 @@ struct WeightGradArgs {
 size_t weight_grad_workspace_bytes(int E, int a_max, int N, int K, bool packed);
 cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t s);
 
+// The gated block: forward from x (writes y, z, out), backward from x = dout and y (writes dy, z, out = dx).
+struct GatedArgs {
+  const void* x;
+  const void* w13;
+  const void* w2;
+  const int32_t* counts;
+  int E, a_max, D, H, activation;
+  void* y;                   // forward: nullable; backward: bf16, or codes with exponents
+  const uint8_t* exponents;  // backward only
+  void* dy;                  // backward only
+  void* z;                   // backward: nullable
+  void* out;
+  unsigned int* err;
+};
+
+cudaError_t launch_gated_mlp(const GatedArgs& a, cudaStream_t s);
+cudaError_t launch_gated_mlp_backward(const GatedArgs& a, cudaStream_t s);
+
+struct OrthoArgs {
+  const void* g;
+  int64_t batch_stride, row_stride;
+  int dtype, B, N, K;
+  float* momentum;           // nullable
+  float mu;
+  int nesterov;
+  int steps;
+  float coef[3];
+  float eps;
+  bool update;               // out are weights: w = (1 - lr decay) w - lr scale X; else out = scale X, bf16
+  void* out;
+  int w_dtype;
+  float scale, decay;
+  const float* lr;           // nullable: 1
+  void* ws;
+  unsigned int* err;
+};
+
+size_t orthogonalize_workspace_bytes(int B, int N, int K);
+cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,156 @@
+"""Refusals of the gated block's and the orthogonalised update's entry points and wrappers, and the streams
+that their calls take their memory from.  Nothing is launched, so this runs without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from tests import gated_ref as ref
+from tests.test_streams import BF16, F32, I32, U8, World, _t, _tensors, mb  # noqa: F401  (mb: a fixture)
+from tests.test_train_abi import FAKE, ODD, _sweep
+
+OFF8 = ctypes.c_void_p(0x1008)
+NAN, INF = float("nan"), float("inf")
+
+
+def test_gated_refusals(mb):  # noqa: F811
+    inv, uns, ok = mb.MOE_ERR_INVALID, mb.MOE_ERR_UNSUPPORTED, mb.MOE_OK
+    fwd = dict(x=FAKE, w13=FAKE, w2=FAKE, counts=FAKE, E=4, a=64, D=64, H=32, act=0, y=None, z=FAKE, out=FAKE,
+               stream=None)
+    common = [(dict(w13=None), inv), (dict(w2=None), inv), (dict(counts=None), inv), (dict(E=0), inv), (dict(a=-1), inv),
+              (dict(D=0), inv), (dict(H=0), inv), (dict(H=-16), inv), (dict(act=2), inv), (dict(act=-1), inv),
+              (dict(E=1025), uns), (dict(D=72), uns), (dict(H=40), uns), (dict(w13=ODD), uns), (dict(w2=OFF8), uns),
+              (dict(z=OFF8), uns), (dict(y=OFF8), uns)]
+    _sweep(mb, mb.library().moe_gated_mlp, fwd, common + [
+        (dict(x=None), inv), (dict(out=None), inv), (dict(z=None), inv), (dict(x=OFF8), uns), (dict(out=OFF8), uns),
+        (dict(a=0, x=None, out=None, z=None), ok)])
+    bwd = dict(dout=FAKE, y=FAKE, exps=None, w13=FAKE, w2=FAKE, counts=FAKE, E=4, a=64, D=64, H=32, act=1, dy=FAKE,
+               z=None, dx=FAKE, stream=None)
+    _sweep(mb, mb.library().moe_gated_mlp_backward, bwd, common + [
+        (dict(dout=None), inv), (dict(y=None), inv), (dict(dy=None), inv), (dict(dx=None), inv), (dict(dy=OFF8), uns),
+        (dict(dout=OFF8), uns), (dict(dx=OFF8), uns), (dict(a=0, dout=None, y=None, dy=None, dx=None), ok)])
+
+
+def test_orthogonalize_refusals(mb):  # noqa: F811
+    inv, uns, ok = mb.MOE_ERR_INVALID, mb.MOE_ERR_UNSUPPORTED, mb.MOE_OK
+    n = ctypes.c_size_t(0)
+    size = mb.library().moe_orthogonalize_workspace_size
+    assert size(-1, 8, 8, ctypes.byref(n)) == inv and size(1, 8, 8, None) == inv
+    assert size(1, 65537, 8, ctypes.byref(n)) == uns and size(65536, 8, 8, ctypes.byref(n)) == uns
+    assert size(0, 8, 8, ctypes.byref(n)) == ok and n.value == 0
+    assert size(2, 40, 56, ctypes.byref(n)) == ok and n.value > 0
+    need = n.value
+    c3 = lambda *v: (ctypes.c_float * 3)(*v)
+    shared = [(dict(B=-1), inv), (dict(N=-1), inv), (dict(steps=0), inv), (dict(steps=17), inv), (dict(eps=0.0), inv),
+              (dict(eps=NAN), inv), (dict(eps=INF), inv), (dict(ws=None), inv), (dict(nws=need - 1), mb.MOE_ERR_WORKSPACE),
+              (dict(ws=ctypes.c_void_p(0x1010)), inv), (dict(K=65537), uns), (dict(coef=c3(NAN, 0, 0)), inv),
+              (dict(coef=c3(5.0, 0.0, 0.0)), inv),              # leaves [0, 4)
+              (dict(coef=c3(1.9, 0.0, 0.0), steps=3), inv)]   # grows step by step
+    one = dict(g=FAKE, dtype=0, bs=40 * 56, rs=56, B=2, N=40, K=56, steps=5, coef=None, eps=1e-7, scale=1.0, out=FAKE,
+               ws=FAKE, nws=need, stream=None)
+    _sweep(mb, mb.library().moe_orthogonalize, one, shared + [
+        (dict(g=None), inv), (dict(out=None), inv), (dict(dtype=2), inv), (dict(scale=INF), inv), (dict(bs=-1), inv),
+        (dict(rs=-1), inv), (dict(g=ODD), uns), (dict(out=ODD), uns), (dict(N=0, g=None), ok)])
+    two = dict(w=FAKE, wd=0, g=FAKE, gd=1, m=FAKE, B=2, N=40, K=56, mu=0.9, nesterov=1, lr=0.1, lrs=None, decay=0.0,
+               steps=5, coef=None, eps=1e-7, ws=FAKE, nws=need, stream=None)
+    _sweep(mb, mb.library().moe_muon_update, two, shared + [
+        (dict(w=None), inv), (dict(g=None), inv), (dict(m=None), inv), (dict(wd=2), inv), (dict(gd=2), inv),
+        (dict(mu=1.0), inv), (dict(mu=-0.1), inv), (dict(mu=NAN), inv), (dict(lr=NAN), inv), (dict(decay=INF), inv),
+        (dict(w=ODD), uns), (dict(g=ctypes.c_void_p(0x1002)), uns), (dict(m=ctypes.c_void_p(0x1002)), uns),
+        (dict(B=0, w=None), ok)])
+
+
+def _calls(mb):  # noqa: F811
+    E, D, H, a = 4, 64, 32, 16
+    x, w13, w2, counts = _t(BF16, a, D), _t(BF16, E, 2 * H, D), _t(BF16, E, D, H), _t(I32, E)
+    return dict(gated=lambda **s: mb.moe_gated_mlp(x, w13, w2, counts, **s),
+                gated_grad=lambda **s: mb.moe_gated_mlp_backward(x, _t(BF16, a, 2 * H), w13, w2, counts, **s),
+                orthogonal=lambda **s: mb.moe_orthogonalize(w13, **s),
+                update=lambda **s: mb.moe_muon_update(w13, w13, _t(F32, E, 2 * H, D), lr=0.1, **s))
+
+
+@pytest.mark.parametrize("name", ["gated", "gated_grad", "orthogonal", "update"])
+def test_a_call_takes_its_memory_from_the_stream_it_runs_on(mb, monkeypatch, name):  # noqa: F811
+    world = World(monkeypatch, mb)
+    result = _calls(mb)[name](stream=world.side)
+    assert [s for _, s in world.launched] == [world.side.cuda_stream]
+    assert world.allocated and {s.cuda_stream for _, s in world.allocated} == {world.side.cuda_stream}
+    made = {id(t) for t, _ in world.allocated}
+    got = [t for t in _tensors(mb, result) if id(t) in made]
+    assert all(world.main in getattr(t, "recorded", []) for t in got) and (got or name == "update")
+    world.allocated.clear()
+    _calls(mb)[name]()
+    assert {s.cuda_stream for _, s in world.allocated} == {world.main.cuda_stream}
+
+
+def test_wrappers_refuse_what_does_not_fit(mb, monkeypatch):  # noqa: F811
+    world = World(monkeypatch, mb)
+    E, D, H, a = 4, 64, 32, 16
+    x, w13, w2, counts = _t(BF16, a, D), _t(BF16, E, 2 * H, D), _t(BF16, E, D, H), _t(I32, E)
+    y = _t(BF16, a, 2 * H)
+    half = mb.Checkpoint(_t(torch.float8_e4m3fn, a, 2 * H), _t(U8, a, 1))
+    wrong = [
+        lambda: mb.moe_gated_mlp(x, w13, _t(BF16, E, H, D), counts),
+        lambda: mb.moe_gated_mlp(x, _t(BF16, E, 2 * H + 1, D), w2, counts),
+        lambda: mb.moe_gated_mlp(x, w13[0], w2, counts),
+        lambda: mb.moe_gated_mlp(x, w13, w2, _t(I32, E - 1)),
+        lambda: mb.moe_gated_mlp(x, w13, w2, _t(I32, 1, E)),
+        lambda: mb.moe_gated_mlp(_t(BF16, a, D + 16), w13, w2, counts),
+        lambda: mb.moe_gated_mlp(x, w13, w2, counts, y=_t(BF16, a, H)),
+        lambda: mb.moe_gated_mlp(x, w13, w2, counts, out=_t(BF16, a + 1, D)),
+        lambda: mb.moe_gated_mlp(x.t().contiguous().as_subclass(type(x)).t(), w13, w2, counts),
+        lambda: mb.moe_gated_mlp_backward(x, _t(BF16, a, H), w13, w2, counts),
+        lambda: mb.moe_gated_mlp_backward(x, half, w13, w2, counts),
+        lambda: mb.moe_gated_mlp_backward(x, y, w13, w2, counts, dy=_t(BF16, a, H)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8, 8), coefficients=(1.0, 2.0)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8, 8), out=_t(BF16, 8, 9)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8, 6).t()),
+        lambda: mb.moe_muon_update(_t(F32, 8, 8), _t(F32, 8, 9), _t(F32, 8, 8), lr=0.1),
+        lambda: mb.moe_muon_update(_t(F32, 8, 8), _t(F32, 8, 8), _t(F32, 1, 8, 8), lr=0.1),
+        lambda: mb.moe_muon_update(_t(F32, 8, 8), _t(F32, 8, 8), _t(F32, 8, 8), lr=0.1, lr_scale=_t(F32, 0)),
+        lambda: mb.moe_muon_update(_t(F32, 8, 6).t(), _t(F32, 6, 8), _t(F32, 6, 8), lr=0.1),
+    ]
+    for call in wrong:
+        with pytest.raises(ValueError):
+            call()
+    types = [
+        lambda: mb.moe_gated_mlp(x.float(), w13, w2, counts),
+        lambda: mb.moe_gated_mlp(x, w13.float(), w2, counts),
+        lambda: mb.moe_gated_mlp(x, w13, w2, counts.long()),
+        lambda: mb.moe_gated_mlp(torch.ones(a, D, dtype=BF16), w13, w2, counts),
+        lambda: mb.moe_gated_mlp_backward(x, y.float(), w13, w2, counts),
+        lambda: mb.moe_orthogonalize(_t(torch.float16, 8, 8)),
+        lambda: mb.moe_orthogonalize(torch.ones(8, 8)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8, 8), out=_t(F32, 8, 8)),
+        lambda: mb.moe_orthogonalize(_t(F32, 8, 8), workspace=torch.ones(1 << 20, dtype=U8)),
+        lambda: mb.moe_muon_update(_t(F32, 8, 8), _t(F32, 8, 8), _t(BF16, 8, 8), lr=0.1),
+    ]
+    for call in types:
+        with pytest.raises(TypeError):
+            call()
+    assert not world.launched
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_reference_gradient_against_differences(kind):
+    """The formula of the backward against central differences of the forward, in 64 bits."""
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)
+    a, E, D, H, counts = 5, 2, 16, 16, [3, 2]
+    x, w13, w2, dout = r(a, D), r(E, 2 * H, D) / 4, r(E, D, H) / 4, r(a, D)
+    _, y, _, _ = ref.forward(x, w13, w2, counts, kind)
+    dx, dy, z, *_ = ref.backward(dout, y, w13, w2, counts, kind)
+    loss = lambda x_: float((ref.forward(x_, w13, w2, counts, kind)[0] * dout).sum())
+    for _ in range(4):
+        d = r(a, D)
+        want = (loss(x + 1e-5 * d) - loss(x - 1e-5 * d)) / 2e-5
+        assert abs(float((dx * d).sum()) - want) <= 1e-7 * (1 + abs(want))
+
+
+def test_reference_iteration_reaches_orthonormal_rows():
+    g = torch.randn(1, 12, 20, generator=torch.Generator().manual_seed(1))
+    x = ref.orthogonalize(g, 40, (1.5, -0.5, 0.0))
+    assert float((x @ x.transpose(1, 2) - torch.eye(12).double()).abs().max()) < 1e-10
+    u, _, vh = torch.linalg.svd(g[0].double(), full_matrices=False)
+    assert float((x[0] - u @ vh).abs().max()) < 1e-10

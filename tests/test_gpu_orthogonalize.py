@@ -1,0 +1,190 @@
+"""Newton-Schulz orthogonalisation and the momentum update against 64-bit forms.
+
+One step is held element by element to the bound of its roundings.  Over several steps the
+worst case grows with the iteration's largest slope to the power of the steps and says
+nothing, so five steps are held to what the same roundings do in 64 bits: no further from the
+exact result than 1.5 times as far as that (its roundings fall otherwise where sums differ
+in their last bits), plus the half bf16 step of the output."""
+import pytest
+import torch
+
+from tests import gated_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+SHAPES = [(1, 1, 1), (2, 1, 7), (3, 17, 16), (1, 33, 257), (2, 300, 64), (1, 256, 256), (2, 517, 263), (1, 128, 1024),
+          (1, 1024, 136), (5, 64, 96), (1, 257, 513)]
+
+
+def _mb():
+    from moe_token_routing_index_gb300 import binding
+
+    return binding
+
+
+def _g(B, N, K, dtype, seed=0, strong=True):
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(B, N, K, generator=g)
+    if strong:
+        r = min(4, N, K)
+        v = 0.2 * v + torch.randn(B, N, r, generator=g) @ torch.randn(B, r, K, generator=g)
+    return (1e-3 * v).to(dtype)
+
+
+def _check_five(got, g, scale=1.0, steps=5):
+    exact = ref.orthogonalize(g, steps) * scale
+    half = ref.orthogonalize(g, steps, half=True) * scale
+    for b in range(len(g)):
+        norm = float(exact[b].norm())
+        off = float((got[b].cpu().double() - exact[b]).norm())
+        most = 1.5 * float((half[b] - exact[b]).norm()) + ref.HALF16 * norm + 1e-30
+        assert off <= most, f"matrix {b}: {off / norm:.3e} of its norm, allowed {most / norm:.3e}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,K", SHAPES)
+def test_one_step(B, N, K, dtype):
+    mb = _mb()
+    g = _g(B, N, K, dtype)
+    got = mb.moe_orthogonalize(g.cuda(), steps=1).cpu().double()
+    want, bound = ref.one_step_error(g)
+    over = (got - want).abs() - bound
+    assert float(over.max()) <= 0, f"{float(over.max()):.3e} over its bound"
+    assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("strong", [True, False])
+@pytest.mark.parametrize("B,N,K", SHAPES)
+def test_five_steps(B, N, K, strong):
+    mb = _mb()
+    g = _g(B, N, K, F32, seed=1, strong=strong)
+    _check_five(mb.moe_orthogonalize(g.cuda()), g)
+    _check_five(mb.moe_orthogonalize(g.cuda(), scale=-0.5), g, -0.5)
+    assert mb.device_error() == 0
+
+
+def test_two_dimensions_strides_and_odd_bases():
+    mb = _mb()
+    big = _g(3, 70, 131, F32, seed=2).cuda()
+    rows = big[:, :65, 3:100]                       # rows and matrices apart, base not 16-byte aligned
+    whole = mb.moe_orthogonalize(rows.contiguous())
+    assert torch.equal(mb.moe_orthogonalize(rows), whole)
+    assert torch.equal(mb.moe_orthogonalize(rows[1]), whole[1])
+    same = rows[:1].expand(3, -1, -1)               # one matrix three times: stride 0
+    assert torch.equal(mb.moe_orthogonalize(same), whole[:1].expand(3, -1, -1))
+    flat = torch.full((65 * 97 + 2,), 7.0, dtype=BF16, device="cuda")
+    out = flat[1:-1].view(65, 97)
+    mb.moe_orthogonalize(rows[0], out=out)
+    assert torch.equal(out, whole[0]) and float(flat[0]) == 7 and float(flat[-1]) == 7
+    half = big.to(BF16)[:, :65, 3:100]
+    assert torch.equal(mb.moe_orthogonalize(half), mb.moe_orthogonalize(half.contiguous()))
+    assert mb.device_error() == 0
+
+
+def test_zeros_nan_infinities_and_extreme_sizes():
+    """Each matrix for itself: zeros stay zeros, what is not finite is NaN in its own matrix, and the size
+    of a matrix does not matter from 1e-4 of 1/eps to the largest fp32 (the norm is far above both)."""
+    mb = _mb()
+    g = _g(6, 40, 56, F32, seed=3)
+    g[1] = 0
+    g[2, 3, 5] = float("nan")
+    g[4, 0, 0] = float("inf")
+    got = mb.moe_orthogonalize(g.cuda())
+    alone = mb.moe_orthogonalize(g[[0, 3, 5]].cuda())
+    assert torch.equal(got[[0, 3, 5]], alone)
+    assert bool((got[1] == 0).all())
+    assert bool(torch.isnan(got[2]).all()) and bool(torch.isnan(got[4]).all())
+    # a power of two changes no rounding but eps's part, which is 1e-7 of the norm at most
+    base = (g[0] / g[0].abs().max()).to(F32)
+    for e in (0, 40, 100, 126):
+        _check_five(mb.moe_orthogonalize((base * 2.0 ** e)[None].cuda()), (base * 2.0 ** e)[None].double())
+    assert mb.device_error() == 0
+
+
+def test_other_coefficients_and_steps():
+    mb = _mb()
+    cubic = (1.5, -0.5, 0.0)
+    g = _g(2, 48, 80, F32, seed=4, strong=False)
+    for steps in (1, 3, 12, 16):
+        got = mb.moe_orthogonalize(g.cuda(), steps=steps, coefficients=cubic).cpu().double()
+        exact = ref.orthogonalize(g, steps, cubic)
+        half = ref.orthogonalize(g, steps, cubic, half=True)
+        assert float((got - exact).norm()) <= 1.5 * float((half - exact).norm()) + ref.HALF16 * float(exact.norm())
+    # 16 steps of the cubic reach the nearest matrix with orthonormal rows: bf16 rounding and fp16 operands are left
+    gram = got @ got.transpose(1, 2)
+    assert float((gram - torch.eye(48).double()).abs().max()) < 0.02
+
+
+@pytest.mark.parametrize("w_dtype,g_dtype", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("B,N,K,nesterov", [(1, 1, 3, True), (2, 40, 56, False), (3, 130, 33, True), (1, 300, 520, True)])
+def test_update(B, N, K, nesterov, w_dtype, g_dtype):
+    mb = _mb()
+    gen = torch.Generator().manual_seed(5)
+    w = (0.02 * torch.randn(B, N, K, generator=gen)).to(w_dtype)
+    g = _g(B, N, K, g_dtype, seed=6)
+    m = (2 * _g(B, N, K, F32, seed=7)).float()
+    mu, lr, decay = 0.9, 0.03, 0.1
+    wd, md = w.cuda(), m.cuda()
+    scale = torch.tensor([0.5], device="cuda")
+    assert mb.moe_muon_update(wd, g.cuda(), md, lr=lr, mu=mu, nesterov=nesterov, weight_decay=decay, lr_scale=scale) is wd
+    m64 = mu * m.double() + g.double()
+    assert bool(((md.cpu().double() - m64).abs() <= 2.0 ** -23 * (m64.abs() + mu * m.double().abs())).all())
+    u = g.double() + mu * m64 if nesterov else m64
+    exact, half = ref.orthogonalize(u), ref.orthogonalize(u, half=True)
+    want = (1 - 0.5 * lr * decay) * w.double() - 0.5 * lr * exact
+    step = 2.0 ** -24 if w_dtype == F32 else ref.HALF16
+    for b in range(B):
+        off = float((wd[b].cpu().double() - want[b]).norm())
+        most = 0.5 * lr * (1.5 * float((half[b] - exact[b]).norm()) + 1e-5 * float(exact[b].norm()))
+        assert off <= most + 4 * step * float(want[b].norm()) if w_dtype == F32 else off <= most + 1.01 * step * float(
+            want[b].norm())
+    assert mb.device_error() == 0
+
+
+def test_update_of_nothing_moves_only_by_decay():
+    mb = _mb()
+    w = torch.randn(2, 20, 30, generator=torch.Generator().manual_seed(8)).cuda()
+    before = w.clone()
+    zero = torch.zeros_like(w)
+    mb.moe_muon_update(w, zero, zero.clone(), lr=0.1, weight_decay=0.0)
+    assert torch.equal(w, before)
+    mb.moe_muon_update(w, zero, zero.clone(), lr=0.5, weight_decay=0.5)
+    assert torch.equal(w, before * 0.75)
+
+
+def test_same_bytes_again_captured_and_on_another_stream():
+    mb = _mb()
+    g = _g(2, 300, 200, BF16, seed=9).cuda()
+    w0 = torch.randn(2, 300, 200, device="cuda").to(BF16)
+    m0 = torch.randn(2, 300, 200, device="cuda")
+    out = mb.moe_orthogonalize(g)
+    w, m = w0.clone(), m0.clone()
+    mb.moe_muon_update(w, g, m, lr=0.1)
+    side = torch.cuda.Stream()
+    w2, m2 = w0.clone(), m0.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    out2 = mb.moe_orthogonalize(g, stream=side)
+    mb.moe_muon_update(w2, g, m2, lr=0.1, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(w, w2) and torch.equal(m, m2)
+    # two captured graphs with a workspace of their own each, replayed by turns
+    graphs = []
+    for k in range(2):
+        wk, mk, lr = w0.clone(), m0.clone(), torch.tensor([1.0], device="cuda")
+        ws = torch.empty(mb.moe_orthogonalize_workspace_size(2, 300, 200), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mb.moe_muon_update(wk, g, mk, lr=0.1, lr_scale=lr, workspace=ws)
+        graphs.append((graph, wk, mk, lr))
+    for graph, wk, mk, _ in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(wk, w) and torch.equal(mk, m) for _, wk, mk, _ in graphs)
+    graph, wk, mk, lr = graphs[0]
+    lr.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(wk, w) and not torch.equal(mk, m)      # a rate of zero: the momentum moves alone
+    assert mb.device_error() == 0
