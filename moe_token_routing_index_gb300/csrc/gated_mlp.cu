@@ -22,9 +22,6 @@ namespace {
 
 using namespace pg;
 
-constexpr int kHeights = 4;  // boxes of 16, 32, 64 and 128 routed rows
-__host__ __device__ constexpr int box_rows(int h) { return 16 << h; }
-
 struct Rows {           // the routed rows and how the tiles walk them
   CUtensorMap w;
   CUtensorMap x[kHeights];
@@ -32,13 +29,12 @@ struct Rows {           // the routed rows and how the tiles walk them
   int E, a_max;
   int mt;               // tiles along a product's output columns
   int band;             // row tiles of a band of the tile order
-  int blocks;           // of the reduction
+  int k;                // the reduction's length
 };
 
 struct RowTile {
-  int n, blocks;
+  int n, k;
   int m, expert, row0, rows;  // tile along the columns; rows: those of the tile that are the expert's
-  int height;
 };
 
 // tables: the experts' first row tiles [E + 1] and rows [E + 1].  One warp; counts as in the
@@ -112,37 +108,35 @@ __device__ __forceinline__ RowTile locate_rows(const Rows& p, const int* tables,
   t.row0 = row_off[lo] + rt * part;
   t.rows = min(part, c - rt * part);
   t.n = (t.rows + 31) / 32 * 32;
-  t.blocks = p.blocks;
-  const int half = t.n / 2;
-  t.height = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+  t.k = p.k;
   return t;
 }
 
 __device__ __forceinline__ uint32_t row_stage_bytes(const RowTile& t) {
-  return 2u * (uint32_t)(kOperandBytes + box_rows(t.height) * 128 * (kBK / 64));
+  return 2u * (uint32_t)(kOperandBytes + t.n / 2 * 128 * (kBK / 64));
 }
 
 __device__ __forceinline__ void load_rows(const Rows& p, const RowTile& t, int rank, int block, uint32_t dst,
                                           uint32_t bar) {
   const int row = t.row0 + rank * (t.n / 2), k = block * kBK;
-  // (each height's by itself: a map chosen by an index slows the loads)
-  auto load = [&](const CUtensorMap* map) {
+  const CUtensorMap* map = &p.x[t.n / 32 - 1];
 #pragma unroll
-    for (int h = 0; h < kBK / 64; ++h) load_2d(dst + h * 128 * 128, map, bar, k + 64 * h, row);
-  };
-  if (t.height == 3) load(&p.x[3]);
-  else if (t.height == 2) load(&p.x[2]);
-  else if (t.height == 1) load(&p.x[1]);
-  else load(&p.x[0]);
+  for (int h = 0; h < kBK / 64; ++h) load_2d(dst + h * 128 * 128, map, bar, k + 64 * h, row);
 }
 
 // ------------------------------------------------------------- activations
 
 // act(v) = v * sigmoid(u(v)): u = v (SiLU), or sqrt(8 / pi) (v + 0.044715 v^3) (GELU, tanh form).
+__device__ __forceinline__ float rcp(float v) {  // to 1 ulp; 0 for infinity
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float gate_of(float v) {
   const float u = ACT == MOE_ACT_SILU ? v : 1.5957691216f * v * fmaf(0.044715f * v, v, 1.0f);
-  return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-u)));
+  return rcp(1.0f + __expf(-u));
 }
 
 template <int ACT>
@@ -156,8 +150,12 @@ __device__ __forceinline__ void act_slope(float v, float* f, float* slope) {
   const float p = gate_of<ACT>(v);
   *f = v * p;
   const float q = *f * (1.0f - p);
-  const float du = ACT == MOE_ACT_SILU ? 1.0f : fmaf(0.2140644488f * v, v, 1.5957691216f);
-  *slope = q == 0.0f ? p : fmaf(q, du, p);  // (du may be infinite where q has vanished)
+  if (ACT == MOE_ACT_SILU) {
+    *slope = p + q;
+  } else {
+    const float du = fmaf(0.2140644488f * v, v, 1.5957691216f);
+    *slope = q == 0.0f ? p : fmaf(q, du, p);  // (du may be infinite where q has vanished)
+  }
 }
 
 // ------------------------------------------------------- the four products
@@ -186,34 +184,37 @@ struct GatedForward {
       load_5d(a + h * 128 * 128, &p.rows.w, bar, block * kBK + 64 * h, 0, 0, t.m * 8 + rank * 4, t.expert);
     load_rows(p.rows, t, rank, block, b, bar);
   }
-  template <class Release>
-  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int lane, uint32_t tbase,
-                                  Release release) {
+  template <class Wait, class Release>
+  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int group, int lane, uint32_t tbase,
+                                  Wait wait, Release release) {
     const int f = t.m * 128 + rank * 64 + sub * 16 + (lane & 15);
     const bool first = lane < 16, keep = f < p.H;  // (H is a multiple of 16: all of a half-warp)
     const int64_t H = p.H;
     __nv_bfloat16* z = p.z + (int64_t)t.row0 * H + f;
     __nv_bfloat16* y = p.y + (int64_t)t.row0 * 2 * H + f;
-    for (int c = 0; c < t.rows; c += 32) {
-      float v[32];
-      tmem_ld32(tbase + c, v);
+    auto use = [&](int c, const NoSource&, const float* v) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < kChunk / 2; ++j) {
         // the first half-warp takes row 2j, the second row 2j + 1
         const float other = __shfl_xor_sync(0xffffffffu, first ? v[2 * j + 1] : v[2 * j], 16);
         const float y0 = first ? v[2 * j] : other, y1 = first ? other : v[2 * j + 1];
         const int r = c + 2 * j + (first ? 0 : 1);
+        const float zr = act<ACT>(y0) * y1;
         if (keep && r < t.rows) {
-          z[r * H] = __float2bfloat16_rn(act<ACT>(y0) * y1);
+          z[r * H] = __float2bfloat16_rn(zr);
           if (p.y) {
             y[r * 2 * H] = __float2bfloat16_rn(y0);
             y[r * 2 * H + H] = __float2bfloat16_rn(y1);
           }
         }
       }
-    }
-    release();
+    };
+    by_chunks<NoSource>(t.rows, group, tbase, [](int, NoSource&) {}, use, wait, release);
   }
+};
+
+struct Kept {  // y0 and y1 of a lane's share of a chunk: two bf16, or two codes and their exponent byte
+  uint32_t y0[kChunk / 2], y1[kChunk / 2];
 };
 
 // dy and z from dz = dout w2 and the kept y (bf16, or a checkpoint's codes and exponents).
@@ -240,47 +241,62 @@ struct GatedGrad {
     load_half<true>(a, &p.rows.w, bar, block * kBK, t.m * kTileM + rank * kHalfM, t.expert);
     load_rows(p.rows, t, rank, block, b, bar);
   }
-  template <class Release>
-  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int lane, uint32_t tbase,
-                                  Release release) {
-    const int f = t.m * kTileM + rank * kHalfM + sub * 32 + lane;
-    const int64_t H = p.H, at = (int64_t)t.row0 * 2 * H + f;
-    const bool keep = f < p.H;
+  template <class Wait, class Release>
+  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int group, int lane, uint32_t tbase,
+                                  Wait wait, Release release) {
+    // two neighbouring columns of y, of every second row (H is a multiple of 16: both or none)
+    const int f = t.m * kTileM + rank * kHalfM + sub * 32 + (lane & 30);
+    const bool odd = lane & 1, keep = f < p.H;
+    const int fc = keep ? f : 0;  // lanes without columns read what others read
+    const int64_t H = p.H;
     const int nb = (p.H + 127) / 128;
-    __nv_bfloat16* dy = p.dy + at;
-    __nv_bfloat16* z = p.z + (int64_t)t.row0 * H + f;
-    for (int c = 0; c < t.rows; c += 32) {
-      float y0[32], y1[32], v[32];
+    auto load = [&](int c, Kept& s) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        y0[i] = y1[i] = 0.0f;
-        if (keep && c + i < t.rows) {
-          const int64_t o = at + (int64_t)(c + i) * 2 * H;
-          if (CODES) {
-            const uint8_t* e = p.exponents + (int64_t)(t.row0 + c + i) * 2 * nb + f / 128;
-            const __nv_fp8_e4m3* q = static_cast<const __nv_fp8_e4m3*>(p.y) + o;
-            y0[i] = static_cast<float>(q[0]) * __uint_as_float((uint32_t)__ldg(e) << 23);
-            y1[i] = static_cast<float>(q[H]) * __uint_as_float((uint32_t)__ldg(e + nb) << 23);
-          } else {
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.y) + o;
-            y0[i] = __bfloat162float(__ldg(q));
-            y1[i] = __bfloat162float(__ldg(q + H));
-          }
+      for (int j = 0; j < kChunk / 2; ++j) {
+        const int64_t r = t.row0 + min(c + 2 * j + odd, t.rows - 1);
+        if (CODES) {
+          const uint8_t* e = p.exponents + r * 2 * nb + fc / 128;
+          const uint8_t* q = static_cast<const uint8_t*>(p.y) + r * 2 * H + fc;
+          s.y0[j] = *reinterpret_cast<const uint16_t*>(q) | (uint32_t)__ldg(e) << 16;
+          s.y1[j] = *reinterpret_cast<const uint16_t*>(q + H) | (uint32_t)__ldg(e + nb) << 16;
+        } else {
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.y) + r * 2 * H + fc;
+          s.y0[j] = __ldg(reinterpret_cast<const uint32_t*>(q));
+          s.y1[j] = __ldg(reinterpret_cast<const uint32_t*>(q + H));
         }
       }
-      tmem_ld32(tbase + c, v);
+    };
+    auto values = [](uint32_t v) {
+      if (!CODES) return bf16x2_bits_to_f32(v);
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
+      const float2 q = __half22float2(__half2(h));
+      const float s = __uint_as_float((v >> 16) << 23);
+      return make_float2(q.x * s, q.y * s);
+    };
+    auto pack = [](float x, float y) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    auto use = [&](int c, const Kept& s, const float* v) {
+      const int64_t r = t.row0 + c + odd;
+      __nv_bfloat16* dy = p.dy + r * 2 * H + f;
+      __nv_bfloat16* z = p.z + r * H + f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (!keep || c + i >= t.rows) continue;
-        float g, slope;
-        act_slope<ACT>(y0[i], &g, &slope);
-        __nv_bfloat16* d = dy + (int64_t)(c + i) * 2 * H;
-        d[0] = __float2bfloat16_rn(v[i] * y1[i] * slope);
-        d[H] = __float2bfloat16_rn(v[i] * g);
-        if (p.z) z[(int64_t)(c + i) * H] = __float2bfloat16_rn(g * y1[i]);
+      for (int j = 0; j < kChunk / 2; ++j) {
+        const float2 dz = deal(v, j, odd), y0 = values(s.y0[j]), y1 = values(s.y1[j]);
+        float2 g, slope;
+        act_slope<ACT>(y0.x, &g.x, &slope.x);
+        act_slope<ACT>(y0.y, &g.y, &slope.y);
+        if (keep && c + 2 * j + odd < t.rows) {
+          *reinterpret_cast<uint32_t*>(dy) = pack(dz.x * y1.x * slope.x, dz.y * y1.y * slope.y);
+          *reinterpret_cast<uint32_t*>(dy + H) = pack(dz.x * g.x, dz.y * g.y);
+          if (p.z) *reinterpret_cast<uint32_t*>(z) = pack(g.x * y1.x, g.y * y1.y);
+        }
+        dy += 4 * H;
+        z += 2 * H;
       }
-    }
-    release();
+    };
+    by_chunks<Kept>(t.rows, group, tbase, load, use, wait, release);
   }
 };
 
@@ -305,20 +321,21 @@ struct Plain {
     load_half<WMN>(a, &p.rows.w, bar, block * kBK, t.m * kTileM + rank * kHalfM, t.expert);
     load_rows(p.rows, t, rank, block, b, bar);
   }
-  template <class Release>
-  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int lane, uint32_t tbase,
-                                  Release release) {
-    const int f = t.m * kTileM + rank * kHalfM + sub * 32 + lane;
-    const bool keep = f < p.F;
-    __nv_bfloat16* out = p.out + (int64_t)t.row0 * p.F + f;
-    for (int c = 0; c < t.rows; c += 32) {
-      float v[32];
-      tmem_ld32(tbase + c, v);
+  template <class Wait, class Release>
+  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int group, int lane, uint32_t tbase,
+                                  Wait wait, Release release) {
+    const int f = t.m * kTileM + rank * kHalfM + sub * 32 + (lane & 30);
+    const bool odd = lane & 1, keep = f < p.F;  // (F is a multiple of 16)
+    auto use = [&](int c, const NoSource&, const float* v) {
+      __nv_bfloat16* out = p.out + (int64_t)(t.row0 + c + odd) * p.F + f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (keep && c + i < t.rows) out[(int64_t)(c + i) * p.F] = __float2bfloat16_rn(v[i]);
-    }
-    release();
+      for (int j = 0; j < kChunk / 2; ++j) {
+        const float2 w = deal(v, j, odd);
+        if (keep && c + 2 * j + odd < t.rows)
+          *reinterpret_cast<__nv_bfloat162*>(out + (int64_t)(2 * j) * p.F) = __floats2bfloat162_rn(w.x, w.y);
+      }
+    };
+    by_chunks<NoSource>(t.rows, group, tbase, [](int, NoSource&) {}, use, wait, release);
   }
 };
 
@@ -333,7 +350,7 @@ bool make_rows(Rows* r, const GatedArgs& g, const void* x, int K, int cols, int 
   r->E = g.E;
   r->a_max = g.a_max;
   r->mt = (cols + tile_cols - 1) / tile_cols;
-  r->blocks = (K + kBK - 1) / kBK;
+  r->k = K;
   const int64_t b = kBandBytes / ((int64_t)kMaxN * K * 2);
   r->band = (int)(b < 1 ? 1 : b > 1024 ? 1024 : b);
   for (int h = 0; h < kHeights; ++h) {

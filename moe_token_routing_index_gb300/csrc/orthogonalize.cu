@@ -131,26 +131,22 @@ __global__ void __launch_bounds__(kNormThreads) first_kernel(const Source p, con
 
 // ------------------------------------------------------------------ products
 
-// A tile of 256 columns (lanes) x n rows of a [rows, cols] result of one matrix.
+// A tile of 256 rows (lanes) x n columns of a [rows, cols] result of one matrix.
 struct MatTile {
-  int n, blocks;
-  int at, col, row;    // the matrix, first column and first row
-  int height;          // of B's boxes where it is K-major
+  int n, k;
+  int at, row, col;    // the matrix, first row and first column
   bool mirror;         // symmetric results: stored across the diagonal too
 };
-
-constexpr int kHeights = 4;
-__host__ __device__ constexpr int box_rows(int h) { return 16 << h; }
 
 struct Mats {
   CUtensorMap a, b[kHeights];
   int count, rows, cols;  // of the result
   int ct, rt;             // tiles along its columns and rows
   int per;                // tiles of a matrix
-  int blocks;             // of the reduction
+  int k;                  // the reduction's length
 };
 
-// SYM: the tiles of column block >= row block (cols == rows).
+// SYM: the tiles of row block >= column block (cols == rows).
 template <bool SYM>
 __device__ __forceinline__ MatTile locate_mat(const Mats& p, int i) {
   MatTile t;
@@ -168,13 +164,23 @@ __device__ __forceinline__ MatTile locate_mat(const Mats& p, int i) {
     c = l - r * p.ct;
     t.mirror = false;
   }
-  t.col = c * kTileM;
-  t.row = r * kMaxN;
-  t.n = min(kMaxN, (p.rows - t.row + 31) / 32 * 32);
-  t.blocks = p.blocks;
-  const int half = t.n / 2;
-  t.height = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+  t.row = r * kTileM;
+  t.col = c * kMaxN;
+  t.n = min(kMaxN, (p.cols - t.col + 31) / 32 * 32);
+  t.k = p.k;
   return t;
+}
+
+// 32 bytes of a lane.
+__device__ __forceinline__ void load32(const void* p, uint32_t* r) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 enum Product { kGram, kPolynomial, kNext, kOut, kWeights };
@@ -190,6 +196,7 @@ struct Result {
   float scale, keep;    // out = scale * result, or keep * w - scale * result
   const float* lr;      // nullable: multiplies scale, and what keep takes from 1
   int w_dtype;
+  bool whole;           // out's chunks are whole and 32-byte aligned
 };
 
 template <bool AMN, bool BMN, Product KIND>
@@ -205,78 +212,141 @@ struct Ns {
   static __device__ int setup(const Params& p, int*, int) { return p.m.count * p.m.per; }
   static __device__ Tile tile(const Params& p, const int*, int i) { return locate_mat<kSym>(p.m, i); }
   static __device__ uint32_t stage_bytes(const Params&, const Tile& t) {
-    return 2u * (uint32_t)(kOperandBytes + (BMN ? kOperandBytes : box_rows(t.height) * 128 * (kBK / 64)));
+    return 2u * (uint32_t)(kOperandBytes + (BMN ? kOperandBytes : t.n / 2 * 128 * (kBK / 64)));
   }
   static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
                               uint32_t bar) {
-    load_half<AMN>(a, &p.m.a, bar, block * kBK, t.col + rank * kHalfM, t.at);
-    const int row = t.row + rank * (t.n / 2);
-    if (BMN || t.height == 3) load_half<BMN>(b, &p.m.b[3], bar, block * kBK, row, t.at);
-    else if (t.height == 2) load_half<BMN>(b, &p.m.b[2], bar, block * kBK, row, t.at);
-    else if (t.height == 1) load_half<BMN>(b, &p.m.b[1], bar, block * kBK, row, t.at);
-    else load_half<BMN>(b, &p.m.b[0], bar, block * kBK, row, t.at);
+    load_half<AMN>(a, &p.m.a, bar, block * kBK, t.row + rank * kHalfM, t.at);
+    const int col = t.col + rank * (t.n / 2);
+    load_half<BMN>(b, &p.m.b[BMN ? 0 : t.n / 32 - 1], bar, block * kBK, col, t.at);
   }
-  template <class Release>
-  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int lane, uint32_t tbase,
-                                  Release release) {
+  static constexpr int kWords = kChunk / 2;
+  struct Source {  // a chunk of a row: of X's halves, or of A; of the weights
+    uint32_t hi[KIND == kGram ? 1 : kWords], lo[kSym ? 1 : kWords];
+    uint32_t w[KIND == kWeights ? kChunk : 1];
+  };
+  static __device__ __forceinline__ float2 halves(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t pack_half(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  template <class Wait, class Release>
+  static __device__ void epilogue(const Params& p, const Tile& t, int rank, int sub, int group, int lane, uint32_t tbase,
+                                  Wait wait, Release release) {
     const Result& g = p.r;
-    const int f = t.col + rank * kHalfM + sub * 32 + lane;
-    const bool keep = f < p.m.cols;
-    const int rows = min(t.n, p.m.rows - t.row);
-    const int64_t ld = g.ld, base = (int64_t)t.at * p.m.rows * ld;
-    const int64_t first = base + (int64_t)t.row * ld + f;
+    const int row = t.row + rank * kHalfM + sub * 32 + lane;
+    const bool keep = row < p.m.rows;
+    const int cols = min(t.n, p.m.cols - t.col);
+    // rows of the workspace are multiples of kChunk apart: whole chunks are read and written, what lies past
+    // the columns is not read as an operand
+    const int64_t matrix = (int64_t)t.at * p.m.rows * g.ld;
+    const int64_t at = matrix + (int64_t)(keep ? row : 0) * g.ld + t.col;
+    const int64_t out_at = ((int64_t)t.at * p.m.rows + (keep ? row : 0)) * p.m.cols + t.col;
     float lr = 1.0f;
     if (KIND == kWeights && g.lr) lr = __ldg(g.lr);
     const float w_keep = 1.0f - lr * g.keep, w_scale = lr * g.scale;
-    for (int c = 0; c < rows; c += 32) {
-      float x[32], v[32];
-      if (KIND != kGram) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = 0.0f;
-          if (keep && c + i < rows) {
-            const int64_t o = first + (int64_t)(c + i) * ld;
-            x[i] = __half2float(g.src[o]);
-            if (KIND != kPolynomial) x[i] += __half2float(g.lo[o]);
-          }
-        }
-      }
-      tmem_ld32(tbase + c, v);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[i] *= g.beta;
-        if (KIND != kGram) v[i] = fmaf(g.alpha, x[i], v[i]);
-        if (!keep || c + i >= rows) continue;
-        if (kSym || KIND == kNext) {
-          const int64_t o = first + (int64_t)(c + i) * ld;
-          const __half h = __float2half_rn(v[i]);
-          if (kSym) {
-            g.sym[o] = h;
+    const bool f32 = KIND == kWeights && g.w_dtype == MOE_DTYPE_F32;
+    auto load = [&](int c, Source& s) {
+      if constexpr (KIND != kGram) load32(g.src + at + c, s.hi);
+      if constexpr (!kSym) load32(g.lo + at + c, s.lo);
+      if constexpr (KIND == kWeights) {
+        if (g.whole) {
+          if (f32) {
+            load32(static_cast<const float*>(g.out) + out_at + c, s.w);
+            load32(static_cast<const float*>(g.out) + out_at + c + 8, s.w + 8);
           } else {
-            g.next[o] = h;
-            g.lo[o] = __float2half_rn(v[i] - __half2float(h));
+            load32(static_cast<const __nv_bfloat16*>(g.out) + out_at + c, s.w);
           }
         } else {
-          const int64_t o = ((int64_t)t.at * p.m.rows + t.row + c + i) * p.m.cols + f;
-          if (KIND == kOut) {
-            static_cast<__nv_bfloat16*>(g.out)[o] = __float2bfloat16_rn(v[i] * g.scale);
-          } else if (g.w_dtype == MOE_DTYPE_F32) {
-            float* w = static_cast<float*>(g.out) + o;
-            *w = w_keep * *w - w_scale * v[i];
-          } else {
-            __nv_bfloat16* w = static_cast<__nv_bfloat16*>(g.out) + o;
-            *w = __float2bfloat16_rn(w_keep * __bfloat162float(*w) - w_scale * v[i]);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            const int64_t o = out_at + min(c + i, cols - 1);
+            s.w[i] = f32 ? static_cast<const uint32_t*>(g.out)[o] : static_cast<const uint16_t*>(g.out)[o];
           }
         }
       }
-      if (kSym && t.mirror && keep) {  // this lane's row of the mirrored tile
-        __half* m = g.sym + base + (int64_t)f * ld + t.row + c;
+    };
+    auto use = [&](int c, const Source& s, float* v) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < rows) m[i] = __float2half_rn(v[i]);
+      for (int i = 0; i < kWords; ++i) {
+        float2 x = make_float2(v[2 * i] * g.beta, v[2 * i + 1] * g.beta);
+        if constexpr (KIND != kGram) {
+          const float2 h = halves(s.hi[i]);
+          x = make_float2(fmaf(g.alpha, h.x, x.x), fmaf(g.alpha, h.y, x.y));
+        }
+        if constexpr (!kSym) {
+          const float2 l = halves(s.lo[i]);
+          x = make_float2(fmaf(g.alpha, l.x, x.x), fmaf(g.alpha, l.y, x.y));
+        }
+        v[2 * i] = x.x;
+        v[2 * i + 1] = x.y;
       }
-    }
-    release();
+      if constexpr (kSym || KIND == kNext) {
+        uint32_t hi[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) hi[i] = pack_half(v[2 * i], v[2 * i + 1]);
+        if (keep) store32((kSym ? g.sym : g.next) + at + c, hi);
+        if constexpr (KIND == kNext) {
+          uint32_t lo[kWords];
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const float2 h = halves(hi[i]);
+            lo[i] = pack_half(v[2 * i] - h.x, v[2 * i + 1] - h.y);
+          }
+          if (keep) store32(g.lo + at + c, lo);
+        } else if (t.mirror) {  // the same across the diagonal, by columns
+          const bool odd = lane & 1;
+          __half* m = g.sym + matrix + (int64_t)(t.col + c + odd) * g.ld + (row & ~1);
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            const float2 w = deal(v, j, odd);
+            // (an odd last row's pair writes one element into the padding)
+            if ((row & ~1) < p.m.rows && c + 2 * j + odd < cols)
+              *reinterpret_cast<uint32_t*>(m + (int64_t)(2 * j) * g.ld) = pack_half(w.x, w.y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          if (KIND == kOut) {
+            v[i] *= g.scale;
+          } else {
+            const uint32_t w = f32 ? s.w[i] : g.whole ? (i & 1 ? s.w[i / 2] & 0xffff0000u : s.w[i / 2] << 16) : s.w[i] << 16;
+            v[i] = w_keep * __uint_as_float(w) - w_scale * v[i];
+          }
+        }
+        if (!keep) return;
+        if (f32) {
+          float* o = static_cast<float*>(g.out) + out_at + c;
+          if (g.whole) {
+            store32(o, reinterpret_cast<const uint32_t*>(v));
+            store32(o + 8, reinterpret_cast<const uint32_t*>(v) + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+              if (c + i < cols) o[i] = v[i];
+          }
+        } else {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.out) + out_at + c;
+          if (g.whole) {
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            store32(o, w);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+              if (c + i < cols) o[i] = __float2bfloat16_rn(v[i]);
+          }
+        }
+      }
+    };
+    by_chunks<Source>(cols, group, tbase, load, use, wait, release);
   }
 };
 
@@ -299,8 +369,8 @@ struct Layout {
 Layout layout(const OrthoArgs& g) {
   Layout l;
   l.m = g.N < g.K ? g.N : g.K;
-  l.ldx = (int)up(g.K, 8);
-  l.ldm = (int)up(l.m, 8);
+  l.ldx = (int)up(g.K, kChunk);
+  l.ldm = (int)up(l.m, kChunk);
   const size_t x = up((int64_t)g.B * g.N * l.ldx * 2, 256), sym = up((int64_t)g.B * l.m * l.ldm * 2, 256);
   l.part = 0;
   l.x0 = up((int64_t)g.B * norm_blocks(g) * (int64_t)sizeof(float2), 256);
@@ -317,9 +387,9 @@ bool make_mats(Mats* m, const OrthoArgs& g, int rows, int cols, int k, bool sym)
   m->count = g.B;
   m->rows = rows;
   m->cols = cols;
-  m->ct = (cols + kTileM - 1) / kTileM;
-  m->rt = (rows + kMaxN - 1) / kMaxN;
-  m->blocks = (k + kBK - 1) / kBK;
+  m->ct = (cols + kMaxN - 1) / kMaxN;
+  m->rt = (rows + kTileM - 1) / kTileM;
+  m->k = k;
   m->per = sym ? m->rt * (m->rt + 1) / 2 : m->rt * m->ct;
   return (int64_t)m->per * g.B <= INT32_MAX / 2;
 }
@@ -341,12 +411,12 @@ cudaError_t launch(const typename P::Params& p, cudaStream_t s) {
 
 template <bool TALL, Product KIND>
 cudaError_t multiply(const OrthoArgs& g, const Layout& l, const Result& r, const __half* poly, cudaStream_t s) {
-  // X [N, K] with lanes along K: A is X read along its columns (wide), or P (tall)
-  using P = Ns<!TALL, false, KIND>;
+  // X [N, K]: P X (wide: P's rows, X's columns) or X P (tall: X's rows, P's rows, as P is symmetric)
+  using P = Ns<false, !TALL, KIND>;
   typename P::Params p{};
   if (!make_mats(&p.m, g, g.N, g.K, l.m, false)) return cudaErrorNotSupported;
-  if (TALL ? !(map_a(&p.m, false, poly, g.B, l.m, l.m, l.ldm) && map_b(&p.m, false, r.src, g.B, g.N, g.K, l.ldx))
-           : !(map_a(&p.m, true, r.src, g.B, g.N, g.K, l.ldx) && map_b(&p.m, false, poly, g.B, l.m, l.m, l.ldm)))
+  if (TALL ? !(map_a(&p.m, false, r.src, g.B, g.N, g.K, l.ldx) && map_b(&p.m, false, poly, g.B, l.m, l.m, l.ldm))
+           : !(map_a(&p.m, false, poly, g.B, l.m, l.m, l.ldm) && map_b(&p.m, true, r.src, g.B, g.N, g.K, l.ldx)))
     return cudaErrorInvalidValue;
   p.r = r;
   p.err = g.err;
@@ -398,6 +468,7 @@ cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t 
     r.keep = g.decay;
     r.lr = g.lr;
     r.w_dtype = g.w_dtype;
+    r.whole = g.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31) == 0;
     if (step + 1 < g.steps) e = multiply<TALL, kNext>(g, l, r, poly, s);
     else if (g.update) e = multiply<TALL, kWeights>(g, l, r, poly, s);
     else e = multiply<TALL, kOut>(g, l, r, poly, s);

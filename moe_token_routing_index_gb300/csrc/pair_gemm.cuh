@@ -7,13 +7,15 @@
 // n / 2 of B, the MMAs of the leader (rank 0) read both CTAs' shared memory, and each CTA's
 // tensor memory receives its 128 rows of the tile: one lane per row, one column per row of B.
 // An operand lies K-major (its rows contiguous along the reduction: boxes of 64 k) or MN-major
-// (rows of the reduction, contiguous along the tile: boxes of 64 columns).  6 warps:
+// (rows of the reduction, contiguous along the tile: boxes of 64 columns).  10 warps:
 //   warp 0     TMA producer of this CTA's halves, into a ring of stages of kBK of the
 //              reduction; both CTAs' copies complete on the leader's barrier
 //   warp 1     (leader) MMA issuer, into one of two 256-column accumulators
-//   warps 2-5  the policy's epilogue, each on the 32 lanes of its quarter
-// What an epilogue stores has its lanes as the contiguous dimension, so that a warp's store of a
-// column is 64 contiguous bytes and needs no staging.
+//   warps 2-9  the policy's epilogue: two warps for the 32 lanes of a quarter, which take its
+//              columns by turns of kChunk
+// Results go from registers to memory, without staging: where a column's lanes are contiguous there,
+// neighbouring lanes deal two columns out among them and a warp stores two columns of 64 bytes at
+// once; where a lane's columns are contiguous, a lane stores the 32 bytes of a chunk.
 //
 // Every wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT, all roles stop,
 // copies and MMAs in flight are drained, and tensor memory is freed.
@@ -29,13 +31,22 @@ namespace pg {
 using namespace tc;
 
 constexpr int kTileM = 256, kHalfM = 128, kMaxN = 256;
-constexpr int kBK = 64;                                  // of the reduction per stage
+// Of the reduction per stage.  (Stages twice as long, half as many: 128 experts of 344 rows, D = 4096,
+// H = 1536, forward 950 us instead of 784.  Boxes brought into L2 8 stages ahead: 929, as the way from L2
+// to the SMs is what binds next to DRAM.)
+constexpr int kBK = 64;
 constexpr int kOperandBytes = 128 * kBK * 2;             // of a CTA's half of A; room for its half of B
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 192 * 1024 / kStageBytes;
 constexpr int kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kMaxN;
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8, kEpiGroups = kEpiWarps / 4;
+constexpr int kChunk = 16;                               // columns of an epilogue's step
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+// Boxes of a K-major B, of 16, 32, ... 128 rows: a CTA loads its n / 2 rows and no more.  (With boxes of
+// 16, 32, 64 and 128 rows, 128 experts of 344 rows loaded a third more of them than they used.)
+constexpr int kHeights = 8;
+__host__ __device__ constexpr int box_rows(int h) { return 16 * (h + 1); }
 constexpr int kBoxBytes = 64 * 128;                      // of an MN-major box: 64 columns x kBK rows
 
 struct Smem {
@@ -57,11 +68,22 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   return d;
 }
 
-// The descriptor of the 16 reduction steps from 16 * kk on of an operand's half at addr.
+// The descriptor of an operand's half at addr, and how far on that of the 16 reduction steps from 16 * kk lies.
 template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int kk) {
-  if (MN) return desc_mn(addr + kk * 2048);                            // 16 rows of 128 bytes
-  return smem_desc_sw128(addr + (kk >> 2) * (128 * 128) + (kk & 3) * 32);  // 64 k of 128 rows a box
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return MN ? desc_mn(addr) : smem_desc_sw128(addr);
+}
+template <bool MN>
+__device__ __forceinline__ constexpr uint32_t operand_step(int kk) {
+  return (MN ? kk * 2048                                      // 16 rows of 128 bytes
+             : (kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;  // 64 k of 128 rows a box
+}
+
+// One lane of the (whole) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -137,16 +159,64 @@ __device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
+// kChunk consecutive accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, float* v) {
+  uint32_t r[kChunk];
+  static_assert(kChunk == 16, "one load a chunk");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Columns 2j and 2j + 1 of two neighbouring lanes, dealt out so that the even lane has both lanes'
+// column 2j and the odd one both lanes' column 2j + 1 (the even lane's value in x).
+__device__ __forceinline__ float2 deal(const float* v, int j, bool odd) {
+  const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1);
+  return odd ? make_float2(other, v[2 * j + 1]) : make_float2(v[2 * j], other);
+}
+
+// An epilogue over `rows` columns of a tile: load(c, s) brings what column chunk c needs from memory
+// into s, ahead of the chunk's turn (the first before the accumulator is waited for); use(c, s, v)
+// takes it with the accumulator's columns c .. c + kChunk - 1.
+template <class Source, class Load, class Use, class Wait, class Release>
+__device__ __forceinline__ void by_chunks(int rows, int group, uint32_t tbase, Load load, Use use, Wait wait,
+                                          Release release) {
+  int c = group * kChunk;
+  Source s{};
+  if (c < rows) load(c, s);
+  if (!wait()) return;
+  while (c < rows) {
+    float v[kChunk];
+    tmem_ld_chunk(tbase + c, v);
+    Source next{};
+    if (c + kEpiGroups * kChunk < rows) load(c + kEpiGroups * kChunk, next);
+    else release();
+    use(c, s, v);
+    s = next;
+    c += kEpiGroups * kChunk;
+  }
+  if (group * kChunk >= rows) release();
+}
+struct NoSource {};
+
 // A policy P has
 //   kAMN, kBMN                       an operand is MN-major
 //   kF16                             fp16 operands (else bf16)
 //   Params                           kernel parameter, with unsigned int* err
-//   Tile                             with int n (rows of B, a multiple of 32) and int blocks (of kBK) > 0
+//   Tile                             with int n (rows of B, a multiple of 32) and int k > 0, the reduction's length
 //   setup(p, tables, lane) -> int    the number of tiles (one warp; it may fill the tables)
 //   tile(p, tables, i) -> Tile
 //   stage_bytes(p, t)                what both CTAs' loads of a stage complete
 //   load(p, t, rank, block, a, b, bar)
-//   epilogue(p, t, rank, sub, lane, tbase, release)   release(): the accumulator has been read
+//   epilogue(p, t, rank, sub, group, lane, tbase, wait, release)
+//     wait() -> bool: the accumulator is whole (false: give up); release(): it has been read.
+//     group: which of the quarter's two warps
 template <class P>
 __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -176,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
     }
     for (int b = 0; b < kAccBufs; ++b) {
       mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), 8);  // 4 epilogue warps in each CTA of the pair
+      mbar_init(bar_tempty(b), 2 * kEpiWarps);  // of both CTAs
     }
     mbar_init(bar_drain, 1);
     *s_abort = 0;
@@ -211,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
       for (int i = pair; i < total && ok; i += pairs) {
         const typename P::Tile t = P::tile(p, tables, i);
         const uint32_t bytes = P::stage_bytes(p, t);
-        for (int kb = 0; kb < t.blocks; ++kb) {
+        const int blocks = (t.k + kBK - 1) / kBK;
+        for (int kb = 0; kb < blocks; ++kb) {
           if (!mbar_wait(bar_empty(s), phase ^ 1u, s_abort)) {
             ok = false;
             break;
@@ -241,47 +312,53 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA (leader)
-    if (lane == 0 && leader) {
+    // The whole warp keeps the loop, so that its values are uniform, and one lane issues: with a lane that
+    // does it all, an MMA took 128 cycles to issue whatever its n, which left no slack for a late stage.
+    if (leader) {
       const uint32_t fmt = P::kF16 ? 0u : 1u;
       const uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((P::kAMN ? 1u : 0u) << 15) |
                             ((P::kBMN ? 1u : 0u) << 16) | ((uint32_t)(kTileM >> 4) << 24);
+      const uint64_t a0 = operand_desc<P::kAMN>(sbase + Smem::stage);
+      const uint64_t b0 = operand_desc<P::kBMN>(sbase + Smem::stage + kOperandBytes);
       int s = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued_any = false;
       for (int i = pair; i < total && ok; i += pairs) {
         const typename P::Tile t = P::tile(p, tables, i);
         const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
-        if (!mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * kMaxN);
-        for (int kb = 0; kb < t.blocks; ++kb) {
-          if (!mbar_wait_cluster(bar_full(s), phase, s_abort)) {
-            ok = false;
-            break;
-          }
+        for (int k = 0; k < t.k; k += kBK) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_full(s), phase, s_abort));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = sbase + Smem::stage + s * kStageBytes, b = a + kOperandBytes;
+          const uint64_t a = a0 + (uint64_t)(s * (kStageBytes >> 4)), b = b0 + (uint64_t)(s * (kStageBytes >> 4));
+          const int steps = (t.k - k + 15) / 16;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_issue_pair(d, operand_desc<P::kAMN>(a, kk), operand_desc<P::kBMN>(b, kk), idesc, (kb | kk) != 0);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              if (kk < steps)
+                mma_issue_pair(d, a + operand_step<P::kAMN>(kk), b + operand_step<P::kBMN>(kk), idesc, (k | kk) != 0);
+            mma_commit_pair(bar_empty(s));
+          }
+          __syncwarp();
           issued_any = true;
-          mma_commit_pair(bar_empty(s));
           if (++s == kStages) {
             s = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        mma_commit_pair(bar_tfull(acc));
+        if (elect_one()) mma_commit_pair(bar_tfull(acc));
+        __syncwarp();
         if (++acc == kAccBufs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         flag_error(p.err, MOE_DEVERR_TIMEOUT);
         *s_abort = 1;
         if (issued_any) {  // the MMAs in flight finish before tensor memory is freed
@@ -296,20 +373,26 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
     const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = pair; i < total; i += pairs) {
+    bool ok = true;
+    for (int i = pair; i < total && ok; i += pairs) {
       const typename P::Tile t = P::tile(p, tables, i);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull(acc), acc_phase, s_abort))) {
-        if (lane == 0) flag_error(p.err, MOE_DEVERR_TIMEOUT);
-        *s_abort = 1;
-        break;
-      }
-      tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kMaxN);
-      P::epilogue(p, t, rank, sub, lane, tbase, [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
-      });
+      P::epilogue(
+          p, t, rank, sub, (warp - 2) >> 2, lane, tbase,
+          [&] {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_tfull(acc), acc_phase, s_abort));
+            if (!ok) {
+              if (lane == 0) flag_error(p.err, MOE_DEVERR_TIMEOUT);
+              *s_abort = 1;
+            }
+            tc_fence_after();
+            return ok;
+          },
+          [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
+          });
       if (++acc == kAccBufs) {
         acc = 0;
         acc_phase ^= 1u;
