@@ -37,53 +37,60 @@ struct RowTile {
   int m, expert, row0, rows;  // tile along the columns; rows: those of the tile that are the expert's
 };
 
-// tables: the experts' first row tiles [E + 1] and rows [E + 1].  One warp; counts as in the
-// grouped GEMMs: negative ones are empty, a sum past a_max is cut, both flagged.
-__device__ __forceinline__ int setup_rows(const Rows& p, int* tables, int lane, unsigned int* err) {
+// tables: the experts' first row tiles [E + 1] and rows [E + 1].  Counts as in the grouped GEMMs: negative
+// ones are empty, a sum past a_max is cut, both flagged.
+__device__ __forceinline__ int setup_rows(const Rows& p, int* tables, unsigned int* err) {
   int* tile_start = tables;
   int* row_off = tables + p.E + 1;
-  int64_t run = 0;
-  int tiles = 0;
-  bool bad = false;
-  for (int base = 0; base < p.E; base += 32) {
-    const int e = base + lane;
-    int c = e < p.E ? p.counts[e] : 0;
-    if (c < 0) {
-      c = 0;
-      bad = true;
-    }
-    int64_t incl = c;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    int64_t run = 0;
+    int tiles = 0;
+    bool bad = false;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      int c = e < p.E ? p.counts[e] : 0;
+      if (c < 0) {
+        c = 0;
+        bad = true;
+      }
+      int64_t incl = c;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int r0 = (int)min(run + incl - c, (int64_t)p.a_max), r1 = (int)min(run + incl, (int64_t)p.a_max);
-    const int mine = (r1 - r0 + kMaxN - 1) / kMaxN;
-    int n = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int r0 = (int)min(run + incl - c, (int64_t)p.a_max), r1 = (int)min(run + incl, (int64_t)p.a_max);
+      const int mine = (r1 - r0 + kMaxN - 1) / kMaxN;
+      int n = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += v;
+      }
+      if (e < p.E) {
+        tile_start[e] = tiles + n - mine;
+        row_off[e] = r0;
+      }
+      tiles += __shfl_sync(0xffffffffu, n, 31);
+      run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (e < p.E) {
-      tile_start[e] = tiles + n - mine;
-      row_off[e] = r0;
+    if (run > p.a_max) bad = true;
+    if (lane == 0) {
+      tile_start[p.E] = tiles;
+      row_off[p.E] = (int)min(run, (int64_t)p.a_max);
     }
-    tiles += __shfl_sync(0xffffffffu, n, 31);
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) flag_error(err, MOE_DEVERR_BAD_COUNT);
   }
-  if (run > p.a_max) bad = true;
-  if (lane == 0) {
-    tile_start[p.E] = tiles;
-    row_off[p.E] = (int)min(run, (int64_t)p.a_max);
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) flag_error(err, MOE_DEVERR_BAD_COUNT);
-  return tiles * p.mt;
+  __syncthreads();
+  return tile_start[p.E] * p.mt;
 }
 
-// Tile i: the experts in order; within one, bands of row tiles, in a band the row tiles innermost,
-// so that pairs running together share the weights' tile and the band's rows.
+// Tile i: the experts in order; within one, bands of row tiles, in a band the row tiles innermost, so that
+// pairs running together share the weights' tile and the band's rows.  (Experts by their rows, and each
+// pair, or half of the pairs, taking tiles from either end of that order, so that tiles bound by the weights
+// run beside those bound by the products: 32768 rows of 128 experts by Zipf's law, 2420 us in all orders;
+// 128 experts of 344 rows, 1230 us in this order, 1300 to 1630 in those.)
 __device__ __forceinline__ RowTile locate_rows(const Rows& p, const int* tables, int i) {
   const int* tile_start = tables;
   const int* row_off = tables + p.E + 1;
@@ -110,6 +117,13 @@ __device__ __forceinline__ RowTile locate_rows(const Rows& p, const int* tables,
   t.n = (t.rows + 31) / 32 * 32;
   t.k = p.k;
   return t;
+}
+
+__device__ __forceinline__ void narrow_rows(RowTile* t, int part, int parts) {
+  const int n = ((t->n + parts - 1) / parts + 31) / 32 * 32, from = part * n;
+  t->row0 += from;
+  t->rows = min(n, t->rows - from);
+  t->n = max(0, min(n, t->n - from));
 }
 
 __device__ __forceinline__ uint32_t row_stage_bytes(const RowTile& t) {
@@ -172,9 +186,8 @@ struct GatedForward {
     unsigned int* err;
   };
   using Tile = RowTile;
-  static __device__ int setup(const Params& p, int* tables, int lane) {
-    return setup_rows(p.rows, tables, lane, p.err);
-  }
+  static __device__ int setup(const Params& p, int* tables) { return setup_rows(p.rows, tables, p.err); }
+  static __device__ void narrow(Tile* t, int part, int parts) { narrow_rows(t, part, parts); }
   static __device__ Tile tile(const Params& p, const int* tables, int i) { return locate_rows(p.rows, tables, i); }
   static __device__ uint32_t stage_bytes(const Params&, const Tile& t) { return row_stage_bytes(t); }
   static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
@@ -231,9 +244,8 @@ struct GatedGrad {
     unsigned int* err;
   };
   using Tile = RowTile;
-  static __device__ int setup(const Params& p, int* tables, int lane) {
-    return setup_rows(p.rows, tables, lane, p.err);
-  }
+  static __device__ int setup(const Params& p, int* tables) { return setup_rows(p.rows, tables, p.err); }
+  static __device__ void narrow(Tile* t, int part, int parts) { narrow_rows(t, part, parts); }
   static __device__ Tile tile(const Params& p, const int* tables, int i) { return locate_rows(p.rows, tables, i); }
   static __device__ uint32_t stage_bytes(const Params&, const Tile& t) { return row_stage_bytes(t); }
   static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
@@ -311,9 +323,8 @@ struct Plain {
     unsigned int* err;
   };
   using Tile = RowTile;
-  static __device__ int setup(const Params& p, int* tables, int lane) {
-    return setup_rows(p.rows, tables, lane, p.err);
-  }
+  static __device__ int setup(const Params& p, int* tables) { return setup_rows(p.rows, tables, p.err); }
+  static __device__ void narrow(Tile* t, int part, int parts) { narrow_rows(t, part, parts); }
   static __device__ Tile tile(const Params& p, const int* tables, int i) { return locate_rows(p.rows, tables, i); }
   static __device__ uint32_t stage_bytes(const Params&, const Tile& t) { return row_stage_bytes(t); }
   static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,

@@ -30,21 +30,14 @@ constexpr int kNormThreads = 256;
 
 // ------------------------------------------------- momentum, norm, first iterate
 
-struct Source {            // u: g itself, or g and the momentum
+struct Input {             // u: g itself, or g and the momentum
   const void* g;
   int64_t batch, row;      // strides of g, elements
-  int dtype;
   float* momentum;         // nullable; contiguous
   float mu;
   int nesterov;
-  int B, N, K;
+  int N, K;
 };
-
-__device__ __forceinline__ float load_g(const Source& p, int b, int r, int c) {
-  const int64_t o = b * p.batch + r * p.row + c;
-  return p.dtype == MOE_DTYPE_F32 ? static_cast<const float*>(p.g)[o]
-                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(p.g)[o]);
-}
 
 // Squares whose sum would overflow are summed a second time as multiples of 2^160.
 constexpr float kDown = 0x1p-80f;
@@ -76,29 +69,76 @@ __device__ __forceinline__ float2 block_sum(float2 v) {
   return t;
 }
 
-// Block (i, b): rows i, i + gridDim.x, ... of matrix b.  The momentum is updated, and the
-// squares of u are summed: part[b][i].
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Source p, float2* part) {
-  pdl_launch_dependents();
-  const int b = blockIdx.y;
-  Squares q;
-  for (int r = blockIdx.x; r < p.N; r += gridDim.x)
-    for (int c = threadIdx.x; c < p.K; c += kNormThreads) {
-      float u = load_g(p, b, r, c);
-      if (p.momentum) {
-        float* m = p.momentum + ((int64_t)b * p.N + r) * p.K + c;
-        const float v = fmaf(p.mu, *m, u);
-        *m = v;
-        u = p.nesterov ? fmaf(p.mu, v, u) : v;
+// V neighbouring elements of a row: 8 where rows and bases allow 16-byte accesses, else 1.
+template <int V>
+__device__ __forceinline__ void load_values(const float* p, float* v) {
+  if constexpr (V == 8) {
+    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
+  } else {
+    *v = *p;
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_values(const __nv_bfloat16* p, float* v) {
+  if constexpr (V == 8) bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
+  else *v = __bfloat162float(*p);
+}
+
+// Every V elements of matrix b that are this thread's: of kAtOnce places at once the inputs are loaded
+// first, so that their ways overlap.  take(row, column, g's values, the momentum's, its address)
+template <class T, int V, bool MOMENTUM, class Take>
+__device__ __forceinline__ void each_value(const Input& p, int b, Take take) {
+  constexpr int kAtOnce = MOMENTUM ? 2 : 4;
+  const uint32_t per_row = (uint32_t)p.K / V, total = per_row * (uint32_t)p.N;
+  const uint32_t stride = gridDim.x * kNormThreads;
+  const T* g = static_cast<const T*>(p.g) + b * p.batch;
+  float* momentum = MOMENTUM ? p.momentum + (int64_t)b * p.N * p.K : nullptr;
+  for (uint32_t i = blockIdx.x * kNormThreads + threadIdx.x; i < total; i += kAtOnce * stride) {
+    float u[kAtOnce][V], m[kAtOnce][V];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const uint32_t at = i + j * stride;
+      if (at >= i && at < total) {  // (the sum may pass 32 bits)
+        const uint32_t r = at / per_row, c = at - r * per_row;
+        load_values<V>(g + r * p.row + c * V, u[j]);
+        if (MOMENTUM) load_values<V>(momentum + (int64_t)at * V, m[j]);
       }
-      q.add(u);
     }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const uint32_t at = i + j * stride;
+      if (at >= i && at < total) take(at / per_row, at % per_row * V, u[j], m[j], momentum + (int64_t)at * V);
+    }
+  }
+}
+
+// Matrix blockIdx.y: the momentum is updated, and the squares of u are summed into part.
+template <class T, int V, bool MOMENTUM>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p, float2* part) {
+  pdl_launch_dependents();
+  Squares q;
+  each_value<T, V, MOMENTUM>(p, blockIdx.y, [&](uint32_t, uint32_t, const float* u, const float* m, float* to) {
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      v[k] = MOMENTUM ? fmaf(p.mu, m[k], u[k]) : u[k];
+      q.add(MOMENTUM && p.nesterov ? fmaf(p.mu, v[k], u[k]) : v[k]);
+    }
+    if constexpr (MOMENTUM && V == 8) {
+      reinterpret_cast<float4*>(to)[0] = *reinterpret_cast<const float4*>(v);
+      reinterpret_cast<float4*>(to)[1] = *reinterpret_cast<const float4*>(v + 4);
+    } else if constexpr (MOMENTUM) {
+      *to = *v;
+    }
+  });
   const float2 t = block_sum(make_float2(q.plain, q.small));
-  if (threadIdx.x == 0) part[(int64_t)b * gridDim.x + blockIdx.x] = t;
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
 }
 
 // X = u / (|u| + eps), scaled, in two fp16 with rows ld elements apart.
-__global__ void __launch_bounds__(kNormThreads) first_kernel(const Source p, const float2* part, int parts, float eps,
+template <class T, int V, bool MOMENTUM>
+__global__ void __launch_bounds__(kNormThreads) first_kernel(const Input p, const float2* part, int parts, float eps,
                                                              __half* hi, __half* lo, int ld) {
   pdl_launch_dependents();
   pdl_wait();
@@ -114,19 +154,23 @@ __global__ void __launch_bounds__(kNormThreads) first_kernel(const Source p, con
   const bool big = isinf(t.x);
   const float pre = big ? kDown : 1.0f;
   const float f = kScale / (big ? sqrtf(t.y) : sqrtf(t.x) + eps);
-  for (int r = blockIdx.x; r < p.N; r += gridDim.x)
-    for (int c = threadIdx.x; c < p.K; c += kNormThreads) {
-      float u = load_g(p, b, r, c);
-      if (p.momentum) {
-        const float m = p.momentum[((int64_t)b * p.N + r) * p.K + c];
-        u = p.nesterov ? fmaf(p.mu, m, u) : m;
-      }
-      const float x = u * pre * f;
-      const __half h = __float2half_rn(x);
-      const int64_t o = ((int64_t)b * p.N + r) * ld + c;
-      hi[o] = h;
-      lo[o] = __float2half_rn(x - __half2float(h));
+  each_value<T, V, MOMENTUM>(p, b, [&](uint32_t r, uint32_t c, const float* u, const float* m, float*) {
+    __half h[V], l[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float x = (MOMENTUM ? (p.nesterov ? fmaf(p.mu, m[k], u[k]) : m[k]) : u[k]) * pre * f;
+      h[k] = __float2half_rn(x);
+      l[k] = __float2half_rn(x - __half2float(h[k]));
     }
+    const int64_t o = ((int64_t)b * p.N + r) * ld + c;
+    if constexpr (V == 8) {
+      *reinterpret_cast<uint4*>(hi + o) = *reinterpret_cast<const uint4*>(h);
+      *reinterpret_cast<uint4*>(lo + o) = *reinterpret_cast<const uint4*>(l);
+    } else {
+      hi[o] = *h;
+      lo[o] = *l;
+    }
+  });
 }
 
 // ------------------------------------------------------------------ products
@@ -209,7 +253,12 @@ struct Ns {
     unsigned int* err;
   };
   using Tile = MatTile;
-  static __device__ int setup(const Params& p, int*, int) { return p.m.count * p.m.per; }
+  static __device__ int setup(const Params& p, int*) { return p.m.count * p.m.per; }
+  static __device__ void narrow(Tile* t, int part, int parts) {
+    const int n = ((t->n + parts - 1) / parts + 31) / 32 * 32, from = part * n;
+    t->col += from;
+    t->n = max(0, min(n, t->n - from));
+  }
   static __device__ Tile tile(const Params& p, const int*, int i) { return locate_mat<kSym>(p.m, i); }
   static __device__ uint32_t stage_bytes(const Params&, const Tile& t) {
     return 2u * (uint32_t)(kOperandBytes + (BMN ? kOperandBytes : t.n / 2 * 128 * (kBK / 64)));
@@ -354,11 +403,11 @@ struct Ns {
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+// Blocks of a matrix in the passes over G: no more than 8 on an SM in all, 8 elements a thread or more.
 int norm_blocks(const OrthoArgs& g) {
   const int64_t most = (8 * (int64_t)kNumSmsGB300 + g.B - 1) / g.B;
-  const int64_t want = ((int64_t)g.N * g.K + 4095) / 4096;
-  const int64_t n = want < most ? want : most;
-  return (int)(n < 1 ? 1 : n > g.N ? g.N : n);
+  const int64_t want = ((int64_t)g.N * g.K + 8 * kNormThreads - 1) / (8 * kNormThreads);
+  return (int)(want < most ? want : most);
 }
 
 struct Layout {
@@ -477,6 +526,35 @@ cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t 
   return cudaSuccess;
 }
 
+// The norms and the first iterate.
+template <class T, int V, bool MOMENTUM>
+cudaError_t begin(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s) {
+  Input in{};
+  in.g = g.g;
+  in.batch = g.batch_stride;
+  in.row = g.row_stride;
+  in.momentum = g.momentum;
+  in.mu = g.mu;
+  in.nesterov = g.nesterov;
+  in.N = g.N;
+  in.K = g.K;
+  float2* part = reinterpret_cast<float2*>(ws + l.part);
+  const int parts = norm_blocks(g);
+  const dim3 grid(parts, g.B);
+  norm_kernel<T, V, MOMENTUM><<<grid, kNormThreads, 0, s>>>(in, part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, first_kernel<T, V, MOMENTUM>, (const Input)in, (const float2*)part, parts, g.eps,
+                            reinterpret_cast<__half*>(ws + l.x0), reinterpret_cast<__half*>(ws + l.lo), l.ldx);
+}
+
 }  // namespace
 
 size_t orthogonalize_workspace_bytes(int B, int N, int K) {
@@ -490,32 +568,17 @@ size_t orthogonalize_workspace_bytes(int B, int N, int K) {
 cudaError_t launch_orthogonalize(const OrthoArgs& g, cudaStream_t s) {
   const Layout l = layout(g);
   char* ws = static_cast<char*>(g.ws);
-  Source src{};
-  src.g = g.g;
-  src.batch = g.batch_stride;
-  src.row = g.row_stride;
-  src.dtype = g.dtype;
-  src.momentum = g.momentum;
-  src.mu = g.mu;
-  src.nesterov = g.nesterov;
-  src.B = g.B;
-  src.N = g.N;
-  src.K = g.K;
-  float2* part = reinterpret_cast<float2*>(ws + l.part);
-  const int parts = norm_blocks(g);
-  const dim3 grid(parts, g.B);
-  norm_kernel<<<grid, kNormThreads, 0, s>>>(src, part);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kNormThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, first_kernel, src, (const float2*)part, parts, g.eps,
-                         reinterpret_cast<__half*>(ws + l.x0), reinterpret_cast<__half*>(ws + l.lo), l.ldx);
+  const auto whole = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vector = g.K % 8 == 0 && g.row_stride % 8 == 0 && g.batch_stride % 8 == 0 && whole(g.g) && whole(g.momentum);
+  const bool f32 = g.dtype == MOE_DTYPE_F32;
+  cudaError_t e;
+  if (g.momentum) {
+    if (vector) e = f32 ? begin<float, 8, true>(g, l, ws, s) : begin<__nv_bfloat16, 8, true>(g, l, ws, s);
+    else e = f32 ? begin<float, 1, true>(g, l, ws, s) : begin<__nv_bfloat16, 1, true>(g, l, ws, s);
+  } else {
+    if (vector) e = f32 ? begin<float, 8, false>(g, l, ws, s) : begin<__nv_bfloat16, 8, false>(g, l, ws, s);
+    else e = f32 ? begin<float, 1, false>(g, l, ws, s) : begin<__nv_bfloat16, 1, false>(g, l, ws, s);
+  }
   if (e != cudaSuccess) return e;
   return g.N > g.K ? iterate<true>(g, l, ws, s) : iterate<false>(g, l, ws, s);
 }

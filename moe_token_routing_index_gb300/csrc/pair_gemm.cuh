@@ -210,13 +210,47 @@ struct NoSource {};
 //   kF16                             fp16 operands (else bf16)
 //   Params                           kernel parameter, with unsigned int* err
 //   Tile                             with int n (rows of B, a multiple of 32) and int k > 0, the reduction's length
-//   setup(p, tables, lane) -> int    the number of tiles (one warp; it may fill the tables)
+//   setup(p, tables) -> int          the number of tiles, called by all threads (it may fill the tables)
 //   tile(p, tables, i) -> Tile
+//   narrow(t, part, parts)           makes t its part-th of `parts` parts along B (n = 0: there is none)
 //   stage_bytes(p, t)                what both CTAs' loads of a stage complete
 //   load(p, t, rank, block, a, b, bar)
 //   epilogue(p, t, rank, sub, group, lane, tbase, wait, release)
 //     wait() -> bool: the accumulator is whole (false: give up); release(): it has been read.
 //     group: which of the quarter's two warps
+// A pair's tiles, every pairs-th, the same for all of its roles.  Of `tiles` tiles the last round, which not
+// every pair has one of, is cut into `parts` parts along B, as many as give each pair at most one: 640 tiles
+// of 256 rows are 8 rounds and 32 tiles of 128 rows on either of 64 pairs, where 9 rounds were (120 experts
+// of 344 rows, gradient: 1287 -> 1232 us); a few tiles in all become so many smaller ones.
+template <class P>
+struct Walk {
+  const typename P::Params& p;
+  const int* tables;
+  int pair, pairs, whole, parts, count, step = 0;
+  __device__ __forceinline__ Walk(const typename P::Params& p_, const int* tables_, int tiles, int pair_, int pairs_)
+      : p(p_), tables(tables_), pair(pair_), pairs(pairs_) {
+    whole = tiles / pairs * pairs;
+    const int rest = tiles - whole;
+    parts = rest ? min(kMaxN / 32, pairs / rest) : 1;
+    const int total = whole + rest * parts;
+    count = total > pair ? (total - pair + pairs - 1) / pairs : 0;
+  }
+  __device__ __forceinline__ bool next(typename P::Tile* t) {
+    while (step < count) {
+      const int i = pair + step++ * pairs;
+      if (i < whole) {
+        *t = P::tile(p, tables, i);
+        return true;
+      }
+      const int j = (i - whole) / parts;
+      *t = P::tile(p, tables, whole + j);
+      P::narrow(t, i - whole - j * parts, parts);
+      if (t->n > 0) return true;
+    }
+    return false;
+  }
+};
+
 template <class P>
 __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -235,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
   const uint32_t bar_drain = smem_u32(&bars[2 * kStages + 2 * kAccBufs]);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
-  int* s_total = reinterpret_cast<int*>(smem + Smem::misc + 8);
   int* tables = reinterpret_cast<int*>(smem + Smem::tables);
 
   pdl_launch_dependents();
@@ -260,16 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   pdl_wait();  // what the previous kernel of the stream wrote
-  if (warp == 2) {
-    const int total = P::setup(p, tables, lane);
-    if (lane == 0) *s_total = total;
-  }
+  Walk<P> walk(p, tables, P::setup(p, tables), pair, pairs);
+  typename P::Tile t;
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  const int total = *s_total;
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
@@ -278,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
       int s = 0;
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      for (int i = pair; i < total && ok; i += pairs) {
-        const typename P::Tile t = P::tile(p, tables, i);
+      while (ok && walk.next(&t)) {
         const uint32_t bytes = P::stage_bytes(p, t);
         const int blocks = (t.k + kBK - 1) / kBK;
         for (int kb = 0; kb < blocks; ++kb) {
@@ -323,8 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
       int s = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued_any = false;
-      for (int i = pair; i < total && ok; i += pairs) {
-        const typename P::Tile t = P::tile(p, tables, i);
+      while (ok && walk.next(&t)) {
         const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort));
         if (!ok) break;
@@ -374,8 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int i = pair; i < total && ok; i += pairs) {
-      const typename P::Tile t = P::tile(p, tables, i);
+    while (ok && walk.next(&t)) {
       const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kMaxN);
       P::epilogue(
           p, t, rank, sub, (warp - 2) >> 2, lane, tbase,
@@ -432,7 +459,7 @@ inline bool make_map_3d(CUtensorMap* map, const void* base, bool f16, int64_t co
   return make_map(map, base, f16, 3, dims, strides, box);
 }
 
-// tiles: at most so many.  pdl: the launch may begin before the stream's previous kernel ends.
+// tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's previous kernel ends.
 template <class P>
 cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int table_ints, bool pdl, cudaStream_t s) {
   const int smem = Smem::tables + table_ints * 4 + 1024;
@@ -456,7 +483,7 @@ cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int table_i
   e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
   if (e != cudaSuccess) return e;
   if (pairs < 1) return cudaErrorNotSupported;
-  if (tiles < pairs) pairs = (int)tiles;
+  if (tiles * (kMaxN / 32) < pairs) pairs = (int)tiles * (kMaxN / 32);
   if (pairs < 1) return cudaSuccess;
   cfg.gridDim = dim3(2 * pairs);
   cfg.numAttrs = pdl ? 2 : 1;
