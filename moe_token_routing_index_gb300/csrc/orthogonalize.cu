@@ -115,8 +115,9 @@ __device__ __forceinline__ void each_value(const Input& p, int b, Take take) {
 
 // Matrix blockIdx.y: the momentum is updated, and the squares of u are summed into part.
 template <class T, int V, bool MOMENTUM>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p, float2* part) {
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p, float2* part, unsigned int* arrived) {
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *arrived = 0u;  // of the products' barriers
   Squares q;
   each_value<T, V, MOMENTUM>(p, blockIdx.y, [&](uint32_t, uint32_t, const float* u, const float* m, float* to) {
     float v[V];
@@ -179,41 +180,19 @@ __global__ void __launch_bounds__(kNormThreads) first_kernel(const Input p, cons
 struct MatTile {
   int n, k;
   int at, row, col;    // the matrix, first row and first column
+  int k0, split;       // where its part of the reduction begins, and which part that is
   bool mirror;         // symmetric results: stored across the diagonal too
 };
 
-struct Mats {
-  CUtensorMap a, b[kHeights];
+enum Product { kGram, kPartial, kReduce, kPolynomial, kNext, kOut, kWeights };
+
+struct Dims {
   int count, rows, cols;  // of the result
-  int ct, rt;             // tiles along its columns and rows
+  int ct;                 // tiles along its columns
   int per;                // tiles of a matrix
   int k;                  // the reduction's length
+  int splits, part_k;     // kPartial: parts of the reduction, and the length of one
 };
-
-// SYM: the tiles of row block >= column block (cols == rows).
-template <bool SYM>
-__device__ __forceinline__ MatTile locate_mat(const Mats& p, int i) {
-  MatTile t;
-  t.at = i / p.per;
-  const int l = i - t.at * p.per;
-  int r, c;
-  if (SYM) {  // row block r has the column blocks 0 .. r
-    r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
-    while (r * (r + 1) / 2 > l) --r;
-    while ((r + 1) * (r + 2) / 2 <= l) ++r;
-    c = l - r * (r + 1) / 2;
-    t.mirror = c != r;
-  } else {
-    r = l / p.ct;
-    c = l - r * p.ct;
-    t.mirror = false;
-  }
-  t.row = r * kTileM;
-  t.col = c * kMaxN;
-  t.n = min(kMaxN, (p.cols - t.col + 31) / 32 * 32);
-  t.k = p.k;
-  return t;
-}
 
 // 32 bytes of a lane.
 __device__ __forceinline__ void load32(const void* p, uint32_t* r) {
@@ -227,13 +206,12 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
                : "memory");
 }
 
-enum Product { kGram, kPolynomial, kNext, kOut, kWeights };
-
 struct Result {
   __half* sym;          // A or P, rows ldm elements apart
   const __half* src;    // P: A.  X: its first half
   __half* next;         // X's next first half
   __half* lo;           // X's second half, in place
+  float* partial;       // A's parts: [splits][count][rows] of ld
   void* out;            // bf16 result, or weights
   int ld;               // of sym and src's matrices; X: of src, next and lo
   float alpha, beta;    // result = alpha * src + beta * product
@@ -247,31 +225,60 @@ template <bool AMN, bool BMN, Product KIND>
 struct Ns {
   static constexpr bool kAMN = AMN, kBMN = BMN, kF16 = true;
   static constexpr bool kSym = KIND == kGram || KIND == kPolynomial;
+  static constexpr bool kX = KIND == kNext || KIND == kOut || KIND == kWeights;
   struct Params {
-    Mats m;
+    const CUtensorMap *a, *b;  // b: by box height where it is K-major
+    Dims d;
     Result r;
-    unsigned int* err;
   };
   using Tile = MatTile;
-  static __device__ int setup(const Params& p, int*) { return p.m.count * p.m.per; }
-  static __device__ void narrow(Tile* t, int part, int parts) {
+  // Symmetric results: the tiles of row block >= column block.
+  static __device__ __forceinline__ Tile tile(const Params& p, const int*, int i) {
+    const Dims& d = p.d;
+    Tile t;
+    t.at = i / d.per;
+    int l = i - t.at * d.per, r, c;
+    t.k0 = t.split = 0;
+    t.k = d.k;
+    t.mirror = false;
+    if (KIND == kPartial) {
+      t.split = l % d.splits;
+      l /= d.splits;
+      t.k0 = t.split * d.part_k;
+      t.k = min(d.part_k, d.k - t.k0);
+    }
+    if (kSym) {  // row block r has the column blocks 0 .. r
+      r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+      while (r * (r + 1) / 2 > l) --r;
+      while ((r + 1) * (r + 2) / 2 <= l) ++r;
+      c = l - r * (r + 1) / 2;
+      t.mirror = c != r;
+    } else {
+      r = l / d.ct;
+      c = l - r * d.ct;
+    }
+    t.row = r * kTileM;
+    t.col = c * kMaxN;
+    t.n = min(kMaxN, (d.cols - t.col + 31) / 32 * 32);
+    return t;
+  }
+  static __device__ __forceinline__ void narrow(Tile* t, int part, int parts) {
     const int n = ((t->n + parts - 1) / parts + 31) / 32 * 32, from = part * n;
     t->col += from;
     t->n = max(0, min(n, t->n - from));
   }
-  static __device__ Tile tile(const Params& p, const int*, int i) { return locate_mat<kSym>(p.m, i); }
-  static __device__ uint32_t stage_bytes(const Params&, const Tile& t) {
+  static __device__ __forceinline__ uint32_t stage_bytes(const Params&, const Tile& t) {
     return 2u * (uint32_t)(kOperandBytes + (BMN ? kOperandBytes : t.n / 2 * 128 * (kBK / 64)));
   }
-  static __device__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
-                              uint32_t bar) {
-    load_half<AMN>(a, &p.m.a, bar, block * kBK, t.row + rank * kHalfM, t.at);
-    const int col = t.col + rank * (t.n / 2);
-    load_half<BMN>(b, &p.m.b[BMN ? 0 : t.n / 32 - 1], bar, block * kBK, col, t.at);
+  static __device__ __forceinline__ void load(const Params& p, const Tile& t, int rank, int block, uint32_t a, uint32_t b,
+                                              uint32_t bar) {
+    const int k = t.k0 + block * kBK;
+    load_half<AMN>(a, p.a, bar, k, t.row + rank * kHalfM, t.at);
+    load_half<BMN>(b, p.b + (BMN ? 0 : t.n / 32 - 1), bar, k, t.col + rank * (t.n / 2), t.at);
   }
   static constexpr int kWords = kChunk / 2;
   struct Source {  // a chunk of a row: of X's halves, or of A; of the weights
-    uint32_t hi[KIND == kGram ? 1 : kWords], lo[kSym ? 1 : kWords];
+    uint32_t hi[kX || KIND == kPolynomial ? kWords : 1], lo[kX ? kWords : 1];
     uint32_t w[KIND == kWeights ? kChunk : 1];
   };
   static __device__ __forceinline__ float2 halves(uint32_t w) {
@@ -286,20 +293,20 @@ struct Ns {
                                   Wait wait, Release release) {
     const Result& g = p.r;
     const int row = t.row + rank * kHalfM + sub * 32 + lane;
-    const bool keep = row < p.m.rows;
-    const int cols = min(t.n, p.m.cols - t.col);
+    const bool keep = row < p.d.rows;
+    const int cols = min(t.n, p.d.cols - t.col);
     // rows of the workspace are multiples of kChunk apart: whole chunks are read and written, what lies past
     // the columns is not read as an operand
-    const int64_t matrix = (int64_t)t.at * p.m.rows * g.ld;
+    const int64_t matrix = (int64_t)t.at * p.d.rows * g.ld;
     const int64_t at = matrix + (int64_t)(keep ? row : 0) * g.ld + t.col;
-    const int64_t out_at = ((int64_t)t.at * p.m.rows + (keep ? row : 0)) * p.m.cols + t.col;
+    const int64_t out_at = ((int64_t)t.at * p.d.rows + (keep ? row : 0)) * p.d.cols + t.col;
     float lr = 1.0f;
     if (KIND == kWeights && g.lr) lr = __ldg(g.lr);
     const float w_keep = 1.0f - lr * g.keep, w_scale = lr * g.scale;
     const bool f32 = KIND == kWeights && g.w_dtype == MOE_DTYPE_F32;
     auto load = [&](int c, Source& s) {
-      if constexpr (KIND != kGram) load32(g.src + at + c, s.hi);
-      if constexpr (!kSym) load32(g.lo + at + c, s.lo);
+      if constexpr (kX || KIND == kPolynomial) load32(g.src + at + c, s.hi);
+      if constexpr (kX) load32(g.lo + at + c, s.lo);
       if constexpr (KIND == kWeights) {
         if (g.whole) {
           if (f32) {
@@ -317,15 +324,22 @@ struct Ns {
         }
       }
     };
+    auto part = [&](int c, const Source&, const float* v) {
+      float* o = g.partial + (int64_t)t.split * p.d.count * p.d.rows * g.ld + at + c;
+      if (keep) {
+        store32(o, reinterpret_cast<const uint32_t*>(v));
+        store32(o + 8, reinterpret_cast<const uint32_t*>(v) + 8);
+      }
+    };
     auto use = [&](int c, const Source& s, float* v) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         float2 x = make_float2(v[2 * i] * g.beta, v[2 * i + 1] * g.beta);
-        if constexpr (KIND != kGram) {
+        if constexpr (kX || KIND == kPolynomial) {
           const float2 h = halves(s.hi[i]);
           x = make_float2(fmaf(g.alpha, h.x, x.x), fmaf(g.alpha, h.y, x.y));
         }
-        if constexpr (!kSym) {
+        if constexpr (kX) {
           const float2 l = halves(s.lo[i]);
           x = make_float2(fmaf(g.alpha, l.x, x.x), fmaf(g.alpha, l.y, x.y));
         }
@@ -352,7 +366,7 @@ struct Ns {
           for (int j = 0; j < kWords; ++j) {
             const float2 w = deal(v, j, odd);
             // (an odd last row's pair writes one element into the padding)
-            if ((row & ~1) < p.m.rows && c + 2 * j + odd < cols)
+            if ((row & ~1) < p.d.rows && c + 2 * j + odd < cols)
               *reinterpret_cast<uint32_t*>(m + (int64_t)(2 * j) * g.ld) = pack_half(w.x, w.y);
           }
         }
@@ -395,9 +409,181 @@ struct Ns {
         }
       }
     };
-    by_chunks<Source>(cols, group, tbase, load, use, wait, release);
+    if constexpr (KIND == kPartial) by_chunks<Source>(cols, group, tbase, load, part, wait, release);
+    else by_chunks<Source>(cols, group, tbase, load, use, wait, release);
   }
 };
+
+// ------------------------------------------------------------------ iteration
+
+// All products of a call in one launch, with a barrier over the grid between them: of small matrices a
+// product's launch, prologue and first loads took 8 us each.  The epilogue's warps arrive when a CTA's
+// results are stored; they and the producer wait.
+struct Plan {
+  CUtensorMap x_rows[2], x_cols[2];        // X as A: boxes of 128 rows, or of kBK rows x 64 columns
+  CUtensorMap x_low[2][kHeights];          // X as a K-major B
+  CUtensorMap gram, gram_low[kHeights];
+  CUtensorMap poly, poly_low[kHeights];
+  Dims sym, sym_poly, square;              // A, P, X
+  __half *x[2], *lo, *a, *p;
+  float* partial;
+  int steps, m, ldx, ldm;
+  float coef[3];
+  Result last;                             // out and what goes with it
+  unsigned int* arrived;
+  unsigned int* err;
+};
+
+constexpr int kEpiThreads = 32 * kEpiWarps;
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+
+// Until `target` CTAs have arrived (bounded).
+__device__ __forceinline__ bool wait_grid(const Block& b, const unsigned int* arrived, unsigned int target) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
+    if (v >= target) return true;
+    if (i == 0) t0 = global_timer_ns();
+    if ((i & 63) == 63 && (*b.abort || global_timer_ns() - t0 > kWaitTimeoutNs)) return false;
+  }
+}
+
+// A from its parts, added in order: 8 elements a thread.
+__device__ __forceinline__ void reduce_parts(const Plan& p, int thread) {
+  const int64_t size = (int64_t)p.sym.count * p.m * p.ldm;
+  for (int64_t i = ((int64_t)blockIdx.x * kEpiThreads + thread) * 8; i < size; i += (int64_t)gridDim.x * kEpiThreads * 8) {
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.sym.splits; ++s) {
+      uint32_t w[8];
+      load32(p.partial + s * size + i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(w[j]);
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 x = __floats2half2_rn(v[2 * j] * kUnscale, v[2 * j + 1] * kUnscale);
+      h[j] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    *reinterpret_cast<uint4*>(p.a + i) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+// Calls role(policy, its parameters) for product `kind` of a step.
+template <bool TALL, Product LAST, class Role>
+__device__ __forceinline__ bool product(const Plan& p, Product kind, int step, Role role) {
+  const int cur = step & 1;
+  Result r = p.last;
+  r.src = p.x[cur];
+  r.lo = p.lo;
+  if (kind == kGram || kind == kPartial) {
+    r.sym = p.a;
+    r.partial = p.partial;
+    r.ld = p.ldm;
+    r.beta = kUnscale;
+    const CUtensorMap* a = TALL ? &p.x_cols[cur] : &p.x_rows[cur];
+    const CUtensorMap* b = TALL ? &p.x_cols[cur] : p.x_low[cur];
+    using G = Ns<TALL, TALL, kGram>;
+    using S = Ns<TALL, TALL, kPartial>;
+    if (kind == kGram) return role(G(), typename G::Params{a, b, p.sym, r});
+    return role(S(), typename S::Params{a, b, p.sym, r});
+  }
+  if (kind == kPolynomial) {
+    using P = Ns<false, false, kPolynomial>;
+    r.sym = p.p;
+    r.src = p.a;
+    r.ld = p.ldm;
+    r.alpha = p.coef[1];
+    r.beta = p.coef[2] * kUnscale;
+    return role(P(), typename P::Params{&p.gram, p.gram_low, p.sym_poly, r});
+  }
+  // X [N, K]: P X (wide: P's rows, X's columns) or X P (tall: X's rows, P's rows, as P is symmetric)
+  r.next = p.x[cur ^ 1];
+  r.ld = p.ldx;
+  r.alpha = p.coef[0];
+  r.beta = kUnscale;
+  const CUtensorMap* a = TALL ? &p.x_rows[cur] : &p.poly;
+  const CUtensorMap* b = TALL ? p.poly_low : &p.x_cols[cur];
+  using N = Ns<false, !TALL, kNext>;
+  using L = Ns<false, !TALL, LAST>;
+  if (kind == kNext) return role(N(), typename N::Params{a, b, p.square, r});
+  return role(L(), typename L::Params{a, b, p.square, r});
+}
+
+template <bool TALL, Product LAST>
+__global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_constant__ Plan p) {
+  extern __shared__ uint8_t smem_raw[];
+  Block b;
+  b.begin(smem_raw, p.err);
+  b.meet();
+  // the products in order, with how many barriers lie before each
+  auto all = [&](auto run) {
+    unsigned int before = 0;
+    bool ok = true;
+    for (int step = 0; step < p.steps && ok; ++step) {
+      const bool split = p.sym.splits > 1;
+      ok = run(split ? kPartial : kGram, step, before++);
+      if (ok && split) ok = run(kReduce, step, before++);
+      if (ok) ok = run(kPolynomial, step, before++);
+      if (ok) ok = run(step + 1 < p.steps ? kNext : LAST, step, before++);
+    }
+    return ok;
+  };
+  auto walk = [&](const auto& params, auto policy) {
+    using P = decltype(policy);
+    return Walk<P>(params, nullptr, params.d.count * params.d.per, b.pair, b.pairs);
+  };
+  if (b.warp == 0) {
+    if (b.lane == 0) {
+      Producer r(b);
+      r.finish(all([&](Product kind, int step, unsigned int before) {
+        if (kind == kReduce) return true;
+        if (!wait_grid(b, p.arrived, before * gridDim.x)) return false;
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // the loads see what other CTAs stored
+        return product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+          return r.template run<decltype(policy)>(params, walk(params, policy));
+        });
+      }));
+    }
+  } else if (b.warp == 1) {
+    if (b.rank == 0) {
+      Issuer r(b);
+      r.finish(all([&](Product kind, int step, unsigned int) {
+        if (kind == kReduce) return true;
+        return product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+          return r.template run<decltype(policy)>(walk(params, policy));
+        });
+      }));
+    }
+  } else {
+    Epilogue r(b);
+    const int thread = threadIdx.x - 64;
+    int* s_ok = b.tables();
+    all([&](Product kind, int step, unsigned int before) {
+      if (kind == kReduce) {
+        reduce_parts(p, thread);
+      } else {  // (a warp that gives up raises the abort flag, and stays for the barriers)
+        product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+          return r.template run<decltype(policy)>(params, walk(params, policy));
+        });
+      }
+      if (kind == LAST) return true;
+      // this CTA's results are stored; then those of all
+      epilogue_sync();
+      if (thread == 0) {  // (the release covers what the other warps stored before the barrier)
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.arrived) : "memory");
+        const bool all_here = wait_grid(b, p.arrived, (before + 1) * gridDim.x);
+        if (!all_here) b.fail();
+        *s_ok = all_here && !*b.abort;
+      }
+      epilogue_sync();
+      return *s_ok != 0;
+    });
+  }
+  b.end();
+}
 
 // ------------------------------------------------------------------- host
 
@@ -410,9 +596,14 @@ int norm_blocks(const OrthoArgs& g) {
   return (int)(want < most ? want : most);
 }
 
+constexpr int kPairsGB300 = kNumSmsGB300 / 2;
+// A's reduction is split where its tiles are few and each would take long: what it saves, in blocks of
+// kBK, has to be worth a barrier and a pass over the parts (about 4 us).
+constexpr int kWorthSplitting = 24;
+
 struct Layout {
-  int m, ldx, ldm;
-  size_t part, x0, x1, lo, gram, poly, total;  // offsets
+  int m, ldx, ldm, splits;
+  size_t arrived, part, x0, x1, lo, gram, poly, partial, total;  // offsets
 };
 
 Layout layout(const OrthoArgs& g) {
@@ -420,110 +611,89 @@ Layout layout(const OrthoArgs& g) {
   l.m = g.N < g.K ? g.N : g.K;
   l.ldx = (int)up(g.K, kChunk);
   l.ldm = (int)up(l.m, kChunk);
+  const int64_t side = (l.m + kTileM - 1) / kTileM, blocks = ((g.N < g.K ? g.K : g.N) + kBK - 1) / kBK;
+  int64_t splits = kPairsGB300 / (g.B * side * side);
+  if (splits > blocks / 4) splits = blocks / 4;
+  l.splits = splits > 1 && blocks - blocks / splits >= kWorthSplitting ? (int)splits : 1;
   const size_t x = up((int64_t)g.B * g.N * l.ldx * 2, 256), sym = up((int64_t)g.B * l.m * l.ldm * 2, 256);
-  l.part = 0;
-  l.x0 = up((int64_t)g.B * norm_blocks(g) * (int64_t)sizeof(float2), 256);
+  l.arrived = 0;
+  l.part = 256;
+  l.x0 = l.part + up((int64_t)g.B * norm_blocks(g) * (int64_t)sizeof(float2), 256);
   l.x1 = l.x0 + x;
   l.lo = l.x1 + x;
   l.gram = l.lo + x;
   l.poly = l.gram + sym;
-  l.total = l.poly + sym;
+  l.partial = l.poly + sym;
+  l.total = l.partial + (l.splits > 1 ? 2 * sym * l.splits : 0);
   return l;
 }
 
-// The result [rows, cols] of count matrices; reduction over k.
-bool make_mats(Mats* m, const OrthoArgs& g, int rows, int cols, int k, bool sym) {
-  m->count = g.B;
-  m->rows = rows;
-  m->cols = cols;
-  m->ct = (cols + kMaxN - 1) / kMaxN;
-  m->rt = (rows + kTileM - 1) / kTileM;
-  m->k = k;
-  m->per = sym ? m->rt * (m->rt + 1) / 2 : m->rt * m->ct;
-  return (int64_t)m->per * g.B <= INT32_MAX / 2;
-}
-
-// The operand maps: matrices [rows, cols] with rows ld elements apart.
-bool map_a(Mats* m, bool mn, const void* x, int count, int rows, int cols, int ld) {
-  return make_map_3d(&m->a, x, true, count, rows, cols, ld, mn ? kBK : kHalfM);
-}
-bool map_b(Mats* m, bool mn, const void* x, int count, int rows, int cols, int ld) {
-  for (int h = 0; h < kHeights; ++h)
-    if (!make_map_3d(&m->b[h], x, true, count, rows, cols, ld, mn ? kBK : box_rows(h))) return false;
+// The tiles of a result [rows, cols] of each matrix; reduction over k.
+bool make_dims(Dims* d, int B, int rows, int cols, int k, bool sym, int splits) {
+  const int rt = (rows + kTileM - 1) / kTileM;
+  d->count = B;
+  d->rows = rows;
+  d->cols = cols;
+  d->ct = (cols + kMaxN - 1) / kMaxN;
+  d->k = k;
+  d->splits = splits;
+  const int blocks = (k + kBK - 1) / kBK;
+  d->part_k = (blocks + splits - 1) / splits * kBK;
+  d->splits = (k + d->part_k - 1) / d->part_k;  // parts that are not empty
+  const int64_t per = sym && splits == 1 ? (int64_t)rt * (rt + 1) / 2 : (int64_t)rt * d->ct * d->splits;
+  if (per * B > INT32_MAX / 16) return false;
+  d->per = (int)per;
   return true;
 }
 
-template <class P>
-cudaError_t launch(const typename P::Params& p, cudaStream_t s) {
-  return launch_pairs<P>(p, (int64_t)p.m.count * p.m.per, 0, true, s);
-}
-
-template <bool TALL, Product KIND>
-cudaError_t multiply(const OrthoArgs& g, const Layout& l, const Result& r, const __half* poly, cudaStream_t s) {
-  // X [N, K]: P X (wide: P's rows, X's columns) or X P (tall: X's rows, P's rows, as P is symmetric)
-  using P = Ns<false, !TALL, KIND>;
-  typename P::Params p{};
-  if (!make_mats(&p.m, g, g.N, g.K, l.m, false)) return cudaErrorNotSupported;
-  if (TALL ? !(map_a(&p.m, false, r.src, g.B, g.N, g.K, l.ldx) && map_b(&p.m, false, poly, g.B, l.m, l.m, l.ldm))
-           : !(map_a(&p.m, false, poly, g.B, l.m, l.m, l.ldm) && map_b(&p.m, true, r.src, g.B, g.N, g.K, l.ldx)))
-    return cudaErrorInvalidValue;
-  p.r = r;
-  p.err = g.err;
-  return launch<P>(p, s);
-}
-
-template <bool TALL>
+template <bool TALL, Product LAST>
 cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s) {
-  __half* x[2] = {reinterpret_cast<__half*>(ws + l.x0), reinterpret_cast<__half*>(ws + l.x1)};
-  __half* gram = reinterpret_cast<__half*>(ws + l.gram);
-  __half* poly = reinterpret_cast<__half*>(ws + l.poly);
-  using Gram = Ns<TALL, TALL, kGram>;
-  using Poly = Ns<false, false, kPolynomial>;
-  for (int step = 0; step < g.steps; ++step) {
-    const __half* cur = x[step & 1];
-    typename Gram::Params a{};
-    if (!make_mats(&a.m, g, l.m, l.m, TALL ? g.N : g.K, true)) return cudaErrorNotSupported;
-    if (!map_a(&a.m, TALL, cur, g.B, g.N, g.K, l.ldx) || !map_b(&a.m, TALL, cur, g.B, g.N, g.K, l.ldx))
-      return cudaErrorInvalidValue;
-    a.r.sym = gram;
-    a.r.ld = l.ldm;
-    a.r.beta = kUnscale;
-    a.err = g.err;
-    cudaError_t e = launch<Gram>(a, s);
-    if (e != cudaSuccess) return e;
-
-    typename Poly::Params q{};
-    if (!make_mats(&q.m, g, l.m, l.m, l.m, true)) return cudaErrorNotSupported;
-    if (!map_a(&q.m, false, gram, g.B, l.m, l.m, l.ldm) || !map_b(&q.m, false, gram, g.B, l.m, l.m, l.ldm))
-      return cudaErrorInvalidValue;
-    q.r.sym = poly;
-    q.r.src = gram;
-    q.r.ld = l.ldm;
-    q.r.alpha = g.coef[1];
-    q.r.beta = g.coef[2] * kUnscale;
-    q.err = g.err;
-    e = launch<Poly>(q, s);
-    if (e != cudaSuccess) return e;
-
-    Result r{};
-    r.src = cur;
-    r.next = x[(step + 1) & 1];
-    r.lo = reinterpret_cast<__half*>(ws + l.lo);
-    r.ld = l.ldx;
-    r.alpha = g.coef[0];
-    r.beta = kUnscale;
-    r.out = g.out;
-    r.scale = kUnscale * g.scale;
-    r.keep = g.decay;
-    r.lr = g.lr;
-    r.w_dtype = g.w_dtype;
-    r.whole = g.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31) == 0;
-    if (step + 1 < g.steps) e = multiply<TALL, kNext>(g, l, r, poly, s);
-    else if (g.update) e = multiply<TALL, kWeights>(g, l, r, poly, s);
-    else e = multiply<TALL, kOut>(g, l, r, poly, s);
-    if (e != cudaSuccess) return e;
+  Plan p{};
+  const int n = TALL ? g.N : g.K;
+  if (!make_dims(&p.sym, g.B, l.m, l.m, n, true, l.splits) || !make_dims(&p.sym_poly, g.B, l.m, l.m, l.m, true, 1) ||
+      !make_dims(&p.square, g.B, g.N, g.K, l.m, false, 1))
+    return cudaErrorNotSupported;
+  p.x[0] = reinterpret_cast<__half*>(ws + l.x0);
+  p.x[1] = reinterpret_cast<__half*>(ws + l.x1);
+  p.lo = reinterpret_cast<__half*>(ws + l.lo);
+  p.a = reinterpret_cast<__half*>(ws + l.gram);
+  p.p = reinterpret_cast<__half*>(ws + l.poly);
+  p.partial = reinterpret_cast<float*>(ws + l.partial);
+  auto map = [&](CUtensorMap* to, const void* x, bool of_x, int box) {
+    return of_x ? make_map_3d(to, x, true, g.B, g.N, g.K, l.ldx, box) : make_map_3d(to, x, true, g.B, l.m, l.m, l.ldm, box);
+  };
+  bool ok = map(&p.gram, p.a, false, kHalfM) && map(&p.poly, p.p, false, kHalfM);
+  for (int i = 0; i < 2 && ok; ++i) ok = map(&p.x_rows[i], p.x[i], true, kHalfM) && map(&p.x_cols[i], p.x[i], true, kBK);
+  for (int h = 0; h < kHeights && ok; ++h) {
+    ok = map(&p.gram_low[h], p.a, false, box_rows(h));
+    if (ok && TALL) ok = map(&p.poly_low[h], p.p, false, box_rows(h));
+    for (int i = 0; i < 2 && ok && !TALL; ++i) ok = map(&p.x_low[i][h], p.x[i], true, box_rows(h));
   }
-  return cudaSuccess;
+  if (!ok) return cudaErrorInvalidValue;
+  p.steps = g.steps;
+  p.m = l.m;
+  p.ldx = l.ldx;
+  p.ldm = l.ldm;
+  for (int i = 0; i < 3; ++i) p.coef[i] = g.coef[i];
+  p.last.out = g.out;
+  p.last.scale = kUnscale * g.scale;
+  p.last.keep = g.decay;
+  p.last.lr = g.lr;
+  p.last.w_dtype = g.w_dtype;
+  p.last.whole = g.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31) == 0;
+  p.arrived = reinterpret_cast<unsigned int*>(ws + l.arrived);
+  p.err = g.err;
+  // no more pairs than the product with the most tiles, cut as they may be, has work for
+  int64_t most = p.sym.per > p.square.per ? p.sym.per : p.square.per;
+  most *= (int64_t)g.B * (kMaxN / 32);
+  Launch launch;
+  const auto kern = iterate_kernel<TALL, LAST>;
+  cudaError_t e = launch.prepare(kern, 4, most, s);
+  if (e != cudaSuccess) return e;
+  launch.attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all are resident
+  launch.attr[1].val.cooperative = 1;
+  launch.cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&launch.cfg, kern, p);
 }
 
 // The norms and the first iterate.
@@ -541,7 +711,7 @@ cudaError_t begin(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s)
   float2* part = reinterpret_cast<float2*>(ws + l.part);
   const int parts = norm_blocks(g);
   const dim3 grid(parts, g.B);
-  norm_kernel<T, V, MOMENTUM><<<grid, kNormThreads, 0, s>>>(in, part);
+  norm_kernel<T, V, MOMENTUM><<<grid, kNormThreads, 0, s>>>(in, part, reinterpret_cast<unsigned int*>(ws + l.arrived));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -580,7 +750,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& g, cudaStream_t s) {
     else e = f32 ? begin<float, 1, false>(g, l, ws, s) : begin<__nv_bfloat16, 1, false>(g, l, ws, s);
   }
   if (e != cudaSuccess) return e;
-  return g.N > g.K ? iterate<true>(g, l, ws, s) : iterate<false>(g, l, ws, s);
+  if (g.update) return g.N > g.K ? iterate<true, kWeights>(g, l, ws, s) : iterate<false, kWeights>(g, l, ws, s);
+  return g.N > g.K ? iterate<true, kOut>(g, l, ws, s) : iterate<false, kOut>(g, l, ws, s);
 }
 
 }  // namespace moe

@@ -182,24 +182,27 @@ __device__ __forceinline__ float2 deal(const float* v, int j, bool odd) {
 }
 
 // An epilogue over `rows` columns of a tile: load(c, s) brings what column chunk c needs from memory
-// into s, ahead of the chunk's turn (the first before the accumulator is waited for); use(c, s, v)
+// into s, two chunks ahead (the first two before the accumulator is waited for); use(c, s, v)
 // takes it with the accumulator's columns c .. c + kChunk - 1.
 template <class Source, class Load, class Use, class Wait, class Release>
 __device__ __forceinline__ void by_chunks(int rows, int group, uint32_t tbase, Load load, Use use, Wait wait,
                                           Release release) {
+  constexpr int kStep = kEpiGroups * kChunk;
   int c = group * kChunk;
-  Source s{};
+  Source s{}, next{};
   if (c < rows) load(c, s);
+  if (c + kStep < rows) load(c + kStep, next);
   if (!wait()) return;
   while (c < rows) {
     float v[kChunk];
     tmem_ld_chunk(tbase + c, v);
-    Source next{};
-    if (c + kEpiGroups * kChunk < rows) load(c + kEpiGroups * kChunk, next);
-    else release();
+    Source later{};
+    if (c + 2 * kStep < rows) load(c + 2 * kStep, later);
+    if (c + kStep >= rows) release();
     use(c, s, v);
     s = next;
-    c += kEpiGroups * kChunk;
+    next = later;
+    c += kStep;
   }
   if (group * kChunk >= rows) release();
 }
@@ -251,189 +254,242 @@ struct Walk {
   }
 };
 
-template <class P>
-__global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)(cluster_ctarank() & 1u);
-  const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
-  auto bar_full = [&](int s) { return smem_u32(&bars[s]); };
-  auto bar_empty = [&](int s) { return smem_u32(&bars[kStages + s]); };
-  auto bar_tfull = [&](int b) { return smem_u32(&bars[2 * kStages + b]); };
-  auto bar_tempty = [&](int b) { return smem_u32(&bars[2 * kStages + kAccBufs + b]); };
-  const uint32_t bar_drain = smem_u32(&bars[2 * kStages + 2 * kAccBufs]);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::misc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
-  int* tables = reinterpret_cast<int*>(smem + Smem::tables);
+// What the roles of a CTA share.
+struct Block {
+  uint8_t* smem;
+  uint32_t sbase, tmem;
+  int warp, lane, rank, pair, pairs;
+  volatile int* abort;
+  unsigned int* err;
 
-  pdl_launch_dependents();
-  if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
-    }
-    for (int b = 0; b < kAccBufs; ++b) {
-      mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), 2 * kEpiWarps);  // of both CTAs
-    }
-    mbar_init(bar_drain, 1);
-    *s_abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-  pdl_wait();  // what the previous kernel of the stream wrote
-  Walk<P> walk(p, tables, P::setup(p, tables), pair, pairs);
-  typename P::Tile t;
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
-  tc_fence_after();
-  const uint32_t tmem_base = *s_tmem;
+  __device__ __forceinline__ uint32_t bar(int i) const { return sbase + Smem::bars + 8 * i; }
+  __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }  // the leader's: both CTAs' stages are whole
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar(kStages + s); }
+  __device__ __forceinline__ uint32_t tfull(int b) const { return bar(2 * kStages + b); }
+  __device__ __forceinline__ uint32_t tempty(int b) const { return bar(2 * kStages + kAccBufs + b); }
+  __device__ __forceinline__ uint32_t drain() const { return bar(2 * kStages + 2 * kAccBufs); }
+  __device__ __forceinline__ int* tables() const { return reinterpret_cast<int*>(smem + Smem::tables); }
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint32_t full0 = map_to_rank(bar_full(0), 0);
-      int s = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
-      bool ok = true;
-      while (ok && walk.next(&t)) {
-        const uint32_t bytes = P::stage_bytes(p, t);
-        const int blocks = (t.k + kBK - 1) / kBK;
-        for (int kb = 0; kb < blocks; ++kb) {
-          if (!mbar_wait(bar_empty(s), phase ^ 1u, s_abort)) {
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(bar_full(s), bytes);
-          const uint32_t a = sbase + Smem::stage + s * kStageBytes;
-          P::load(p, t, rank, kb, a, a + kOperandBytes, full0 + (uint32_t)(s * 8));
-          issued_mask |= 1u << s;
-          issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1u;
-          }
+  // Barriers and tensor memory; then what the previous kernel of the stream wrote may be read.
+  __device__ __forceinline__ void begin(uint8_t* raw, unsigned int* error) {
+    const uint32_t raw_addr = smem_u32(raw);
+    smem = raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    sbase = smem_u32(smem);
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    rank = (int)(cluster_ctarank() & 1u);
+    pair = blockIdx.x >> 1;
+    pairs = gridDim.x >> 1;
+    abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
+    err = error;
+    pdl_launch_dependents();
+    if (warp == 0 && lane == 0) {
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(full(s), 1);
+        mbar_init(empty(s), 1);
+      }
+      for (int b = 0; b < kAccBufs; ++b) {
+        mbar_init(tfull(b), 1);
+        mbar_init(tempty(b), 2 * kEpiWarps);  // of both CTAs
+      }
+      mbar_init(drain(), 1);
+      *abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + Smem::misc),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+  }
+  // Both CTAs' barriers exist before any arrival from the other.
+  __device__ __forceinline__ void meet() {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    tmem = *reinterpret_cast<const uint32_t*>(smem + Smem::misc);
+  }
+  // The pair meets, then frees its tensor memory together.
+  __device__ __forceinline__ void end() {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+  __device__ __forceinline__ void fail() const {
+    flag_error(err, MOE_DEVERR_TIMEOUT);
+    *abort = 1;
+  }
+};
+
+// The TMA producer, one lane.
+struct Producer {
+  const Block& b;
+  uint32_t full0;
+  int s = 0;
+  uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+  __device__ __forceinline__ explicit Producer(const Block& b_) : b(b_), full0(map_to_rank(b_.full(0), 0)) {}
+
+  template <class P>
+  __device__ __forceinline__ bool run(const typename P::Params& p, Walk<P> walk) {
+    typename P::Tile t;
+    while (walk.next(&t)) {
+      const uint32_t bytes = P::stage_bytes(p, t);
+      const int blocks = (t.k + kBK - 1) / kBK;
+      for (int kb = 0; kb < blocks; ++kb) {
+        if (!mbar_wait(b.empty(s), phase ^ 1u, b.abort)) return false;
+        if (b.rank == 0) mbar_arrive_expect_tx(b.full(s), bytes);
+        const uint32_t a = b.sbase + Smem::stage + s * kStageBytes;
+        P::load(p, t, b.rank, kb, a, a + kOperandBytes, full0 + (uint32_t)(s * 8));
+        issued_mask |= 1u << s;
+        issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
         }
       }
-      if (ok) {  // every stage this CTA filled has been read by the pair's MMAs before it exits
-        for (int b = 0; b < kStages; ++b)
-          if ((issued_mask >> b) & 1u && !mbar_wait(bar_empty(b), (issued_parity >> b) & 1u, s_abort)) ok = false;
-      }
-      if (!ok) {
-        flag_error(p.err, MOE_DEVERR_TIMEOUT);
-        *s_abort = 1;
-        const uint64_t t0 = global_timer_ns();  // copies in flight complete on the leader's barrier: let them land
-        while (global_timer_ns() - t0 < kDrainTimeoutNs) {
-        }
-      }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------ MMA (leader)
-    // The whole warp keeps the loop, so that its values are uniform, and one lane issues: with a lane that
-    // does it all, an MMA took 128 cycles to issue whatever its n, which left no slack for a late stage.
-    if (leader) {
-      const uint32_t fmt = P::kF16 ? 0u : 1u;
-      const uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((P::kAMN ? 1u : 0u) << 15) |
-                            ((P::kBMN ? 1u : 0u) << 16) | ((uint32_t)(kTileM >> 4) << 24);
-      const uint64_t a0 = operand_desc<P::kAMN>(sbase + Smem::stage);
-      const uint64_t b0 = operand_desc<P::kBMN>(sbase + Smem::stage + kOperandBytes);
-      int s = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true, issued_any = false;
-      while (ok && walk.next(&t)) {
-        const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_tempty(acc), acc_phase ^ 1u, s_abort));
-        if (!ok) break;
+    return true;
+  }
+  // Every stage this CTA filled has been read by the pair's MMAs before it exits.
+  __device__ __forceinline__ void finish(bool ok) {
+    for (int i = 0; i < kStages && ok; ++i)
+      if ((issued_mask >> i) & 1u && !mbar_wait(b.empty(i), (issued_parity >> i) & 1u, b.abort)) ok = false;
+    if (ok) return;
+    b.fail();
+    const uint64_t t0 = global_timer_ns();  // copies in flight complete on the leader's barrier: let them land
+    while (global_timer_ns() - t0 < kDrainTimeoutNs) {
+    }
+  }
+};
+
+// The leader's MMA issuer, a whole warp: it keeps the loop, so that its values are uniform, and one lane
+// issues.  (With a lane that does it all, an MMA took 128 cycles to issue whatever its n, which left no
+// slack for a late stage.)
+struct Issuer {
+  const Block& b;
+  int s = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  bool issued_any = false;
+  __device__ __forceinline__ explicit Issuer(const Block& b_) : b(b_) {}
+
+  template <class P>
+  __device__ __forceinline__ bool run(Walk<P> walk) {
+    const uint32_t fmt = P::kF16 ? 0u : 1u;
+    const uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((P::kAMN ? 1u : 0u) << 15) |
+                          ((P::kBMN ? 1u : 0u) << 16) | ((uint32_t)(kTileM >> 4) << 24);
+    const uint64_t a0 = operand_desc<P::kAMN>(b.sbase + Smem::stage);
+    const uint64_t b0 = operand_desc<P::kBMN>(b.sbase + Smem::stage + kOperandBytes);
+    typename P::Tile t;
+    while (walk.next(&t)) {
+      const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(b.tempty(acc), acc_phase ^ 1u, b.abort))) return false;
+      tc_fence_after();
+      const uint32_t d = b.tmem + (uint32_t)(acc * kMaxN);
+      for (int k = 0; k < t.k; k += kBK) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(b.full(s), phase, b.abort))) return false;
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * kMaxN);
-        for (int k = 0; k < t.k; k += kBK) {
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_full(s), phase, s_abort));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = a0 + (uint64_t)(s * (kStageBytes >> 4)), b = b0 + (uint64_t)(s * (kStageBytes >> 4));
-          const int steps = (t.k - k + 15) / 16;
-          if (elect_one()) {
+        const uint64_t da = a0 + (uint64_t)(s * (kStageBytes >> 4)), db = b0 + (uint64_t)(s * (kStageBytes >> 4));
+        const int steps = (t.k - k + 15) / 16;
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              if (kk < steps)
-                mma_issue_pair(d, a + operand_step<P::kAMN>(kk), b + operand_step<P::kBMN>(kk), idesc, (k | kk) != 0);
-            mma_commit_pair(bar_empty(s));
-          }
-          __syncwarp();
-          issued_any = true;
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1u;
-          }
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            if (kk < steps)
+              mma_issue_pair(d, da + operand_step<P::kAMN>(kk), db + operand_step<P::kBMN>(kk), idesc, (k | kk) != 0);
+          mma_commit_pair(b.empty(s));
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit_pair(bar_tfull(acc));
         __syncwarp();
-        if (++acc == kAccBufs) {
-          acc = 0;
-          acc_phase ^= 1u;
+        issued_any = true;
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok && elect_one()) {
-        flag_error(p.err, MOE_DEVERR_TIMEOUT);
-        *s_abort = 1;
-        if (issued_any) {  // the MMAs in flight finish before tensor memory is freed
-          mma_commit_pair(bar_drain);
-          mbar_wait(bar_drain, 0, nullptr, kDrainTimeoutNs);
-        }
+      if (elect_one()) mma_commit_pair(b.tfull(acc));
+      __syncwarp();
+      if (++acc == kAccBufs) {
+        acc = 0;
+        acc_phase ^= 1u;
       }
     }
-  } else {
-    // ------------------------------------------------- epilogue (both CTAs)
-    const int sub = warp & 3;  // TMEM lane quarter this warp may access
-    const uint32_t tempty0 = map_to_rank(bar_tempty(0), 0);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    return true;
+  }
+  __device__ __forceinline__ void finish(bool ok) {
+    if (ok || !elect_one()) return;
+    b.fail();
+    if (issued_any) {  // the MMAs in flight finish before tensor memory is freed
+      mma_commit_pair(b.drain());
+      mbar_wait(b.drain(), 0, nullptr, kDrainTimeoutNs);
+    }
+  }
+};
+
+// An epilogue warp.
+struct Epilogue {
+  const Block& b;
+  uint32_t tempty0;
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  __device__ __forceinline__ explicit Epilogue(const Block& b_) : b(b_), tempty0(map_to_rank(b_.tempty(0), 0)) {}
+
+  template <class P>
+  __device__ __forceinline__ bool run(const typename P::Params& p, Walk<P> walk) {
+    const int sub = b.warp & 3;  // TMEM lane quarter this warp may access
+    typename P::Tile t;
     bool ok = true;
     while (ok && walk.next(&t)) {
-      const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kMaxN);
+      const uint32_t tbase = b.tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * kMaxN);
       P::epilogue(
-          p, t, rank, sub, (warp - 2) >> 2, lane, tbase,
+          p, t, b.rank, sub, (b.warp - 2) >> 2, b.lane, tbase,
           [&] {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_tfull(acc), acc_phase, s_abort));
-            if (!ok) {
-              if (lane == 0) flag_error(p.err, MOE_DEVERR_TIMEOUT);
-              *s_abort = 1;
-            }
+            ok = __all_sync(0xffffffffu, mbar_wait(b.tfull(acc), acc_phase, b.abort));
+            if (!ok && b.lane == 0) b.fail();
             tc_fence_after();
             return ok;
           },
           [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
+            if (b.lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(acc * 8));
           });
       if (++acc == kAccBufs) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
+    return ok;
   }
+};
 
-  // the pair meets, then frees its tensor memory together
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();
-  tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+// One product.
+template <class P>
+__global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Block b;
+  b.begin(smem_raw, p.err);
+  const Walk<P> walk(p, b.tables(), P::setup(p, b.tables()), b.pair, b.pairs);
+  b.meet();
+  if (b.warp == 0) {
+    if (b.lane == 0) {
+      Producer r(b);
+      r.finish(r.template run<P>(p, walk));
+    }
+  } else if (b.warp == 1) {
+    if (b.rank == 0) {
+      Issuer r(b);
+      r.finish(r.template run<P>(walk));
+    }
+  } else {
+    Epilogue r(b);
+    r.template run<P>(p, walk);
+  }
+  b.end();
 }
 
 // ------------------------------------------------------------------- host
@@ -459,35 +515,46 @@ inline bool make_map_3d(CUtensorMap* map, const void* base, bool f16, int64_t co
   return make_map(map, base, f16, 3, dims, strides, box);
 }
 
-// tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's previous kernel ends.
+// The launch of a pair kernel: pairs of CTAs on all SMs, or fewer where there is not work for so many.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  int pairs = 0;
+  template <class Kernel>
+  cudaError_t prepare(Kernel kern, int table_ints, int64_t most_pairs, cudaStream_t s) {
+    const int smem = Smem::tables + table_ints * 4 + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(device_sm_count() / 2 * 2);
+    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorNotSupported;
+    if (most_pairs < pairs) pairs = (int)most_pairs;
+    cfg.gridDim = dim3(2 * pairs);
+    return cudaSuccess;
+  }
+};
+
+// tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's
+// previous kernel ends.
 template <class P>
 cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int table_ints, bool pdl, cudaStream_t s) {
-  const int smem = Smem::tables + table_ints * 4 + 1024;
-  auto kern = pair_kernel<P>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (tiles < 1) return cudaSuccess;
+  Launch l;
+  cudaError_t e = l.prepare(pair_kernel<P>, table_ints, tiles * (kMaxN / 32), s);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1] = pdl_attribute();
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(device_sm_count() / 2 * 2);
-  int pairs = 0;
-  e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
-  if (e != cudaSuccess) return e;
-  if (pairs < 1) return cudaErrorNotSupported;
-  if (tiles * (kMaxN / 32) < pairs) pairs = (int)tiles * (kMaxN / 32);
-  if (pairs < 1) return cudaSuccess;
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  l.attr[1] = pdl_attribute();
+  l.cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&l.cfg, pair_kernel<P>, p);
 }
 
 }  // namespace pg
