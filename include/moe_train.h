@@ -250,7 +250,7 @@ int moe_gated_mlp_backward(const void* dout, const void* y, const uint8_t* y_exp
  * every singular value in [0, 1] below 4, and |b s^2 + c s^4| below 32 (MOE_ERR_INVALID).
  * The products' operands are fp16 (scaled by a power of two) with fp32 accumulation, X itself has 22 bits.
  * A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN in its own result only.
- * Any 1 <= N, K <= 65536 and B <= 65535 (larger: MOE_ERR_UNSUPPORTED), any element alignment.
+ * Any 1 <= N, K <= 65535 and B <= 65535 (larger: MOE_ERR_UNSUPPORTED), any element alignment.
  * B, N or K == 0 is a no-op.
  * ws: device workspace of moe_orthogonalize_workspace_size bytes, 256-byte aligned; its contents
  * on entry do not matter.  One workspace serves one call at a time.

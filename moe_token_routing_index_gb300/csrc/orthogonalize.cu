@@ -90,25 +90,28 @@ __device__ __forceinline__ void load_values(const __nv_bfloat16* p, float* v) {
 template <class T, int V, bool MOMENTUM, class Take>
 __device__ __forceinline__ void each_value(const Input& p, int b, Take take) {
   constexpr int kAtOnce = MOMENTUM ? 2 : 4;
-  const uint32_t per_row = (uint32_t)p.K / V, total = per_row * (uint32_t)p.N;
-  const uint32_t stride = gridDim.x * kNormThreads;
+  const uint32_t per_row = (uint32_t)p.K / V;
+  const int64_t total = (int64_t)per_row * p.N, stride = gridDim.x * kNormThreads;  // total is below 2^32
   const T* g = static_cast<const T*>(p.g) + b * p.batch;
   float* momentum = MOMENTUM ? p.momentum + (int64_t)b * p.N * p.K : nullptr;
-  for (uint32_t i = blockIdx.x * kNormThreads + threadIdx.x; i < total; i += kAtOnce * stride) {
+  for (int64_t i = blockIdx.x * kNormThreads + threadIdx.x; i < total; i += kAtOnce * stride) {
     float u[kAtOnce][V], m[kAtOnce][V];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      const uint32_t at = i + j * stride;
-      if (at >= i && at < total) {  // (the sum may pass 32 bits)
-        const uint32_t r = at / per_row, c = at - r * per_row;
+      const int64_t at = i + j * stride;
+      if (at < total) {
+        const uint32_t r = (uint32_t)at / per_row, c = (uint32_t)at - r * per_row;
         load_values<V>(g + r * p.row + c * V, u[j]);
-        if (MOMENTUM) load_values<V>(momentum + (int64_t)at * V, m[j]);
+        if (MOMENTUM) load_values<V>(momentum + at * V, m[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      const uint32_t at = i + j * stride;
-      if (at >= i && at < total) take(at / per_row, at % per_row * V, u[j], m[j], momentum + (int64_t)at * V);
+      const int64_t at = i + j * stride;
+      if (at < total) {
+        const uint32_t r = (uint32_t)at / per_row, c = (uint32_t)at - r * per_row;
+        take(r, c * V, u[j], m[j], momentum + at * V);
+      }
     }
   }
 }
@@ -589,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Blocks of a matrix in the passes over G: no more than 8 on an SM in all, 8 elements a thread or more.
+// Blocks of a matrix in the passes over G, 32 elements a thread or more.  They go by the matrix alone, so
+// that its norm is the same in any batch.
 int norm_blocks(const OrthoArgs& g) {
-  const int64_t most = (8 * (int64_t)kNumSmsGB300 + g.B - 1) / g.B;
-  const int64_t want = ((int64_t)g.N * g.K + 8 * kNormThreads - 1) / (8 * kNormThreads);
-  return (int)(want < most ? want : most);
+  const int64_t want = ((int64_t)g.N * g.K + 32 * kNormThreads - 1) / (32 * kNormThreads);
+  return (int)(want < 1024 ? want : 1024);
 }
 
 constexpr int kPairsGB300 = kNumSmsGB300 / 2;

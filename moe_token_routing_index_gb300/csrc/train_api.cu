@@ -64,7 +64,7 @@ int check_gated(const void* x, const void* y, const void* w13, const void* w2, c
   return MOE_OK;
 }
 
-constexpr int kMaxOrthoSide = 65536, kMaxOrthoBatch = 65535, kMaxOrthoSteps = 16;
+constexpr int kMaxOrthoSide = 65535, kMaxOrthoBatch = 65535, kMaxOrthoSteps = 16;
 constexpr float kOrthoDefaults[3] = {3.4445f, -4.7750f, 2.0315f};
 
 // Whether the iteration keeps every singular value of [0, 1] in the range of the kernels' fp16.

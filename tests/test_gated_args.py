@@ -36,14 +36,14 @@ def test_orthogonalize_refusals(mb):  # noqa: F811
     n = ctypes.c_size_t(0)
     size = mb.library().moe_orthogonalize_workspace_size
     assert size(-1, 8, 8, ctypes.byref(n)) == inv and size(1, 8, 8, None) == inv
-    assert size(1, 65537, 8, ctypes.byref(n)) == uns and size(65536, 8, 8, ctypes.byref(n)) == uns
+    assert size(1, 65536, 8, ctypes.byref(n)) == uns and size(65536, 8, 8, ctypes.byref(n)) == uns
     assert size(0, 8, 8, ctypes.byref(n)) == ok and n.value == 0
     assert size(2, 40, 56, ctypes.byref(n)) == ok and n.value > 0
     need = n.value
     c3 = lambda *v: (ctypes.c_float * 3)(*v)
     shared = [(dict(B=-1), inv), (dict(N=-1), inv), (dict(steps=0), inv), (dict(steps=17), inv), (dict(eps=0.0), inv),
               (dict(eps=NAN), inv), (dict(eps=INF), inv), (dict(ws=None), inv), (dict(nws=need - 1), mb.MOE_ERR_WORKSPACE),
-              (dict(ws=ctypes.c_void_p(0x1010)), inv), (dict(K=65537), uns), (dict(coef=c3(NAN, 0, 0)), inv),
+              (dict(ws=ctypes.c_void_p(0x1010)), inv), (dict(K=65536), uns), (dict(coef=c3(NAN, 0, 0)), inv),
               (dict(coef=c3(5.0, 0.0, 0.0)), inv),              # leaves [0, 4)
               (dict(coef=c3(1.9, 0.0, 0.0), steps=3), inv)]   # grows step by step
     one = dict(g=FAKE, dtype=0, bs=40 * 56, rs=56, B=2, N=40, K=56, steps=5, coef=None, eps=1e-7, scale=1.0, out=FAKE,

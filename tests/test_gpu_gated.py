@@ -235,3 +235,44 @@ def test_many_experts_with_few_rows():
     _within(dx, wx, ex, a - 3, "dx")
     _within(dy, wdy, edy, a - 3, "dy")
     assert mb.device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    """Rows whose y lies beyond 2^31 elements, forward and backward, against the same rows by themselves."""
+    mb = _mb()
+    E, D, H, a = 2, 16, 4096, 300_000
+    x, w13, w2, dout = _make(64, E, D, H, seed=10)
+    x, dout = x.cuda().repeat(a // 64 + 1, 1)[:a].contiguous(), dout.cuda().repeat(a // 64 + 1, 1)[:a].contiguous()
+    w13, w2 = w13.cuda(), w2.cuda()
+    counts = _counts([100, a - 130])                # the last 30 rows are of no expert
+    out, y = _filled(a, D), _filled(a, 2 * H)
+    mb.moe_gated_mlp(x, w13, w2, counts, y=y, out=out)
+    n = a - 30
+    assert y.numel() > 2 ** 31
+    tail = slice(n - 64, n)
+    few = _counts([0, 64])
+    want, wy = mb.moe_gated_mlp(x[tail].contiguous(), w13, w2, few)
+    assert torch.equal(out[tail], want) and torch.equal(y[tail], wy)
+    assert bool((y[n:] == 7).all()) and bool((out[n:] == 7).all())
+    dx, dy, z = mb.moe_gated_mlp_backward(dout, y, w13, w2, counts, dy=_filled(a, 2 * H))
+    wx, wdy, wz = mb.moe_gated_mlp_backward(dout[tail].contiguous(), wy, w13, w2, few)
+    assert torch.equal(dx[tail], wx) and torch.equal(dy[tail], wdy) and torch.equal(z[tail], wz)
+    assert bool((dy[n:] == 7).all())
+    assert mb.device_error() == 0
+
+
+def test_two_streams_at_once():
+    mb = _mb()
+    x, w13, w2, dout = (t.cuda() for t in _make(900, 4, 256, 320, seed=11))
+    counts = [_counts([500, 0, 130, 270]), _counts([1, 600, 299, 0])]
+    want = [mb.moe_gated_mlp(x, w13, w2, c) for c in counts]
+    grads = [mb.moe_gated_mlp_backward(dout, y, w13, w2, c) for c, (_, y) in zip(counts, want)]
+    streams = [torch.cuda.Stream() for _ in counts]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [mb.moe_gated_mlp(x, w13, w2, c, stream=s) for c, s in zip(counts, streams)]
+        back = [mb.moe_gated_mlp_backward(dout, y, w13, w2, c, stream=s) for c, s, (_, y) in zip(counts, streams, got)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for p, q in zip(want, got) for u, v in zip(p, q))
+    assert all(torch.equal(u, v) for p, q in zip(grads, back) for u, v in zip(p, q))
+    assert mb.device_error() == 0

@@ -188,3 +188,43 @@ def test_same_bytes_again_captured_and_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(wk, w) and not torch.equal(mk, m)      # a rate of zero: the momentum moves alone
     assert mb.device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    """Matrices beyond 2^31 elements of a batch give the bytes that they give by themselves."""
+    mb = _mb()
+    B, N, K = 40, 8192, 8192
+    g = torch.zeros(B, N, K, dtype=BF16, device="cuda")
+    g[-1] = torch.randn(N, K, device="cuda").to(BF16)
+    g[5] = g[-1]
+    assert g.numel() > 2 ** 31
+    out = mb.moe_orthogonalize(g, steps=1)
+    alone = mb.moe_orthogonalize(g[-1], steps=1)
+    assert torch.equal(out[-1], alone) and torch.equal(out[5], alone)
+    assert not bool(out[-2].any()) and not bool(out[0].any())
+    assert mb.device_error() == 0
+
+
+def test_two_streams_at_once():
+    mb = _mb()
+    gs = [_g(3, 200, 330, BF16, seed=12).cuda(), _g(2, 700, 96, F32, seed=13).cuda(), _g(1, 64, 4096, F32, seed=14).cuda()]
+    want = [mb.moe_orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [mb.moe_orthogonalize(g, stream=s) for g, s in zip(gs, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, got))
+    assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("N,K", [(1, 20000), (20000, 1), (40, 30000), (16, 4000), (300, 9001)])
+def test_long_and_flat(N, K):
+    """Few tiles and a long reduction: A from parts of it."""
+    mb = _mb()
+    g = _g(1, N, K, F32, seed=15)
+    got = mb.moe_orthogonalize(g.cuda(), steps=1).cpu().double()
+    want, bound = ref.one_step_error(g)
+    assert float(((got - want).abs() - bound).max()) <= 0
+    _check_five(mb.moe_orthogonalize(g.cuda()), g)
+    assert mb.device_error() == 0
