@@ -187,7 +187,9 @@ struct MatTile {
   bool mirror;         // symmetric results: stored across the diagonal too
 };
 
-enum Product { kGram, kPartial, kReduce, kPolynomial, kNext, kOut, kWeights };
+// How a product ends: A, a part of A, alpha * src + beta * product (symmetric), the same with two sources
+// (src and lo), X's next iterate, and what the call asked for.
+enum Product { kGram, kPartial, kOneSource, kTwoSources, kNext, kOut, kWeights };
 
 struct Dims {
   int count, rows, cols;  // of the result
@@ -210,10 +212,10 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
 }
 
 struct Result {
-  __half* sym;          // A or P, rows ldm elements apart
-  const __half* src;    // P: A.  X: its first half
+  __half* sym;          // symmetric results, rows ldm elements apart
+  const __half* src;    // X: its first half
   __half* next;         // X's next first half
-  __half* lo;           // X's second half, in place
+  __half* lo;           // X's second half, in place; the second source
   float* partial;       // A's parts: [splits][count][rows] of ld
   void* out;            // bf16 result, or weights
   int ld;               // of sym and src's matrices; X: of src, next and lo
@@ -227,8 +229,9 @@ struct Result {
 template <bool AMN, bool BMN, Product KIND>
 struct Ns {
   static constexpr bool kAMN = AMN, kBMN = BMN, kF16 = true;
-  static constexpr bool kSym = KIND == kGram || KIND == kPolynomial;
+  static constexpr bool kSym = KIND == kGram || KIND == kOneSource || KIND == kTwoSources;
   static constexpr bool kX = KIND == kNext || KIND == kOut || KIND == kWeights;
+  static constexpr bool kSrc = kX || KIND == kOneSource || KIND == kTwoSources, kLo = kX || KIND == kTwoSources;
   struct Params {
     const CUtensorMap *a, *b;  // b: by box height where it is K-major
     Dims d;
@@ -280,8 +283,8 @@ struct Ns {
     load_half<BMN>(b, p.b + (BMN ? 0 : t.n / 32 - 1), bar, k, t.col + rank * (t.n / 2), t.at);
   }
   static constexpr int kWords = kChunk / 2;
-  struct Source {  // a chunk of a row: of X's halves, or of A; of the weights
-    uint32_t hi[kX || KIND == kPolynomial ? kWords : 1], lo[kX ? kWords : 1];
+  struct Source {  // a chunk of a row of the sources, and of the weights
+    uint32_t hi[kSrc ? kWords : 1], lo[kLo ? kWords : 1];
     uint32_t w[KIND == kWeights ? kChunk : 1];
   };
   static __device__ __forceinline__ float2 halves(uint32_t w) {
@@ -308,8 +311,8 @@ struct Ns {
     const float w_keep = 1.0f - lr * g.keep, w_scale = lr * g.scale;
     const bool f32 = KIND == kWeights && g.w_dtype == MOE_DTYPE_F32;
     auto load = [&](int c, Source& s) {
-      if constexpr (kX || KIND == kPolynomial) load32(g.src + at + c, s.hi);
-      if constexpr (kX) load32(g.lo + at + c, s.lo);
+      if constexpr (kSrc) load32(g.src + at + c, s.hi);
+      if constexpr (kLo) load32(g.lo + at + c, s.lo);
       if constexpr (KIND == kWeights) {
         if (g.whole) {
           if (f32) {
@@ -338,11 +341,11 @@ struct Ns {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         float2 x = make_float2(v[2 * i] * g.beta, v[2 * i + 1] * g.beta);
-        if constexpr (kX || KIND == kPolynomial) {
+        if constexpr (kSrc) {
           const float2 h = halves(s.hi[i]);
           x = make_float2(fmaf(g.alpha, h.x, x.x), fmaf(g.alpha, h.y, x.y));
         }
-        if constexpr (kX) {
+        if constexpr (kLo) {
           const float2 l = halves(s.lo[i]);
           x = make_float2(fmaf(g.alpha, l.x, x.x), fmaf(g.alpha, l.y, x.y));
         }
@@ -422,15 +425,24 @@ struct Ns {
 // All products of a call in one launch, with a barrier over the grid between them: of small matrices a
 // product's launch, prologue and first loads took 8 us each.  The epilogue's warps arrive when a CTA's
 // results are stored; they and the producer wait.
+//
+// The first two steps may be made one (twice): with M = aI + P, the next A is M A M, so it follows from
+// products of m x m matrices, and X takes both steps at once:
+//   T = a A + A P,  A' = a T + P T,  P' = b A' + c A' A',  W = a P + a P' + P' P,  X = a^2 X + W X
+// which saves a pass over X for A and one product of 2 m m n for three of m m m (symmetric: half each).
+// The roundings cost what they cost in two steps, because A is far from I there; made one later, or
+// four made two, they do not (Gaussian 512 x 2048: 1.7e-3 of the norm as it is and with the first two,
+// 4.1e-3 with the last two, 2.6e-3 with the first four).
+enum Op { oGram, oPartial, oReduce, oPoly, oTimes, oNextGram, oNextPoly, oBoth, oX };
+
 struct Plan {
   CUtensorMap x_rows[2], x_cols[2];        // X as A: boxes of 128 rows, or of kBK rows x 64 columns
   CUtensorMap x_low[2][kHeights];          // X as a K-major B
-  CUtensorMap gram, gram_low[kHeights];
-  CUtensorMap poly, poly_low[kHeights];
-  Dims sym, sym_poly, square;              // A, P, X
-  __half *x[2], *lo, *a, *p;
+  CUtensorMap q[3], q_low[3][kHeights];    // the square matrices as A and as B
+  Dims sym, sym_square, square;            // A, the products of square matrices, X
+  __half *x[2], *lo, *m[3];                // m: A (then A', W), P, and T (then P')
   float* partial;
-  int steps, m, ldx, ldm;
+  int steps, twice, side, ldx, ldm;
   float coef[3];
   Result last;                             // out and what goes with it
   unsigned int* arrived;
@@ -454,7 +466,7 @@ __device__ __forceinline__ bool wait_grid(const Block& b, const unsigned int* ar
 
 // A from its parts, added in order: 8 elements a thread.
 __device__ __forceinline__ void reduce_parts(const Plan& p, int thread) {
-  const int64_t size = (int64_t)p.sym.count * p.m * p.ldm;
+  const int64_t size = (int64_t)p.sym.count * p.side * p.ldm;
   for (int64_t i = ((int64_t)blockIdx.x * kEpiThreads + thread) * 8; i < size; i += (int64_t)gridDim.x * kEpiThreads * 8) {
     float v[8] = {};
 #pragma unroll 4
@@ -470,19 +482,25 @@ __device__ __forceinline__ void reduce_parts(const Plan& p, int thread) {
       const __half2 x = __floats2half2_rn(v[2 * j] * kUnscale, v[2 * j + 1] * kUnscale);
       h[j] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    *reinterpret_cast<uint4*>(p.a + i) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p.m[0] + i) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
-// Calls role(policy, its parameters) for product `kind` of a step.
+// One of the call's products: what it is, which iterate of X it reads, and whether X takes two steps or ends.
+struct Turn {
+  Op op;
+  int cur;
+  bool both, last;
+};
+
+// Calls role(policy, its parameters) for a turn.
 template <bool TALL, Product LAST, class Role>
-__device__ __forceinline__ bool product(const Plan& p, Product kind, int step, Role role) {
-  const int cur = step & 1;
+__device__ __forceinline__ bool product(const Plan& p, const Turn& turn, Role role) {
+  const int cur = turn.cur;
+  const float a0 = p.coef[0];
   Result r = p.last;
-  r.src = p.x[cur];
-  r.lo = p.lo;
-  if (kind == kGram || kind == kPartial) {
-    r.sym = p.a;
+  if (turn.op == oGram || turn.op == oPartial) {
+    r.sym = p.m[0];
     r.partial = p.partial;
     r.ld = p.ldm;
     r.beta = kUnscale;
@@ -490,28 +508,45 @@ __device__ __forceinline__ bool product(const Plan& p, Product kind, int step, R
     const CUtensorMap* b = TALL ? &p.x_cols[cur] : p.x_low[cur];
     using G = Ns<TALL, TALL, kGram>;
     using S = Ns<TALL, TALL, kPartial>;
-    if (kind == kGram) return role(G(), typename G::Params{a, b, p.sym, r});
+    if (turn.op == oGram) return role(G(), typename G::Params{a, b, p.sym, r});
     return role(S(), typename S::Params{a, b, p.sym, r});
   }
-  if (kind == kPolynomial) {
-    using P = Ns<false, false, kPolynomial>;
-    r.sym = p.p;
-    r.src = p.a;
+  if (turn.op == oBoth) {
+    using W = Ns<false, false, kTwoSources>;
+    r.sym = p.m[0];
+    r.src = p.m[1];
+    r.lo = p.m[2];
     r.ld = p.ldm;
-    r.alpha = p.coef[1];
-    r.beta = p.coef[2] * kUnscale;
-    return role(P(), typename P::Params{&p.gram, p.gram_low, p.sym_poly, r});
+    r.alpha = a0;
+    r.beta = kUnscale;
+    return role(W(), typename W::Params{&p.q[2], p.q_low[1], p.sym_square, r});
+  }
+  if (turn.op != oX) {
+    using P = Ns<false, false, kOneSource>;
+    const bool poly = turn.op == oPoly || turn.op == oNextPoly;
+    const int to = turn.op == oPoly ? 1 : turn.op == oNextGram ? 0 : 2;
+    const int src = turn.op == oNextGram ? 2 : 0, a = turn.op == oNextGram ? 1 : 0;
+    const int b = turn.op == oTimes ? 1 : turn.op == oNextGram ? 2 : 0;
+    r.sym = p.m[to];
+    r.src = p.m[src];
+    r.ld = p.ldm;
+    r.alpha = poly ? p.coef[1] : a0;
+    r.beta = poly ? p.coef[2] * kUnscale : kUnscale;
+    return role(P(), typename P::Params{&p.q[a], p.q_low[b], p.sym_square, r});
   }
   // X [N, K]: P X (wide: P's rows, X's columns) or X P (tall: X's rows, P's rows, as P is symmetric)
+  r.src = p.x[cur];
   r.next = p.x[cur ^ 1];
+  r.lo = p.lo;
   r.ld = p.ldx;
-  r.alpha = p.coef[0];
+  r.alpha = turn.both ? a0 * a0 : a0;
   r.beta = kUnscale;
-  const CUtensorMap* a = TALL ? &p.x_rows[cur] : &p.poly;
-  const CUtensorMap* b = TALL ? p.poly_low : &p.x_cols[cur];
+  const int by = turn.both ? 0 : 1;
+  const CUtensorMap* a = TALL ? &p.x_rows[cur] : &p.q[by];
+  const CUtensorMap* b = TALL ? p.q_low[by] : &p.x_cols[cur];
   using N = Ns<false, !TALL, kNext>;
   using L = Ns<false, !TALL, LAST>;
-  if (kind == kNext) return role(N(), typename N::Params{a, b, p.square, r});
+  if (!turn.last) return role(N(), typename N::Params{a, b, p.square, r});
   return role(L(), typename L::Params{a, b, p.square, r});
 }
 
@@ -525,12 +560,26 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
   auto all = [&](auto run) {
     unsigned int before = 0;
     bool ok = true;
-    for (int step = 0; step < p.steps && ok; ++step) {
-      const bool split = p.sym.splits > 1;
-      ok = run(split ? kPartial : kGram, step, before++);
-      if (ok && split) ok = run(kReduce, step, before++);
-      if (ok) ok = run(kPolynomial, step, before++);
-      if (ok) ok = run(step + 1 < p.steps ? kNext : LAST, step, before++);
+    for (int step = 0, cur = 0; step < p.steps && ok; cur ^= 1) {
+      const bool both = step == 0 && p.twice;
+      step += both ? 2 : 1;
+      auto turn = [&](Op op) {
+        if (ok) ok = run(Turn{op, cur, both, op == oX && step >= p.steps}, before++);
+      };
+      if (p.sym.splits > 1) {
+        turn(oPartial);
+        turn(oReduce);
+      } else {
+        turn(oGram);
+      }
+      turn(oPoly);
+      if (both) {
+        turn(oTimes);
+        turn(oNextGram);
+        turn(oNextPoly);
+        turn(oBoth);
+      }
+      turn(oX);
     }
     return ok;
   };
@@ -541,11 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
   if (b.warp == 0) {
     if (b.lane == 0) {
       Producer r(b);
-      r.finish(all([&](Product kind, int step, unsigned int before) {
-        if (kind == kReduce) return true;
+      r.finish(all([&](const Turn& turn, unsigned int before) {
+        if (turn.op == oReduce) return true;
         if (!wait_grid(b, p.arrived, before * gridDim.x)) return false;
         asm volatile("fence.proxy.async.global;" ::: "memory");  // the loads see what other CTAs stored
-        return product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+        return product<TALL, LAST>(p, turn, [&](auto policy, const auto& params) {
           return r.template run<decltype(policy)>(params, walk(params, policy));
         });
       }));
@@ -553,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
   } else if (b.warp == 1) {
     if (b.rank == 0) {
       Issuer r(b);
-      r.finish(all([&](Product kind, int step, unsigned int) {
-        if (kind == kReduce) return true;
-        return product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+      r.finish(all([&](const Turn& turn, unsigned int) {
+        if (turn.op == oReduce) return true;
+        return product<TALL, LAST>(p, turn, [&](auto policy, const auto& params) {
           return r.template run<decltype(policy)>(walk(params, policy));
         });
       }));
@@ -564,15 +613,15 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
     Epilogue r(b);
     const int thread = threadIdx.x - 64;
     int* s_ok = b.tables();
-    all([&](Product kind, int step, unsigned int before) {
-      if (kind == kReduce) {
+    all([&](const Turn& turn, unsigned int before) {
+      if (turn.op == oReduce) {
         reduce_parts(p, thread);
       } else {  // (a warp that gives up raises the abort flag, and stays for the barriers)
-        product<TALL, LAST>(p, kind, step, [&](auto policy, const auto& params) {
+        product<TALL, LAST>(p, turn, [&](auto policy, const auto& params) {
           return r.template run<decltype(policy)>(params, walk(params, policy));
         });
       }
-      if (kind == LAST) return true;
+      if (turn.last) return true;
       // this CTA's results are stored; then those of all
       epilogue_sync();
       if (thread == 0) {  // (the release covers what the other warps stored before the barrier)
@@ -604,9 +653,14 @@ constexpr int kPairsGB300 = kNumSmsGB300 / 2;
 // kBK, has to be worth a barrier and a pass over the parts (about 4 us).
 constexpr int kWorthSplitting = 24;
 
+// The first two steps are made one where that saves 3 B m m (n - m) operations or more: the turn that it adds
+// takes about 5 us, 7e9 operations.
+constexpr double kWorthTwice = 5e9;
+
 struct Layout {
   int m, ldx, ldm, splits;
-  size_t arrived, part, x0, x1, lo, gram, poly, partial, total;  // offsets
+  bool twice;
+  size_t arrived, part, x0, x1, lo, m0, m1, m2, partial, total;  // offsets
 };
 
 Layout layout(const OrthoArgs& g) {
@@ -624,9 +678,12 @@ Layout layout(const OrthoArgs& g) {
   l.x0 = l.part + up((int64_t)g.B * norm_blocks(g) * (int64_t)sizeof(float2), 256);
   l.x1 = l.x0 + x;
   l.lo = l.x1 + x;
-  l.gram = l.lo + x;
-  l.poly = l.gram + sym;
-  l.partial = l.poly + sym;
+  // (the same for any number of steps and coefficients: it goes into the workspace's size)
+  l.twice = l.splits == 1 && (double)g.B * l.m * l.m * ((double)(g.N < g.K ? g.K : g.N) - l.m) >= kWorthTwice;
+  l.m0 = l.lo + x;
+  l.m1 = l.m0 + sym;
+  l.m2 = l.m1 + sym;
+  l.partial = l.m2 + (l.twice ? sym : 0);
   l.total = l.partial + (l.splits > 1 ? 2 * sym * l.splits : 0);
   return l;
 }
@@ -653,28 +710,30 @@ template <bool TALL, Product LAST>
 cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s) {
   Plan p{};
   const int n = TALL ? g.N : g.K;
-  if (!make_dims(&p.sym, g.B, l.m, l.m, n, true, l.splits) || !make_dims(&p.sym_poly, g.B, l.m, l.m, l.m, true, 1) ||
+  if (!make_dims(&p.sym, g.B, l.m, l.m, n, true, l.splits) || !make_dims(&p.sym_square, g.B, l.m, l.m, l.m, true, 1) ||
       !make_dims(&p.square, g.B, g.N, g.K, l.m, false, 1))
     return cudaErrorNotSupported;
   p.x[0] = reinterpret_cast<__half*>(ws + l.x0);
   p.x[1] = reinterpret_cast<__half*>(ws + l.x1);
   p.lo = reinterpret_cast<__half*>(ws + l.lo);
-  p.a = reinterpret_cast<__half*>(ws + l.gram);
-  p.p = reinterpret_cast<__half*>(ws + l.poly);
+  p.m[0] = reinterpret_cast<__half*>(ws + l.m0);
+  p.m[1] = reinterpret_cast<__half*>(ws + l.m1);
+  p.m[2] = reinterpret_cast<__half*>(ws + l.m2);
   p.partial = reinterpret_cast<float*>(ws + l.partial);
+  p.twice = l.twice && g.steps >= 2 && g.twice_fits;
   auto map = [&](CUtensorMap* to, const void* x, bool of_x, int box) {
     return of_x ? make_map_3d(to, x, true, g.B, g.N, g.K, l.ldx, box) : make_map_3d(to, x, true, g.B, l.m, l.m, l.ldm, box);
   };
-  bool ok = map(&p.gram, p.a, false, kHalfM) && map(&p.poly, p.p, false, kHalfM);
+  bool ok = true;
   for (int i = 0; i < 2 && ok; ++i) ok = map(&p.x_rows[i], p.x[i], true, kHalfM) && map(&p.x_cols[i], p.x[i], true, kBK);
+  for (int i = 0; i < (p.twice ? 3 : 2) && ok; ++i) ok = map(&p.q[i], p.m[i], false, kHalfM);
   for (int h = 0; h < kHeights && ok; ++h) {
-    ok = map(&p.gram_low[h], p.a, false, box_rows(h));
-    if (ok && TALL) ok = map(&p.poly_low[h], p.p, false, box_rows(h));
+    for (int i = 0; i < (p.twice ? 3 : 2) && ok; ++i) ok = map(&p.q_low[i][h], p.m[i], false, box_rows(h));
     for (int i = 0; i < 2 && ok && !TALL; ++i) ok = map(&p.x_low[i][h], p.x[i], true, box_rows(h));
   }
   if (!ok) return cudaErrorInvalidValue;
   p.steps = g.steps;
-  p.m = l.m;
+  p.side = l.m;
   p.ldx = l.ldx;
   p.ldm = l.ldm;
   for (int i = 0; i < 3; ++i) p.coef[i] = g.coef[i];

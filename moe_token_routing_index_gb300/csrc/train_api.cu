@@ -67,16 +67,20 @@ int check_gated(const void* x, const void* y, const void* w13, const void* w2, c
 constexpr int kMaxOrthoSide = 65535, kMaxOrthoBatch = 65535, kMaxOrthoSteps = 16;
 constexpr float kOrthoDefaults[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// Whether the iteration keeps every singular value of [0, 1] in the range of the kernels' fp16.
-bool coefficients_fit(const float* c, int steps) {
+// Whether the iteration keeps every singular value of [0, 1] in the range of the kernels' fp16.  *twice:
+// whether the polynomial of its first two steps, but for its linear term, does as well.
+bool coefficients_fit(const float* c, int steps, bool* twice) {
   for (int i = 0; i < 3; ++i)
     if (!isfinite(c[i])) return false;
+  *twice = true;
   for (int i = 0; i <= 1024; ++i) {
-    double s = i / 1024.0;
+    double s = i / 1024.0, m = 1.0;
     for (int k = 0; k < steps; ++k) {
       const double p = (c[1] + c[2] * s * s) * s * s;
+      if (k < 2) m *= c[0] + p;
       s = fabs((c[0] + p) * s);
       if (!(fabs(p) < 32.0) || !(s < 4.0)) return false;
+      if (k == 1 && !(fabs(m - c[0] * c[0]) < 32.0)) *twice = false;
     }
   }
   return true;
@@ -90,7 +94,7 @@ int check_ortho(moe::OrthoArgs* g, int steps, const float* coefficients, float e
   if (!float_dtype(g->dtype) || steps < 1 || steps > kMaxOrthoSteps) return MOE_ERR_INVALID;
   if (!(eps >= 1e-12f) || !isfinite(eps)) return MOE_ERR_INVALID;
   for (int i = 0; i < 3; ++i) g->coef[i] = coefficients ? coefficients[i] : kOrthoDefaults[i];
-  if (!coefficients_fit(g->coef, steps)) return MOE_ERR_INVALID;
+  if (!coefficients_fit(g->coef, steps, &g->twice_fits)) return MOE_ERR_INVALID;
   g->steps = steps;
   g->eps = eps;
   if (need == 0) return MOE_OK;

@@ -228,3 +228,17 @@ def test_long_and_flat(N, K):
     assert float(((got - want).abs() - bound).max()) <= 0
     _check_five(mb.moe_orthogonalize(g.cuda()), g)
     assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("B,N,K", [(1, 1100, 6144), (2, 6100, 800), (3, 512, 7175)])
+def test_two_steps_made_one(B, N, K):
+    """Sizes at which the first two steps are one polynomial: the same iteration, at the same bounds.  What that
+    polynomial's own roundings add to those of two steps is within the 1.5 of the bound (they are as large)."""
+    mb = _mb()
+    for strong in (True, False):
+        g = _g(B, N, K, F32, seed=16, strong=strong)
+        got = mb.moe_orthogonalize(g.cuda())
+        _check_five(got, g)
+        _check_five(mb.moe_orthogonalize(g.cuda(), steps=2), g, steps=2)
+        _check_five(mb.moe_orthogonalize(g.cuda(), steps=3), g, steps=3)
+    assert mb.device_error() == 0
