@@ -378,7 +378,7 @@ cudaError_t launch(const typename P::Params& p, bool pdl, cudaStream_t s) {
   const Rows& r = p.rows;
   const int64_t tiles = ((int64_t)r.a_max / kMaxN + r.E) * r.mt;  // at most
   if (tiles > INT32_MAX / 2) return cudaErrorNotSupported;
-  return launch_pairs<P>(p, tiles, 2 * (r.E + 1), pdl, s);
+  return launch_pairs<P>(p, tiles, r.k, 2 * (r.E + 1) * (int)sizeof(int), pdl, s);
 }
 
 template <bool WMN>

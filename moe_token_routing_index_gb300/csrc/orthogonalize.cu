@@ -199,7 +199,9 @@ struct Dims {
   int splits, part_k;     // kPartial: parts of the reduction, and the length of one
 };
 
-// 32 bytes of a lane.
+// 32 bytes of a lane.  (Next iterates through boxes in shared memory and TMA instead, which a third of the
+// L1 cache's passes would go without: 3% on 8 matrices of 7168 x 2048, 1% on 16 of 2048 x 7168, and 1% more
+// time on 2 of 5120 x 8192, whose long reductions miss the stage that made room.)
 __device__ __forceinline__ void load32(const void* p, uint32_t* r) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -226,12 +228,15 @@ struct Result {
   bool whole;           // out's chunks are whole and 32-byte aligned
 };
 
+constexpr bool symmetric(Product k) { return k == kGram || k == kOneSource || k == kTwoSources; }
+constexpr bool moves_x(Product k) { return k == kNext || k == kOut || k == kWeights; }
+constexpr bool has_source(Product k) { return moves_x(k) || k == kOneSource || k == kTwoSources; }
+constexpr bool has_second(Product k) { return moves_x(k) || k == kTwoSources; }
+constexpr int kWords = kChunk / 2;
+
 template <bool AMN, bool BMN, Product KIND>
 struct Ns {
   static constexpr bool kAMN = AMN, kBMN = BMN, kF16 = true;
-  static constexpr bool kSym = KIND == kGram || KIND == kOneSource || KIND == kTwoSources;
-  static constexpr bool kX = KIND == kNext || KIND == kOut || KIND == kWeights;
-  static constexpr bool kSrc = kX || KIND == kOneSource || KIND == kTwoSources, kLo = kX || KIND == kTwoSources;
   struct Params {
     const CUtensorMap *a, *b;  // b: by box height where it is K-major
     Dims d;
@@ -253,7 +258,7 @@ struct Ns {
       t.k0 = t.split * d.part_k;
       t.k = min(d.part_k, d.k - t.k0);
     }
-    if (kSym) {  // row block r has the column blocks 0 .. r
+    if (symmetric(KIND)) {  // row block r has the column blocks 0 .. r
       r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
       while (r * (r + 1) / 2 > l) --r;
       while ((r + 1) * (r + 2) / 2 <= l) ++r;
@@ -282,9 +287,8 @@ struct Ns {
     load_half<AMN>(a, p.a, bar, k, t.row + rank * kHalfM, t.at);
     load_half<BMN>(b, p.b + (BMN ? 0 : t.n / 32 - 1), bar, k, t.col + rank * (t.n / 2), t.at);
   }
-  static constexpr int kWords = kChunk / 2;
   struct Source {  // a chunk of a row of the sources, and of the weights
-    uint32_t hi[kSrc ? kWords : 1], lo[kLo ? kWords : 1];
+    uint32_t hi[has_source(KIND) ? kWords : 1], lo[has_second(KIND) ? kWords : 1];
     uint32_t w[KIND == kWeights ? kChunk : 1];
   };
   static __device__ __forceinline__ float2 halves(uint32_t w) {
@@ -311,8 +315,8 @@ struct Ns {
     const float w_keep = 1.0f - lr * g.keep, w_scale = lr * g.scale;
     const bool f32 = KIND == kWeights && g.w_dtype == MOE_DTYPE_F32;
     auto load = [&](int c, Source& s) {
-      if constexpr (kSrc) load32(g.src + at + c, s.hi);
-      if constexpr (kLo) load32(g.lo + at + c, s.lo);
+      if constexpr (has_source(KIND)) load32(g.src + at + c, s.hi);
+      if constexpr (has_second(KIND)) load32(g.lo + at + c, s.lo);
       if constexpr (KIND == kWeights) {
         if (g.whole) {
           if (f32) {
@@ -341,22 +345,22 @@ struct Ns {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         float2 x = make_float2(v[2 * i] * g.beta, v[2 * i + 1] * g.beta);
-        if constexpr (kSrc) {
+        if constexpr (has_source(KIND)) {
           const float2 h = halves(s.hi[i]);
           x = make_float2(fmaf(g.alpha, h.x, x.x), fmaf(g.alpha, h.y, x.y));
         }
-        if constexpr (kLo) {
+        if constexpr (has_second(KIND)) {
           const float2 l = halves(s.lo[i]);
           x = make_float2(fmaf(g.alpha, l.x, x.x), fmaf(g.alpha, l.y, x.y));
         }
         v[2 * i] = x.x;
         v[2 * i + 1] = x.y;
       }
-      if constexpr (kSym || KIND == kNext) {
+      if constexpr (symmetric(KIND) || KIND == kNext) {
         uint32_t hi[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) hi[i] = pack_half(v[2 * i], v[2 * i + 1]);
-        if (keep) store32((kSym ? g.sym : g.next) + at + c, hi);
+        if (keep) store32((symmetric(KIND) ? g.sym : g.next) + at + c, hi);
         if constexpr (KIND == kNext) {
           uint32_t lo[kWords];
 #pragma unroll
@@ -449,11 +453,12 @@ struct Plan {
   unsigned int* err;
 };
 
+constexpr int kStages = 6;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 // Until `target` CTAs have arrived (bounded).
-__device__ __forceinline__ bool wait_grid(const Block& b, const unsigned int* arrived, unsigned int target) {
+__device__ __forceinline__ bool wait_grid(const Block<kStages>& b, const unsigned int* arrived, unsigned int target) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     unsigned int v;
@@ -553,7 +558,7 @@ __device__ __forceinline__ bool product(const Plan& p, const Turn& turn, Role ro
 template <bool TALL, Product LAST>
 __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_constant__ Plan p) {
   extern __shared__ uint8_t smem_raw[];
-  Block b;
+  Block<kStages> b;
   b.begin(smem_raw, p.err);
   b.meet();
   // the products in order, with how many barriers lie before each
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
   };
   if (b.warp == 0) {
     if (b.lane == 0) {
-      Producer r(b);
+      Producer<kStages> r(b);
       r.finish(all([&](const Turn& turn, unsigned int before) {
         if (turn.op == oReduce) return true;
         if (!wait_grid(b, p.arrived, before * gridDim.x)) return false;
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
     }
   } else if (b.warp == 1) {
     if (b.rank == 0) {
-      Issuer r(b);
+      Issuer<kStages> r(b);
       r.finish(all([&](const Turn& turn, unsigned int) {
         if (turn.op == oReduce) return true;
         return product<TALL, LAST>(p, turn, [&](auto policy, const auto& params) {
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) iterate_kernel(const __grid_const
       }));
     }
   } else {
-    Epilogue r(b);
+    Epilogue<kStages> r(b);
     const int thread = threadIdx.x - 64;
     int* s_ok = b.tables();
     all([&](const Turn& turn, unsigned int before) {
@@ -750,7 +755,7 @@ cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t 
   most *= (int64_t)g.B * (kMaxN / 32);
   Launch launch;
   const auto kern = iterate_kernel<TALL, LAST>;
-  cudaError_t e = launch.prepare(kern, 4, most, s);
+  cudaError_t e = launch.prepare(kern, Smem<kStages>::bytes(16), most, s);
   if (e != cudaSuccess) return e;
   launch.attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all are resident
   launch.attr[1].val.cooperative = 1;

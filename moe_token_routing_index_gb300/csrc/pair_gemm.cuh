@@ -37,7 +37,6 @@ constexpr int kTileM = 256, kHalfM = 128, kMaxN = 256;
 constexpr int kBK = 64;
 constexpr int kOperandBytes = 128 * kBK * 2;             // of a CTA's half of A; room for its half of B
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 192 * 1024 / kStageBytes;
 constexpr int kAccBufs = 2;
 constexpr int kTmemCols = kAccBufs * kMaxN;
 constexpr int kEpiWarps = 8, kEpiGroups = kEpiWarps / 4;
@@ -49,12 +48,15 @@ constexpr int kHeights = 8;
 __host__ __device__ constexpr int box_rows(int h) { return 16 * (h + 1); }
 constexpr int kBoxBytes = 64 * 128;                      // of an MN-major box: 64 columns x kBK rows
 
+template <int STAGES>
 struct Smem {
   static constexpr int stage = 0;
-  static constexpr int bars = stage + kStages * kStageBytes;  // full[S], empty[S], tfull[2], tempty[2], drain
-  static constexpr int misc = bars + (2 * kStages + 2 * kAccBufs + 1) * 8;
-  static constexpr int tables = (misc + 16 + 15) / 16 * 16;   // the policy's
+  static constexpr int bars = stage + STAGES * kStageBytes;  // full[S], empty[S], tfull[2], tempty[2], drain
+  static constexpr int misc = bars + (2 * STAGES + 2 * kAccBufs + 1) * 8;
+  static constexpr int extra = (misc + 16 + 15) / 16 * 16;   // the policy's
+  static constexpr int bytes(int more) { return extra + more + 1024; }  // (the base is aligned to 1024)
 };
+constexpr int kSmemMax = 227 * 1024;
 
 // Shared-memory descriptor of an MN-major operand, 128B swizzle: 64-column blocks one box
 // apart, groups of 8 rows 1024 bytes apart.
@@ -255,20 +257,22 @@ struct Walk {
 };
 
 // What the roles of a CTA share.
+template <int STAGES>
 struct Block {
+  using S = Smem<STAGES>;
   uint8_t* smem;
   uint32_t sbase, tmem;
   int warp, lane, rank, pair, pairs;
   volatile int* abort;
   unsigned int* err;
 
-  __device__ __forceinline__ uint32_t bar(int i) const { return sbase + Smem::bars + 8 * i; }
+  __device__ __forceinline__ uint32_t bar(int i) const { return sbase + S::bars + 8 * i; }
   __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }  // the leader's: both CTAs' stages are whole
-  __device__ __forceinline__ uint32_t empty(int s) const { return bar(kStages + s); }
-  __device__ __forceinline__ uint32_t tfull(int b) const { return bar(2 * kStages + b); }
-  __device__ __forceinline__ uint32_t tempty(int b) const { return bar(2 * kStages + kAccBufs + b); }
-  __device__ __forceinline__ uint32_t drain() const { return bar(2 * kStages + 2 * kAccBufs); }
-  __device__ __forceinline__ int* tables() const { return reinterpret_cast<int*>(smem + Smem::tables); }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar(STAGES + s); }
+  __device__ __forceinline__ uint32_t tfull(int b) const { return bar(2 * STAGES + b); }
+  __device__ __forceinline__ uint32_t tempty(int b) const { return bar(2 * STAGES + kAccBufs + b); }
+  __device__ __forceinline__ uint32_t drain() const { return bar(2 * STAGES + 2 * kAccBufs); }
+  __device__ __forceinline__ int* tables() const { return reinterpret_cast<int*>(smem + S::extra); }
 
   // Barriers and tensor memory; then what the previous kernel of the stream wrote may be read.
   __device__ __forceinline__ void begin(uint8_t* raw, unsigned int* error) {
@@ -280,11 +284,11 @@ struct Block {
     rank = (int)(cluster_ctarank() & 1u);
     pair = blockIdx.x >> 1;
     pairs = gridDim.x >> 1;
-    abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
+    abort = reinterpret_cast<volatile int*>(smem + S::misc + 4);
     err = error;
     pdl_launch_dependents();
     if (warp == 0 && lane == 0) {
-      for (int s = 0; s < kStages; ++s) {
+      for (int s = 0; s < STAGES; ++s) {
         mbar_init(full(s), 1);
         mbar_init(empty(s), 1);
       }
@@ -298,7 +302,7 @@ struct Block {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + Smem::misc),
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + S::misc),
                    "r"(kTmemCols)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -311,7 +315,7 @@ struct Block {
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
-    tmem = *reinterpret_cast<const uint32_t*>(smem + Smem::misc);
+    tmem = *reinterpret_cast<const uint32_t*>(smem + S::misc);
   }
   // The pair meets, then frees its tensor memory together.
   __device__ __forceinline__ void end() {
@@ -329,12 +333,13 @@ struct Block {
 };
 
 // The TMA producer, one lane.
+template <int STAGES>
 struct Producer {
-  const Block& b;
+  const Block<STAGES>& b;
   uint32_t full0;
   int s = 0;
   uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
-  __device__ __forceinline__ explicit Producer(const Block& b_) : b(b_), full0(map_to_rank(b_.full(0), 0)) {}
+  __device__ __forceinline__ explicit Producer(const Block<STAGES>& b_) : b(b_), full0(map_to_rank(b_.full(0), 0)) {}
 
   template <class P>
   __device__ __forceinline__ bool run(const typename P::Params& p, Walk<P> walk) {
@@ -345,11 +350,11 @@ struct Producer {
       for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait(b.empty(s), phase ^ 1u, b.abort)) return false;
         if (b.rank == 0) mbar_arrive_expect_tx(b.full(s), bytes);
-        const uint32_t a = b.sbase + Smem::stage + s * kStageBytes;
+        const uint32_t a = b.sbase + s * kStageBytes;
         P::load(p, t, b.rank, kb, a, a + kOperandBytes, full0 + (uint32_t)(s * 8));
         issued_mask |= 1u << s;
         issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
-        if (++s == kStages) {
+        if (++s == STAGES) {
           s = 0;
           phase ^= 1u;
         }
@@ -359,7 +364,7 @@ struct Producer {
   }
   // Every stage this CTA filled has been read by the pair's MMAs before it exits.
   __device__ __forceinline__ void finish(bool ok) {
-    for (int i = 0; i < kStages && ok; ++i)
+    for (int i = 0; i < STAGES && ok; ++i)
       if ((issued_mask >> i) & 1u && !mbar_wait(b.empty(i), (issued_parity >> i) & 1u, b.abort)) ok = false;
     if (ok) return;
     b.fail();
@@ -372,20 +377,21 @@ struct Producer {
 // The leader's MMA issuer, a whole warp: it keeps the loop, so that its values are uniform, and one lane
 // issues.  (With a lane that does it all, an MMA took 128 cycles to issue whatever its n, which left no
 // slack for a late stage.)
+template <int STAGES>
 struct Issuer {
-  const Block& b;
+  const Block<STAGES>& b;
   int s = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   bool issued_any = false;
-  __device__ __forceinline__ explicit Issuer(const Block& b_) : b(b_) {}
+  __device__ __forceinline__ explicit Issuer(const Block<STAGES>& b_) : b(b_) {}
 
   template <class P>
   __device__ __forceinline__ bool run(Walk<P> walk) {
     const uint32_t fmt = P::kF16 ? 0u : 1u;
     const uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((P::kAMN ? 1u : 0u) << 15) |
                           ((P::kBMN ? 1u : 0u) << 16) | ((uint32_t)(kTileM >> 4) << 24);
-    const uint64_t a0 = operand_desc<P::kAMN>(b.sbase + Smem::stage);
-    const uint64_t b0 = operand_desc<P::kBMN>(b.sbase + Smem::stage + kOperandBytes);
+    const uint64_t a0 = operand_desc<P::kAMN>(b.sbase);
+    const uint64_t b0 = operand_desc<P::kBMN>(b.sbase + kOperandBytes);
     typename P::Tile t;
     while (walk.next(&t)) {
       const uint32_t idesc = base | ((uint32_t)(t.n >> 3) << 17);
@@ -406,7 +412,7 @@ struct Issuer {
         }
         __syncwarp();
         issued_any = true;
-        if (++s == kStages) {
+        if (++s == STAGES) {
           s = 0;
           phase ^= 1u;
         }
@@ -431,12 +437,13 @@ struct Issuer {
 };
 
 // An epilogue warp.
+template <int STAGES>
 struct Epilogue {
-  const Block& b;
+  const Block<STAGES>& b;
   uint32_t tempty0;
   int acc = 0;
   uint32_t acc_phase = 0;
-  __device__ __forceinline__ explicit Epilogue(const Block& b_) : b(b_), tempty0(map_to_rank(b_.tempty(0), 0)) {}
+  __device__ __forceinline__ explicit Epilogue(const Block<STAGES>& b_) : b(b_), tempty0(map_to_rank(b_.tempty(0), 0)) {}
 
   template <class P>
   __device__ __forceinline__ bool run(const typename P::Params& p, Walk<P> walk) {
@@ -468,25 +475,25 @@ struct Epilogue {
 };
 
 // One product.
-template <class P>
+template <class P, int STAGES>
 __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ typename P::Params p) {
   extern __shared__ uint8_t smem_raw[];
-  Block b;
+  Block<STAGES> b;
   b.begin(smem_raw, p.err);
   const Walk<P> walk(p, b.tables(), P::setup(p, b.tables()), b.pair, b.pairs);
   b.meet();
   if (b.warp == 0) {
     if (b.lane == 0) {
-      Producer r(b);
+      Producer<STAGES> r(b);
       r.finish(r.template run<P>(p, walk));
     }
   } else if (b.warp == 1) {
     if (b.rank == 0) {
-      Issuer r(b);
+      Issuer<STAGES> r(b);
       r.finish(r.template run<P>(walk));
     }
   } else {
-    Epilogue r(b);
+    Epilogue<STAGES> r(b);
     r.template run<P>(p, walk);
   }
   b.end();
@@ -496,23 +503,25 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
 
 // A map of 16-bit elements with boxes of 64 of them (128 bytes, 128B swizzle) along the first dimension.
 inline bool make_map(CUtensorMap* map, const void* base, bool f16, int nd, const cuuint64_t* dims,
-                     const cuuint64_t* strides, const cuuint32_t* box) {
+                     const cuuint64_t* strides, const cuuint32_t* box,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = encode_fn();
   if (!enc) return false;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [count][rows][cols], rows ld elements apart: boxes of box_rows rows of one matrix.
+// [count][rows][cols], rows ld elements apart: boxes of box_rows rows of one matrix, of 64 columns or of 32
+// (64 bytes, 64B swizzle).
 inline bool make_map_3d(CUtensorMap* map, const void* base, bool f16, int64_t count, int64_t rows, int64_t cols,
-                        int64_t ld, int box_rows) {
+                        int64_t ld, int box_rows, int box_cols = 64) {
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-  return make_map(map, base, f16, 3, dims, strides, box);
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  return make_map(map, base, f16, 3, dims, strides, box,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // The launch of a pair kernel: pairs of CTAs on all SMs, or fewer where there is not work for so many.
@@ -521,8 +530,7 @@ struct Launch {
   cudaLaunchAttribute attr[2];
   int pairs = 0;
   template <class Kernel>
-  cudaError_t prepare(Kernel kern, int table_ints, int64_t most_pairs, cudaStream_t s) {
-    const int smem = Smem::tables + table_ints * 4 + 1024;
+  cudaError_t prepare(Kernel kern, int smem, int64_t most_pairs, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(kThreads);
@@ -544,17 +552,26 @@ struct Launch {
   }
 };
 
-// tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's
-// previous kernel ends.
-template <class P>
-cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int table_ints, bool pdl, cudaStream_t s) {
-  if (tiles < 1) return cudaSuccess;
+template <class P, int STAGES>
+cudaError_t launch_stages(const typename P::Params& p, int64_t tiles, int table_bytes, bool pdl, cudaStream_t s) {
   Launch l;
-  cudaError_t e = l.prepare(pair_kernel<P>, table_ints, tiles * (kMaxN / 32), s);
+  const auto kern = pair_kernel<P, STAGES>;
+  cudaError_t e = l.prepare(kern, Smem<STAGES>::bytes(table_bytes), tiles * (kMaxN / 32), s);
   if (e != cudaSuccess) return e;
   l.attr[1] = pdl_attribute();
   l.cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&l.cfg, pair_kernel<P>, p);
+  return cudaLaunchKernelEx(&l.cfg, kern, p);
+}
+
+// tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's
+// previous kernel ends.  k: the reduction's length.  7 stages where the tables leave room for them (32768 rows
+// on 128 fine-grained experts, forward: 2401 us, 2441 with 6 stages, 2533 with 5, 2765 with 4), 6 where a tile
+// is hardly more than that (64 rows, D = 256, H = 512, forward: 14.8 us, 16.5 with 7).
+template <class P>
+cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int k, int table_bytes, bool pdl, cudaStream_t s) {
+  if (tiles < 1) return cudaSuccess;
+  return k > 8 * kBK && Smem<7>::bytes(table_bytes) <= kSmemMax ? launch_stages<P, 7>(p, tiles, table_bytes, pdl, s)
+                                                                : launch_stages<P, 6>(p, tiles, table_bytes, pdl, s);
 }
 
 }  // namespace pg

@@ -242,3 +242,17 @@ def test_two_steps_made_one(B, N, K):
         _check_five(mb.moe_orthogonalize(g.cuda(), steps=2), g, steps=2)
         _check_five(mb.moe_orthogonalize(g.cuda(), steps=3), g, steps=3)
     assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("B,N,K,times", [(3, 512, 7168, 60), (2, 6100, 800, 20), (16, 512, 256, 60), (1, 1100, 6144, 20),
+                                         (4, 1024, 2048, 30)])
+def test_same_bytes_every_time(B, N, K, times):
+    """A call's products follow one another inside one launch: what one stores has to be whole before the next
+    reads it, whatever the timing, so that repeated calls give the same bytes."""
+    mb = _mb()
+    g = torch.randn(B, N, K, generator=torch.Generator().manual_seed(17)).cuda()
+    ws = torch.empty(mb.moe_orthogonalize_workspace_size(B, N, K), dtype=torch.uint8, device="cuda")
+    want = mb.moe_orthogonalize(g, workspace=ws).clone()
+    for _ in range(times):
+        assert torch.equal(mb.moe_orthogonalize(g, workspace=ws), want)
+    assert mb.device_error() == 0
