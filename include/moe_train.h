@@ -252,8 +252,8 @@ int moe_gated_mlp_backward(const void* dout, const void* y, const uint8_t* y_exp
  * A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN in its own result only.
  * Any 1 <= N, K <= 65535 and B <= 65535 (larger: MOE_ERR_UNSUPPORTED), any element alignment.
  * B, N or K == 0 is a no-op.
- * ws: device workspace of moe_orthogonalize_workspace_size bytes, 256-byte aligned; its contents
- * on entry do not matter.  One workspace serves one call at a time.
+ * ws: device workspace of moe_orthogonalize_workspace_size bytes (0 for small matrices: ws may then be
+ * NULL), 256-byte aligned; its contents on entry do not matter.  One workspace serves one call at a time.
  */
 int moe_orthogonalize_workspace_size(int B, int N, int K, size_t* bytes);
 int moe_orthogonalize(const void* g, int dtype, int64_t batch_stride, int64_t row_stride, int B, int N, int K, int steps,

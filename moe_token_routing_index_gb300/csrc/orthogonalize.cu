@@ -795,6 +795,7 @@ cudaError_t begin(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t s)
 }  // namespace
 
 size_t orthogonalize_workspace_bytes(int B, int N, int K) {
+  if (orthogonalize_small_fits(N, K)) return 0;
   OrthoArgs g{};
   g.B = B;
   g.N = N;
@@ -803,6 +804,7 @@ size_t orthogonalize_workspace_bytes(int B, int N, int K) {
 }
 
 cudaError_t launch_orthogonalize(const OrthoArgs& g, cudaStream_t s) {
+  if (orthogonalize_small_fits(g.N, g.K)) return launch_orthogonalize_small(g, s);
   const Layout l = layout(g);
   char* ws = static_cast<char*>(g.ws);
   const auto whole = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };

@@ -137,5 +137,8 @@ struct OrthoArgs {
 
 size_t orthogonalize_workspace_bytes(int B, int N, int K);
 cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
+// Matrices that stay on the chip: no workspace.
+bool orthogonalize_small_fits(int N, int K);
+cudaError_t launch_orthogonalize_small(const OrthoArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -38,7 +38,8 @@ def test_orthogonalize_refusals(mb):  # noqa: F811
     assert size(-1, 8, 8, ctypes.byref(n)) == inv and size(1, 8, 8, None) == inv
     assert size(1, 65536, 8, ctypes.byref(n)) == uns and size(65536, 8, 8, ctypes.byref(n)) == uns
     assert size(0, 8, 8, ctypes.byref(n)) == ok and n.value == 0
-    assert size(2, 40, 56, ctypes.byref(n)) == ok and n.value > 0
+    assert size(2, 40, 56, ctypes.byref(n)) == ok and n.value == 0      # small ones need none
+    assert size(2, 400, 560, ctypes.byref(n)) == ok and n.value > 0
     need = n.value
     c3 = lambda *v: (ctypes.c_float * 3)(*v)
     shared = [(dict(B=-1), inv), (dict(N=-1), inv), (dict(steps=0), inv), (dict(steps=17), inv), (dict(eps=0.0), inv),
@@ -46,12 +47,12 @@ def test_orthogonalize_refusals(mb):  # noqa: F811
               (dict(ws=ctypes.c_void_p(0x1010)), inv), (dict(K=65536), uns), (dict(coef=c3(NAN, 0, 0)), inv),
               (dict(coef=c3(5.0, 0.0, 0.0)), inv),              # leaves [0, 4)
               (dict(coef=c3(1.9, 0.0, 0.0), steps=3), inv)]   # grows step by step
-    one = dict(g=FAKE, dtype=0, bs=40 * 56, rs=56, B=2, N=40, K=56, steps=5, coef=None, eps=1e-7, scale=1.0, out=FAKE,
+    one = dict(g=FAKE, dtype=0, bs=400 * 560, rs=560, B=2, N=400, K=560, steps=5, coef=None, eps=1e-7, scale=1.0, out=FAKE,
                ws=FAKE, nws=need, stream=None)
     _sweep(mb, mb.library().moe_orthogonalize, one, shared + [
         (dict(g=None), inv), (dict(out=None), inv), (dict(dtype=2), inv), (dict(scale=INF), inv), (dict(bs=-1), inv),
         (dict(rs=-1), inv), (dict(g=ODD), uns), (dict(out=ODD), uns), (dict(N=0, g=None), ok)])
-    two = dict(w=FAKE, wd=0, g=FAKE, gd=1, m=FAKE, B=2, N=40, K=56, mu=0.9, nesterov=1, lr=0.1, lrs=None, decay=0.0,
+    two = dict(w=FAKE, wd=0, g=FAKE, gd=1, m=FAKE, B=2, N=400, K=560, mu=0.9, nesterov=1, lr=0.1, lrs=None, decay=0.0,
                steps=5, coef=None, eps=1e-7, ws=FAKE, nws=need, stream=None)
     _sweep(mb, mb.library().moe_muon_update, two, shared + [
         (dict(w=None), inv), (dict(g=None), inv), (dict(m=None), inv), (dict(wd=2), inv), (dict(gd=2), inv),
@@ -63,10 +64,11 @@ def test_orthogonalize_refusals(mb):  # noqa: F811
 def _calls(mb):  # noqa: F811
     E, D, H, a = 4, 64, 32, 16
     x, w13, w2, counts = _t(BF16, a, D), _t(BF16, E, 2 * H, D), _t(BF16, E, D, H), _t(I32, E)
+    big = _t(BF16, 2, 200, 160)                 # (small matrices need no workspace)
     return dict(gated=lambda **s: mb.moe_gated_mlp(x, w13, w2, counts, **s),
                 gated_grad=lambda **s: mb.moe_gated_mlp_backward(x, _t(BF16, a, 2 * H), w13, w2, counts, **s),
                 orthogonal=lambda **s: mb.moe_orthogonalize(w13, **s),
-                update=lambda **s: mb.moe_muon_update(w13, w13, _t(F32, E, 2 * H, D), lr=0.1, **s))
+                update=lambda **s: mb.moe_muon_update(big, big, _t(F32, 2, 200, 160), lr=0.1, **s))
 
 
 @pytest.mark.parametrize("name", ["gated", "gated_grad", "orthogonal", "update"])
@@ -123,7 +125,7 @@ def test_wrappers_refuse_what_does_not_fit(mb, monkeypatch):  # noqa: F811
         lambda: mb.moe_orthogonalize(_t(torch.float16, 8, 8)),
         lambda: mb.moe_orthogonalize(torch.ones(8, 8)),
         lambda: mb.moe_orthogonalize(_t(F32, 8, 8), out=_t(F32, 8, 8)),
-        lambda: mb.moe_orthogonalize(_t(F32, 8, 8), workspace=torch.ones(1 << 20, dtype=U8)),
+        lambda: mb.moe_orthogonalize(_t(F32, 200, 160), workspace=torch.ones(1 << 20, dtype=U8)),
         lambda: mb.moe_muon_update(_t(F32, 8, 8), _t(F32, 8, 8), _t(BF16, 8, 8), lr=0.1),
     ]
     for call in types:

@@ -256,3 +256,18 @@ def test_same_bytes_every_time(B, N, K, times):
     for _ in range(times):
         assert torch.equal(mb.moe_orthogonalize(g, workspace=ws), want)
     assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,K", [(1, 128, 448), (1, 128, 449), (2, 100, 900), (3, 64, 2000), (1, 65, 3585), (1, 128, 7168),
+                                   (1, 7168, 128), (2, 1793, 60), (1, 3, 7000), (5, 128, 128), (1, 16, 16), (20, 33, 1000),
+                                   (1, 128, 7169), (30, 90, 7000)])
+def test_matrices_that_stay_on_the_chip(B, N, K, dtype):
+    """Sides up to 128, over 1 to 16 CTAs; and sizes just past what fits."""
+    mb = _mb()
+    g = _g(B, N, K, dtype, seed=18)
+    got = mb.moe_orthogonalize(g.cuda(), steps=1).cpu().double()
+    want, bound = ref.one_step_error(g)
+    assert float(((got - want).abs() - bound).max()) <= 0
+    _check_five(mb.moe_orthogonalize(g.cuda()), g)
+    assert mb.device_error() == 0
