@@ -968,6 +968,14 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
 
 # -------------------------------------------------- gated feed-forward block
 
+def _on_current(*tensors):
+    """The kernels run on the current device: tensors of another one are refused."""
+    for t in tensors:
+        d = t.get_device()
+        if d >= 0 and d != _current_device():
+            raise ValueError(f"a tensor on device {d} while device {_current_device()} is the current one")
+
+
 def _gated_weights(w13, w2, counts):
     """Checks w13 [E, 2H, D], w2 [E, D, H] and counts [>= E]; returns E, D, H."""
     if w13.dim() != 3 or w2.dim() != 3:
@@ -1001,6 +1009,7 @@ def moe_gated_mlp(x, w13, w2, counts, *, activation: int = MOE_ACT_SILU, keep: b
         return _call_on(moe_gated_mlp, locals())
     E, D, H = _gated_weights(w13, w2, counts)
     a, dev = _gated_rows(x, D, "x"), x.device
+    _on_current(x, w13, w2)
     y = _output(y, (a, 2 * H), torch.bfloat16, dev, "y") if keep else None
     z = _output(z, (a, H), torch.bfloat16, dev, "z")
     out = _output(out, (a, D), torch.bfloat16, dev, "out")
@@ -1019,6 +1028,7 @@ def moe_gated_mlp_backward(dout, y, w13, w2, counts, *, activation: int = MOE_AC
         return _call_on(moe_gated_mlp_backward, locals())
     E, D, H = _gated_weights(w13, w2, counts)
     a, dev = _gated_rows(dout, D, "dout"), dout.device
+    _on_current(dout, w13, w2)
     if isinstance(y, Checkpoint):
         ck = _checkpoint_arg(y, a, 2 * H, 2)
         y_ptr, exps = _ptr(ck.codes), _ptr(ck.exponents)
@@ -1076,11 +1086,12 @@ def moe_orthogonalize(g, *, steps: int = 5, coefficients=MOE_ORTHOGONALIZE_COEFF
         return _call_on(moe_orthogonalize, locals())
     B, N, K = _matrices(g, "g")
     _need(g, g.dtype, "g", contiguous=False)
+    _on_current(g)
     dt = _dtype_code(g)
     out = _output(out, tuple(g.shape), torch.bfloat16, g.device, "out")
     workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, g.device)
     st = _lib.moe_orthogonalize(_ptr(g), dt, g.stride(0) if B > 1 else 0, g.stride(-2) if N > 1 else 0, B, N, K,
-                                steps, _coefficients(tuple(coefficients)), eps, scale, _ptr(out), _ptr(workspace),
+                                steps, _coefficients(tuple(map(float, coefficients))), eps, scale, _ptr(out), _ptr(workspace),
                                 ws_bytes, _stream())
     _check("moe_orthogonalize", st)
     return out
@@ -1099,11 +1110,12 @@ def moe_muon_update(w, grad, momentum, *, lr: float, mu: float = 0.95, nesterov:
     _need(w, w.dtype, "w")
     _output(grad, w.shape, grad.dtype, None, "grad")
     _output(momentum, w.shape, torch.float32, None, "momentum")
+    _on_current(w, grad, momentum)
     wt, gt = _dtype_code(w), _dtype_code(grad)
     workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, w.device)
     st = _lib.moe_muon_update(_ptr(w), wt, _ptr(grad), gt, _ptr(momentum), B, N, K, mu, int(nesterov), lr,
                               _valid_arg(lr_scale, "lr_scale", torch.float32), weight_decay, steps,
-                              _coefficients(tuple(coefficients)), eps, _ptr(workspace), ws_bytes, _stream())
+                              _coefficients(tuple(map(float, coefficients))), eps, _ptr(workspace), ws_bytes, _stream())
     _check("moe_muon_update", st)
     return w
 

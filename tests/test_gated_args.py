@@ -156,3 +156,19 @@ def test_reference_iteration_reaches_orthonormal_rows():
     assert float((x @ x.transpose(1, 2) - torch.eye(12).double()).abs().max()) < 1e-10
     u, _, vh = torch.linalg.svd(g[0].double(), full_matrices=False)
     assert float((x[0] - u @ vh).abs().max()) < 1e-10
+
+
+def test_a_tensor_of_another_device_is_refused(mb, monkeypatch):  # noqa: F811
+    world = World(monkeypatch, mb)
+    kind = type("Elsewhere", (type(_t(F32, 1)),), {"get_device": lambda self: 1})
+    w = torch.ones(4, 8, 8).as_subclass(kind)
+    with pytest.raises(ValueError):
+        mb.moe_orthogonalize(w)
+    with pytest.raises(ValueError):
+        mb.moe_muon_update(_t(F32, 4, 8, 8), w, _t(F32, 4, 8, 8), lr=0.1)
+    x, w13, w2, counts = _t(BF16, 16, 64), _t(BF16, 4, 64, 64), _t(BF16, 4, 64, 32), _t(I32, 4)
+    with pytest.raises(ValueError):
+        mb.moe_gated_mlp(x, w13.as_subclass(kind), w2, counts)
+    with pytest.raises(ValueError):
+        mb.moe_gated_mlp_backward(x.as_subclass(kind), _t(BF16, 16, 64), w13, w2, counts)
+    assert not world.launched

@@ -118,7 +118,8 @@ def test_other_coefficients_and_steps():
 
 
 @pytest.mark.parametrize("w_dtype,g_dtype", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
-@pytest.mark.parametrize("B,N,K,nesterov", [(1, 1, 3, True), (2, 40, 56, False), (3, 130, 33, True), (1, 300, 520, True)])
+@pytest.mark.parametrize("B,N,K,nesterov", [(1, 1, 3, True), (2, 40, 56, False), (3, 130, 33, True), (1, 300, 520, True),
+                                            (2, 96, 480, False), (1, 100, 1500, True), (1, 2000, 64, True)])
 def test_update(B, N, K, nesterov, w_dtype, g_dtype):
     mb = _mb()
     gen = torch.Generator().manual_seed(5)
@@ -154,11 +155,12 @@ def test_update_of_nothing_moves_only_by_decay():
     assert torch.equal(w, before * 0.75)
 
 
-def test_same_bytes_again_captured_and_on_another_stream():
+@pytest.mark.parametrize("N,K", [(300, 200), (100, 1600)])
+def test_same_bytes_again_captured_and_on_another_stream(N, K):
     mb = _mb()
-    g = _g(2, 300, 200, BF16, seed=9).cuda()
-    w0 = torch.randn(2, 300, 200, device="cuda").to(BF16)
-    m0 = torch.randn(2, 300, 200, device="cuda")
+    g = _g(2, N, K, BF16, seed=9).cuda()
+    w0 = torch.randn(2, N, K, device="cuda").to(BF16)
+    m0 = torch.randn(2, N, K, device="cuda")
     out = mb.moe_orthogonalize(g)
     w, m = w0.clone(), m0.clone()
     mb.moe_muon_update(w, g, m, lr=0.1)
@@ -173,7 +175,7 @@ def test_same_bytes_again_captured_and_on_another_stream():
     graphs = []
     for k in range(2):
         wk, mk, lr = w0.clone(), m0.clone(), torch.tensor([1.0], device="cuda")
-        ws = torch.empty(mb.moe_orthogonalize_workspace_size(2, 300, 200), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(mb.moe_orthogonalize_workspace_size(2, N, K), dtype=torch.uint8, device="cuda")
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             mb.moe_muon_update(wk, g, mk, lr=0.1, lr_scale=lr, workspace=ws)
@@ -207,7 +209,7 @@ def test_offsets_past_32_bits():
 
 def test_two_streams_at_once():
     mb = _mb()
-    gs = [_g(3, 200, 330, BF16, seed=12).cuda(), _g(2, 700, 96, F32, seed=13).cuda(), _g(1, 64, 4096, F32, seed=14).cuda()]
+    gs = [_g(9, 100, 7000, BF16, seed=19).cuda(), _g(3, 200, 330, BF16, seed=12).cuda(), _g(2, 700, 96, F32, seed=13).cuda(), _g(1, 64, 4096, F32, seed=14).cuda()]
     want = [mb.moe_orthogonalize(g) for g in gs]
     streams = [torch.cuda.Stream() for _ in gs]
     torch.cuda.synchronize()
@@ -245,6 +247,7 @@ def test_two_steps_made_one(B, N, K):
 
 
 @pytest.mark.parametrize("B,N,K,times", [(3, 512, 7168, 60), (2, 6100, 800, 20), (16, 512, 256, 60), (1, 1100, 6144, 20),
+                                         (9, 128, 7168, 60), (1, 60, 1793, 60),
                                          (4, 1024, 2048, 30)])
 def test_same_bytes_every_time(B, N, K, times):
     """A call's products follow one another inside one launch: what one stores has to be whole before the next
