@@ -17,6 +17,11 @@
 // neighbouring lanes deal two columns out among them and a warp stores two columns of 64 bytes at
 // once; where a lane's columns are contiguous, a lane stores the 32 bytes of a chunk.
 //
+// 256 x 256 x 64 of products, 512 cycles, need 32 KB a CTA: 18 TB/s from L2 in all, near what it gives.
+// Without an epilogue, operands of zeros from L2: 2390 TFLOP/s, at n = 192 2370, at 128 1760; random operands,
+// one streamed from HBM and used twice: 2035 (the clock falls with the power).  M = 256 on pairs because a
+// CTA by itself needs 48 KB for the same products.
+//
 // Every wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT, all roles stop,
 // copies and MMAs in flight are drained, and tensor memory is freed.
 #pragma once
@@ -223,9 +228,10 @@ struct NoSource {};
 //   epilogue(p, t, rank, sub, group, lane, tbase, wait, release)
 //     wait() -> bool: the accumulator is whole (false: give up); release(): it has been read.
 //     group: which of the quarter's two warps
+
 // A pair's tiles, every pairs-th, the same for all of its roles.  Of `tiles` tiles the last round, which not
 // every pair has one of, is cut into `parts` parts along B, as many as give each pair at most one: 640 tiles
-// of 256 rows are 8 rounds and 32 tiles of 128 rows on either of 64 pairs, where 9 rounds were (120 experts
+// of 256 rows are 8 rounds and 32 tiles of 128 rows on either of 64 pairs, where 9 rounds were (128 experts
 // of 344 rows, gradient: 1287 -> 1232 us); a few tiles in all become so many smaller ones.
 template <class P>
 struct Walk {
