@@ -13,12 +13,13 @@
 // so lanes j and j + 16 of a warp hold y0 and y1 of one column, and one shuffle for two
 // accumulators brings the pairs together.
 //
-// Bound by reading the weights below about 290 rows an expert, by the products above.  8192 rows of 16
-// experts, D = 5120, H = 8192: 775 us gate and up (1770 TFLOP/s), 420 us down (1630), 415 us the gradient
-// of dz (1660, with 400 MB written and 270 MB read beside the weights), 785 us dx (1750).  32768 rows of 128
-// experts, D = 7168, H = 2048: 1250, 690, 705 and 1258 us, 6.3 to 6.9 TB/s.  128 rows of 16 experts, D = 5120,
-// H = 8192, forward: 618 us, 6.5 TB/s.  The gradient's epilogue has y two chunks ahead in registers: loaded
-// at their place behind a condition, its values came one after another (1272 us instead of 415).
+// Bound by reading the weights below about 280 rows an expert, by the products above.  8192 rows of 16
+// experts, D = 5120, H = 8192: 755 us gate and up (1820 TFLOP/s), 410 us down (1680), 416 us the gradient
+// of dz (1650), 773 us dx (1780).  32768 rows of 128 experts, D = 7168, H = 2048: 1231 to 1241, 685 to 699, 713
+// to 720 and 1259 to 1272 us.  128 rows of 16 experts, D = 5120, H = 8192, forward: 603 us, 6.7 TB/s.  The
+// gradient's epilogue has y two chunks ahead in registers, from clamped addresses: loaded at their place
+// behind a condition, its values came one after another (the first form, 1273 us for that gradient; 481
+// with addresses clamped and wider accesses, and 416 with all later steps).
 #include "common.cuh"
 #include "launch.h"
 #include "pair_gemm.cuh"
@@ -96,8 +97,9 @@ __device__ __forceinline__ int setup_rows(const Rows& p, int* tables, unsigned i
 // Tile i: the experts in order; within one, bands of row tiles, in a band the row tiles innermost, so that
 // pairs running together share the weights' tile and the band's rows.  (Experts by their rows, and each
 // pair, or half of the pairs, taking tiles from either end of that order, so that tiles bound by the weights
-// run beside those bound by the products: 32768 rows of 128 experts by Zipf's law, 2420 us in all orders;
-// 128 experts of 344 rows, 1230 us in this order, 1300 to 1630 in those.)
+// run beside those bound by the products: one run each, 32768 rows of 128 experts by Zipf's law, forward, 2415
+// and 2428 us in this order, 2430 to 2550 in those; 128 experts of 344 rows, gradient, 1232 and 1287 in this
+// order, 1236 and 1248 by rows alone, 1300 to 1630 from either end.)
 __device__ __forceinline__ RowTile locate_rows(const Rows& p, const int* tables, int i) {
   const int* tile_start = tables;
   const int* row_off = tables + p.E + 1;

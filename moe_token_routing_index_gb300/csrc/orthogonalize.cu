@@ -17,9 +17,10 @@
 // one fp16).
 //
 // Bound by the products, and the power they take, where the sides are thousands: 8 matrices of 2048 x 7168,
-// A 165 us (1460 TFLOP/s of its half of the tiles, 93% of the tensor pipes' cycles), P 54 us, X 345 us (1390),
-// whose epilogue reads and writes X's two halves; 2 of 5120 x 8192, 303, 220 and 560 us.  By latency where
-// they are hundreds: 3 of 517 x 1003, 15 turns of 10 us, of which loads, epilogue and barrier are 3 each.
+// 2680 us in all; 2 of 5120 x 8192 with the update, 5290.  Products cannot be timed inside the one launch; as
+// launches of their own, an earlier form, A, P and X took 171 to 180, 92 and 339 to 342 us, and 2 of
+// 5120 x 8192 300 to 319, 213 to 229 and 566 to 588.  X's epilogue reads and writes its two halves.  By latency
+// where they are hundreds: 3 of 517 x 1003, 146 us for 15 turns.
 #include "common.cuh"
 #include "launch.h"
 #include "pair_gemm.cuh"

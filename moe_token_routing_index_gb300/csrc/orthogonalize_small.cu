@@ -579,8 +579,8 @@ int cluster_of(int n) {
 
 }  // namespace
 
-// Sides that fit take this way, however many matrices: 60 of 128 x 7168, 9 rounds of 7 clusters, 690 us against
-// 986 by the general way, one 78 against 129; 1000 of 100 x 400, 290 against 1190.
+// Sides that fit take this way, however many matrices: 60 of 128 x 7168, 9 rounds of 7 clusters, 673 us against
+// 996 by the general way, one 74 against 127; 1000 of 100 x 400, 287 against 1211.
 bool orthogonalize_small_fits(int N, int K) {
   const int m = N < K ? N : K, n = N < K ? K : N;
   return m <= kSide && cluster_of(n) > 0;

@@ -17,10 +17,10 @@
 // neighbouring lanes deal two columns out among them and a warp stores two columns of 64 bytes at
 // once; where a lane's columns are contiguous, a lane stores the 32 bytes of a chunk.
 //
-// 256 x 256 x 64 of products, 512 cycles, need 32 KB a CTA: 18 TB/s from L2 in all, near what it gives.
-// Without an epilogue, operands of zeros from L2: 2390 TFLOP/s, at n = 192 2370, at 128 1760; random operands,
-// one streamed from HBM and used twice: 2035 (the clock falls with the power).  M = 256 on pairs because a
-// CTA by itself needs 48 KB for the same products.
+// 256 x 256 x 64 of products, 512 cycles, need 32 KB a CTA: 18 TB/s in all at 2390 TFLOP/s, by arithmetic.
+// The main loop without an epilogue (an early form of it, one run): operands of zeros from L2, K = 4096, 2390
+// TFLOP/s, at n = 192 2370, at 128 1760; random operands, K = 5120, one streamed from HBM and used twice, 2035,
+// the same with zeros 2310.  M = 256 on pairs because a CTA by itself needs 48 KB for the same products.
 //
 // Every wait is bounded; on expiry the kernel records MOE_DEVERR_TIMEOUT, all roles stop,
 // copies and MMAs in flight are drained, and tensor memory is freed.
@@ -231,8 +231,11 @@ struct NoSource {};
 
 // A pair's tiles, every pairs-th, the same for all of its roles.  Of `tiles` tiles the last round, which not
 // every pair has one of, is cut into `parts` parts along B, as many as give each pair at most one: 640 tiles
-// of 256 rows are 8 rounds and 32 tiles of 128 rows on either of 64 pairs, where 9 rounds were (128 experts
-// of 344 rows, gradient: 1287 -> 1232 us); a few tiles in all become so many smaller ones.
+// of 256 rows are 8 rounds and 32 tiles of 128 rows on either of 64 pairs, where 9 rounds were; a few tiles in
+// all become so many smaller ones.  It is for those: 517 rows of 5 experts, D = 272, H = 208, gradient, 18.6 us
+// against 24.9 uncut.  8192 rows of 16 experts, D = 5120, H = 8192, gradient, 1259 and 1281, 128 experts of 344
+// rows 1211 and 1200, both within the spread of their runs; 64 rows, D = 256, H = 512, forward, lose: 15.1
+// and 14.6.
 template <class P>
 struct Walk {
   const typename P::Params& p;
@@ -571,8 +574,8 @@ cudaError_t launch_stages(const typename P::Params& p, int64_t tiles, int table_
 
 // tiles: at most so many, before the last round is cut.  pdl: the launch may begin before the stream's
 // previous kernel ends.  k: the reduction's length.  7 stages where the tables leave room for them (32768 rows
-// on 128 fine-grained experts, forward: 2401 us, 2441 with 6 stages, 2533 with 5, 2765 with 4), 6 where a tile
-// is hardly more than that (64 rows, D = 256, H = 512, forward: 14.8 us, 16.5 with 7).
+// on 128 fine-grained experts, forward: 2373 us, 2425 with 6 stages; 128 rows of 16 experts, D = 5120, H = 8192:
+// 603 and 618), 6 where a tile is hardly more than that.
 template <class P>
 cudaError_t launch_pairs(const typename P::Params& p, int64_t tiles, int k, int table_bytes, bool pdl, cudaStream_t s) {
   if (tiles < 1) return cudaSuccess;
