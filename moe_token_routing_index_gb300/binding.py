@@ -969,11 +969,11 @@ def moe_grouped_weight_grad(dy, x, counts, *, E: int | None = None, out=None, dt
 # -------------------------------------------------- gated feed-forward block
 
 def _on_current(*tensors):
-    """The kernels run on the current device: tensors of another one are refused."""
+    """The kernels run on the current device: tensors of another one are refused (None: not given)."""
+    current = _current_device()
     for t in tensors:
-        d = t.get_device()
-        if d >= 0 and d != _current_device():
-            raise ValueError(f"a tensor on device {d} while device {_current_device()} is the current one")
+        if t is not None and (d := t.get_device()) >= 0 and d != current:
+            raise ValueError(f"a tensor on device {d} while device {current} is the current one")
 
 
 def _gated_weights(w13, w2, counts):
@@ -1009,10 +1009,10 @@ def moe_gated_mlp(x, w13, w2, counts, *, activation: int = MOE_ACT_SILU, keep: b
         return _call_on(moe_gated_mlp, locals())
     E, D, H = _gated_weights(w13, w2, counts)
     a, dev = _gated_rows(x, D, "x"), x.device
-    _on_current(x, w13, w2)
     y = _output(y, (a, 2 * H), torch.bfloat16, dev, "y") if keep else None
     z = _output(z, (a, H), torch.bfloat16, dev, "z")
     out = _output(out, (a, D), torch.bfloat16, dev, "out")
+    _on_current(x, w13, w2, counts, y, z, out)
     st = _lib.moe_gated_mlp(_ptr(x), _ptr(w13), _ptr(w2), _ptr(counts), E, a, D, H, activation, _ptr(y), _ptr(z),
                             _ptr(out), _stream())
     _check("moe_gated_mlp", st)
@@ -1028,17 +1028,17 @@ def moe_gated_mlp_backward(dout, y, w13, w2, counts, *, activation: int = MOE_AC
         return _call_on(moe_gated_mlp_backward, locals())
     E, D, H = _gated_weights(w13, w2, counts)
     a, dev = _gated_rows(dout, D, "dout"), dout.device
-    _on_current(dout, w13, w2)
     if isinstance(y, Checkpoint):
         ck = _checkpoint_arg(y, a, 2 * H, 2)
-        y_ptr, exps = _ptr(ck.codes), _ptr(ck.exponents)
+        y, exponents = ck.codes, ck.exponents
     else:
         _output(y, (a, 2 * H), torch.bfloat16, None, "y")
-        y_ptr, exps = _ptr(y), None
+        exponents = None
     dy = _output(dy, (a, 2 * H), torch.bfloat16, dev, "dy")
     z = _output(z, (a, H), torch.bfloat16, dev, "z") if with_z else None
     out = _output(out, (a, D), torch.bfloat16, dev, "out")
-    st = _lib.moe_gated_mlp_backward(_ptr(dout), y_ptr, exps, _ptr(w13), _ptr(w2), _ptr(counts), E, a, D, H,
+    _on_current(dout, y, exponents, w13, w2, counts, dy, z, out)
+    st = _lib.moe_gated_mlp_backward(_ptr(dout), _ptr(y), _ptr(exponents), _ptr(w13), _ptr(w2), _ptr(counts), E, a, D, H,
                                      activation, _ptr(dy), _ptr(z), _ptr(out), _stream())
     _check("moe_gated_mlp_backward", st)
     return out, dy, z
@@ -1086,10 +1086,10 @@ def moe_orthogonalize(g, *, steps: int = 5, coefficients=MOE_ORTHOGONALIZE_COEFF
         return _call_on(moe_orthogonalize, locals())
     B, N, K = _matrices(g, "g")
     _need(g, g.dtype, "g", contiguous=False)
-    _on_current(g)
     dt = _dtype_code(g)
     out = _output(out, tuple(g.shape), torch.bfloat16, g.device, "out")
     workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, g.device)
+    _on_current(g, out, workspace)
     st = _lib.moe_orthogonalize(_ptr(g), dt, g.stride(0) if B > 1 else 0, g.stride(-2) if N > 1 else 0, B, N, K,
                                 steps, _coefficients(tuple(map(float, coefficients))), eps, scale, _ptr(out), _ptr(workspace),
                                 ws_bytes, _stream())
@@ -1110,9 +1110,9 @@ def moe_muon_update(w, grad, momentum, *, lr: float, mu: float = 0.95, nesterov:
     _need(w, w.dtype, "w")
     _output(grad, w.shape, grad.dtype, None, "grad")
     _output(momentum, w.shape, torch.float32, None, "momentum")
-    _on_current(w, grad, momentum)
     wt, gt = _dtype_code(w), _dtype_code(grad)
     workspace, ws_bytes = _ortho_workspace(workspace, B, N, K, w.device)
+    _on_current(w, grad, momentum, lr_scale, workspace)
     st = _lib.moe_muon_update(_ptr(w), wt, _ptr(grad), gt, _ptr(momentum), B, N, K, mu, int(nesterov), lr,
                               _valid_arg(lr_scale, "lr_scale", torch.float32), weight_decay, steps,
                               _coefficients(tuple(map(float, coefficients))), eps, _ptr(workspace), ws_bytes, _stream())

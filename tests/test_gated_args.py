@@ -172,3 +172,37 @@ def test_a_tensor_of_another_device_is_refused(mb, monkeypatch):  # noqa: F811
     with pytest.raises(ValueError):
         mb.moe_gated_mlp_backward(x.as_subclass(kind), _t(BF16, 16, 64), w13, w2, counts)
     assert not world.launched
+
+
+def _device_cases(mb):  # noqa: F811
+    """(a call of the arguments by name, each of its tensors): every pointer that the kernels get."""
+    E, D, H, a = 4, 64, 32, 16
+    rows = dict(w13=_t(BF16, E, 2 * H, D), w2=_t(BF16, E, D, H), counts=_t(I32, E))
+    forward = dict(rows, x=_t(BF16, a, D), y=_t(BF16, a, 2 * H), z=_t(BF16, a, H), out=_t(BF16, a, D))
+    backward = dict(rows, dout=_t(BF16, a, D), y=_t(BF16, a, 2 * H), dy=_t(BF16, a, 2 * H), z=_t(BF16, a, H),
+                    out=_t(BF16, a, D))
+    codes = dict({k: v for k, v in backward.items() if k != "y"}, codes=_t(torch.float8_e4m3fn, a, 2 * H),
+                 exponents=_t(U8, a, 2))
+    space = _t(U8, mb.moe_orthogonalize_workspace_size(2, 200, 160))
+    one = dict(g=_t(F32, 2, 200, 160), out=_t(BF16, 2, 200, 160), workspace=space)
+    two = dict(w=_t(BF16, 2, 200, 160), grad=_t(BF16, 2, 200, 160), momentum=_t(F32, 2, 200, 160), lr_scale=_t(F32, 1),
+               workspace=space)
+    return dict(gated=(mb.moe_gated_mlp, forward), gated_grad=(mb.moe_gated_mlp_backward, backward),
+                gated_grad_of_codes=(lambda codes, exponents, **s: mb.moe_gated_mlp_backward(
+                    y=mb.Checkpoint(codes, exponents, 2), **s), codes),
+                orthogonal=(mb.moe_orthogonalize, one),
+                update=(lambda **s: mb.moe_muon_update(lr=0.1, **s), two))
+
+
+@pytest.mark.parametrize("name", ["gated", "gated_grad", "gated_grad_of_codes", "orthogonal", "update"])
+def test_each_tensor_of_another_device_is_refused(mb, monkeypatch, name):  # noqa: F811
+    """Whichever argument lies on another device than the current one: its pointer does not reach a kernel."""
+    world = World(monkeypatch, mb)
+    elsewhere = type("Elsewhere", (type(_t(F32, 1)),), {"get_device": lambda self: 1})
+    call, args = _device_cases(mb)[name]
+    call(**args)
+    assert len(world.launched) == 1
+    for which, t in args.items():
+        with pytest.raises(ValueError, match="device"):
+            call(**dict(args, **{which: t.as_subclass(elsewhere)}))
+        assert len(world.launched) == 1, which
