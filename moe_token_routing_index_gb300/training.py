@@ -140,14 +140,17 @@ class MoETrainBlock:
 
     def update(self, grads: dict, lr: float, *, mu: float = 0.95, weight_decay: float = 0.0, lr_scale=None):
         """One update of all weights, in place.  Each expert's gate and up projection, its down projection and
-        the router move by lr * sqrt(max(1, rows / columns)) along their orthogonalised momentum, gamma and beta
-        by lr along their gradients.  lr_scale: fp32 [1] on the device, None: 1."""
+        the router move by lr * sqrt(max(1, rows / columns)) along their orthogonalised momentum and shrink by
+        lr * weight_decay; gamma and beta move by lr along their gradients.  lr_scale: fp32 [1] on the device that
+        multiplies lr, None: 1."""
         for name, w in (("w13", self.w13.view(2 * self.E, self.H, self.D)), ("w2", self.w2), ("router", self.router)):
             if name not in self.momentum:
                 self.momentum[name] = torch.zeros(w.shape, dtype=torch.float32, device=w.device)
+            # (moe_muon_update decays by its rate times weight_decay: the shape's factor is taken out of that again)
             N, K = w.shape[-2:]
-            mb.moe_muon_update(w, grads[name].view(w.shape), self.momentum[name], lr=lr * max(1.0, N / K) ** 0.5, mu=mu,
-                               weight_decay=weight_decay, lr_scale=lr_scale)
+            factor = max(1.0, N / K) ** 0.5
+            mb.moe_muon_update(w, grads[name].view(w.shape), self.momentum[name], lr=lr * factor, mu=mu,
+                               weight_decay=weight_decay / factor, lr_scale=lr_scale)
         for name in ("gamma", "beta"):
             step = lr * grads[name] if lr_scale is None else lr * lr_scale * grads[name]
             w = getattr(self, name)

@@ -1,0 +1,50 @@
+"""The weights' update of the training block, with the kernels replaced by their definition, so that it runs
+without a GPU."""
+import pytest
+import torch
+
+from tests import gated_ref as ref
+from tests.test_streams import mb  # noqa: F401  (a fixture)
+
+BF16 = torch.bfloat16
+NAMES = ("w13", "w2", "router", "gamma", "beta")
+
+
+def _muon(w, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_decay=0.0, lr_scale=None):
+    """moe_muon_update's definition (include/moe_train.h), in 64 bits and rounded once."""
+    momentum.copy_(mu * momentum.double() + grad.double())
+    u = grad.double() + mu * momentum.double() if nesterov else momentum.double()
+    r = lr * (1.0 if lr_scale is None else float(lr_scale))
+    shape = (1, *w.shape)[-3:]
+    w.copy_((1 - r * weight_decay) * w.double() - r * ref.orthogonalize(u.view(shape)).view(w.shape))
+    return w
+
+
+def _block(E, D, H, seed=0):
+    from moe_token_routing_index_gb300.training import MoETrainBlock
+
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)
+    block = MoETrainBlock(2, r(E, 2 * H, D).to(BF16), r(E, D, H).to(BF16), r(E, D).to(BF16), (1 + 0.1 * r(D)).to(BF16),
+                          (0.1 * r(D)).to(BF16), fused=True)
+    return block, {n: r(*getattr(block, n).shape) for n in NAMES}
+
+
+@pytest.mark.parametrize("D,H", [(96, 32), (32, 96), (64, 64)])
+def test_decay_goes_by_the_rate_alone(mb, monkeypatch, D, H):  # noqa: F811
+    """w = (1 - lr wd) w - lr sqrt(max(1, rows / columns)) X: a matrix's shape scales its step, not its decay.
+    Held to one bf16 rounding, and 1e-6 for the 32 bits of rates."""
+    from moe_token_routing_index_gb300 import training
+
+    monkeypatch.setattr(training.mb, "moe_muon_update", _muon)
+    E, lr, decay = 16, 0.05, 4.0
+    block, grads = _block(E, D, H)
+    before = {n: getattr(block, n).double() for n in NAMES}
+    block.update(grads, lr, mu=0.9, weight_decay=decay, lr_scale=torch.tensor([0.5]))
+    for name, shape in (("w13", (2 * E, H, D)), ("w2", (E, D, H)), ("router", (1, E, D))):
+        rate = 0.5 * lr
+        u = 1.9 * grads[name].double().view(shape)
+        want = (1 - rate * decay) * before[name].view(shape)
+        want = want - rate * max(1.0, shape[1] / shape[2]) ** 0.5 * ref.orthogonalize(u)
+        off = (getattr(block, name).double().view(shape) - want).abs()
+        assert bool((off <= (ref.HALF16 + 1e-6) * want.abs() + 1e-6).all()), name
