@@ -169,6 +169,22 @@ class MoETrainBlock:
         return d[:T]
 
 
+def _train_step(block: MoETrainBlock, x, target, valid, n: int, optimizer: str, lr: float):
+    """One step on the first n tokens towards the target; returns (out - target, what the forward kept)."""
+    out, saved = block.forward(x, valid)
+    err = out.float() - target.float()
+    err[n:] = 0
+    grads = block.backward(saved, err.to(torch.bfloat16))
+    if optimizer == "muon":  # (the orthogonalised matrices have no scale; the vectors' gradients are sums over n tokens)
+        block.update(dict(grads, gamma=grads["gamma"].float() / n, beta=grads["beta"].float() / n), lr)
+    else:
+        for name in ("w13", "w2", "router", "gamma", "beta"):
+            w = getattr(block, name)
+            w.copy_(w.float() - lr / n * grads[name].float())
+        block.refresh_weights()
+    return err, saved
+
+
 def _main():
     ap = argparse.ArgumentParser(description="train one MoE block on a fixed random target")
     ap.add_argument("--config", default="tiny", choices=sorted(workloads.CONFIGS))
@@ -192,17 +208,7 @@ def _main():
     for step in range(a.steps):
         torch.cuda.synchronize()
         t0 = time.perf_counter()
-        out, saved = block.forward(x, valid)
-        err = out.float() - target.float()
-        err[n:] = 0
-        grads = block.backward(saved, err.to(bf))
-        if a.optimizer == "muon":
-            block.update(grads, a.lr)
-        else:
-            for name in ("w13", "w2", "router", "gamma", "beta"):
-                w = getattr(block, name)
-                w.copy_(w.float() - a.lr / n * grads[name].float())
-            block.refresh_weights()
+        err, saved = _train_step(block, x, target, valid, n, a.optimizer, a.lr)
         torch.cuda.synchronize()
         ms = (time.perf_counter() - t0) * 1e3
         print(f"step {step}: mean square error {float(err.square().sum()) / (n * cfg.D):.4f}, balance loss "

@@ -48,3 +48,28 @@ def test_decay_goes_by_the_rate_alone(mb, monkeypatch, D, H):  # noqa: F811
         want = want - rate * max(1.0, shape[1] / shape[2]) ** 0.5 * ref.orthogonalize(u)
         off = (getattr(block, name).double().view(shape) - want).abs()
         assert bool((off <= (ref.HALF16 + 1e-6) * want.abs() + 1e-6).all()), name
+
+
+@pytest.mark.parametrize("optimizer", ["sgd", "muon"])
+def test_a_step_of_the_command_takes_the_mean_over_tokens(mb, monkeypatch, optimizer):  # noqa: F811
+    """The gradients of a step are sums over its tokens: gamma and beta move by lr times their mean, and what is
+    orthogonalised moves as it would for any multiple of its gradient.  One bf16 rounding each."""
+    from moe_token_routing_index_gb300 import training
+
+    monkeypatch.setattr(training.mb, "moe_muon_update", _muon)
+    E, D, H, T, n, lr = 16, 64, 32, 80, 75, 0.1
+    block, grads = _block(E, D, H, seed=1)
+    grads = {name: n * g for name, g in grads.items()}
+    before = {name: getattr(block, name).double() for name in NAMES}
+    x, target = torch.randn(T, D).to(BF16), torch.randn(T, D).to(BF16)
+    handed = []
+    monkeypatch.setattr(block, "forward", lambda x, valid: (x.clone(), "kept"))
+    monkeypatch.setattr(block, "backward", lambda saved, dout: handed.append(dout) or grads)
+    err, saved = training._train_step(block, x, target, None, n, optimizer, lr)
+    want_err = x.float() - target.float()
+    want_err[n:] = 0
+    assert saved == "kept" and torch.equal(err, want_err) and torch.equal(handed[0], want_err.to(BF16))
+    for name in ("gamma", "beta") if optimizer == "muon" else NAMES:
+        want = before[name] - lr * grads[name].double() / n
+        off = (getattr(block, name).double() - want).abs()
+        assert bool((off <= (ref.HALF16 + 1e-6) * want.abs() + 1e-6).all()), name
