@@ -699,6 +699,22 @@ Layout layout(const OrthoArgs& g) {
   return l;
 }
 
+// For coefficients that fit: whether the polynomial of the first two steps, but for its linear term, stays in that
+// range as well.  It is of degree 12 in s^2: between these points it exceeds its largest value at them by less than
+// 2%, and the kernels' range ends at twice the limit.
+bool two_steps_fit(const float* c) {
+  for (int i = 0; i <= 1024; ++i) {
+    double s = i / 1024.0, m = 1.0;
+    for (int k = 0; k < 2; ++k) {
+      const double p = (c[1] + c[2] * s * s) * s * s;
+      m *= c[0] + p;
+      s = fabs((c[0] + p) * s);
+    }
+    if (!(fabs(m - c[0] * c[0]) < 32.0)) return false;
+  }
+  return true;
+}
+
 // The tiles of a result [rows, cols] of each matrix; reduction over k.
 bool make_dims(Dims* d, int B, int rows, int cols, int k, bool sym, int splits) {
   const int rt = (rows + kTileM - 1) / kTileM;
@@ -731,7 +747,7 @@ cudaError_t iterate(const OrthoArgs& g, const Layout& l, char* ws, cudaStream_t 
   p.m[1] = reinterpret_cast<__half*>(ws + l.m1);
   p.m[2] = reinterpret_cast<__half*>(ws + l.m2);
   p.partial = reinterpret_cast<float*>(ws + l.partial);
-  p.twice = l.twice && g.steps >= 2 && g.twice_fits;
+  p.twice = l.twice && g.steps >= 2 && two_steps_fit(g.coef);
   auto map = [&](CUtensorMap* to, const void* x, bool of_x, int box) {
     return of_x ? make_map_3d(to, x, true, g.B, g.N, g.K, l.ldx, box) : make_map_3d(to, x, true, g.B, l.m, l.m, l.ldm, box);
   };

@@ -124,7 +124,6 @@ struct OrthoArgs {
   int nesterov;
   int steps;
   float coef[3];
-  bool twice_fits;           // two steps made one stay in the kernels' range too
   float eps;
   bool update;               // out are weights: w = (1 - lr decay) w - lr scale X; else out = scale X, bf16
   void* out;

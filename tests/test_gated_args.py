@@ -206,3 +206,49 @@ def test_each_tensor_of_another_device_is_refused(mb, monkeypatch, name):  # noq
         with pytest.raises(ValueError, match="device"):
             call(**dict(args, **{which: t.as_subclass(elsewhere)}))
         assert len(world.launched) == 1, which
+
+
+def _leaves(c, steps: int, margin: float) -> bool:
+    """Whether the iteration carries a singular value of [0, 1] past the documented limits: on a fine grid of each
+    step's whole range, whose top is moved by the margin."""
+    top = 1.0
+    for _ in range(steps):
+        s = torch.linspace(0, top, 4001, dtype=torch.float64)
+        p = (c[1] + c[2] * s * s) * s * s
+        top = float(((c[0] + p) * s).abs().max()) * (1 + margin)
+        if float(p.abs().max()) * (1 + margin) >= 32 or top >= 4:
+            return True
+    return False
+
+
+def _accepted(mb, c, steps):  # noqa: F811
+    st = mb.library().moe_orthogonalize(None, 0, 0, 0, 0, 8, 8, steps, (ctypes.c_float * 3)(*c), 1e-7, 1.0, None, None, 0,
+                                        None)
+    assert st in (mb.MOE_OK, mb.MOE_ERR_INVALID)
+    return st == mb.MOE_OK
+
+
+def test_coefficients_that_leave_the_range_somewhere_are_refused(mb):  # noqa: F811
+    f32 = lambda *c: tuple(torch.tensor(c, dtype=F32).double().tolist())
+    # just past 3 s - 4 s^3 / R^2, which takes [0, R] onto itself: what is near R / 2 leaves [0, R], by 1e-7, and
+    # each further step multiplies that by 9
+    for c in ((3.000000238418579, -0.9427371025085449, 0.0), (3.000000238418579, -1.4062495231628418, 0.0),
+              (3.000000476837158, -1.4391438961029053, 0.0)):
+        assert f32(*c) == c and _leaves(c, 16, 0.0)
+        assert not _accepted(mb, c, 16) and _accepted(mb, c, 4)
+    always = [ref.COEFFICIENTS, (1.5, -0.5, 0.0), (2.0, -1.5, 0.5), (3.0, -4.0, 0.0), (1.0, 0.0, 0.0), (0.0, 0.0, 0.0),
+              (0.0, 0.0, 3.99), (15 / 8, -10 / 8, 3 / 8)]
+    for c in always[:-2] + always[-1:]:
+        assert all(_accepted(mb, c, steps) for steps in range(1, 17)), c
+    assert _accepted(mb, always[-2], 1) and not _accepted(mb, always[-2], 2)
+    g = torch.Generator().manual_seed(0)
+    size = torch.tensor([5.0, 12.0, 10.0])
+    seen = set()
+    for _ in range(400):
+        c = f32(*((2 * torch.rand(3, generator=g) - 1) * size).tolist())
+        for steps in (1, 2, 3, 5, 16):
+            inside, outside = not _leaves(c, steps, 1e-4), _leaves(c, steps, 0.0)
+            if inside or outside:
+                assert _accepted(mb, c, steps) == inside, (c, steps)
+                seen.add((steps, inside))
+    assert len(seen) == 10
