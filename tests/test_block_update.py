@@ -6,7 +6,7 @@ import torch
 from tests import gated_ref as ref
 from tests.test_streams import mb  # noqa: F401  (a fixture)
 
-BF16 = torch.bfloat16
+BF16, F32 = torch.bfloat16, torch.float32
 NAMES = ("w13", "w2", "router", "gamma", "beta")
 
 
@@ -73,3 +73,34 @@ def test_a_step_of_the_command_takes_the_mean_over_tokens(mb, monkeypatch, optim
         want = before[name] - lr * grads[name].double() / n
         off = (getattr(block, name).double() - want).abs()
         assert bool((off <= (ref.HALF16 + 1e-6) * want.abs() + 1e-6).all()), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,H", [(96, 32), (192, 144)])
+def test_decay_of_the_kernels(D, H):
+    """Without a gradient only the decay is left: half of each weight, to the bit."""
+    block, grads = _block(16, D, H, seed=2)
+    for name in NAMES:
+        setattr(block, name, getattr(block, name).cuda())
+    before = {n: getattr(block, n).clone() for n in NAMES}
+    zero = {n: torch.zeros_like(g, dtype=F32 if n in ("gamma", "beta") else BF16, device="cuda") for n, g in grads.items()}
+    block.update(zero, 0.25, weight_decay=2.0)
+    for name in ("w13", "w2", "router"):
+        assert torch.equal(getattr(block, name), before[name] * 0.5), name
+    assert torch.equal(block.gamma, before["gamma"]) and torch.equal(block.beta, before["beta"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("options", [[], ["--fused"]])
+def test_command_stays_finite(monkeypatch, capsys, options):
+    """Ten steps with the default rate."""
+    import math
+    import sys
+
+    from moe_token_routing_index_gb300 import training
+
+    monkeypatch.setattr(sys, "argv", ["training", "--config", "tiny", "--steps", "10", "--optimizer", "muon", *options])
+    training._main()
+    lines = capsys.readouterr().out.strip().splitlines()
+    errors = [float(line.split("error ")[1].split(",")[0]) for line in lines]
+    assert len(errors) == 10 and all(math.isfinite(e) for e in errors)
