@@ -160,10 +160,9 @@ __global__ void __launch_bounds__(kNormThreads) first_kernel(const Input p, cons
     t.y += v.y;
   }
   t = block_sum(t);
-  // (a sum that overflowed means entries above 2^60: eps is far below the norm)
   const bool big = isinf(t.x);
   const float pre = big ? kDown : 1.0f;
-  const float f = kScale / (big ? sqrtf(t.y) : sqrtf(t.x) + eps);
+  const float f = kScale / (sqrtf(big ? t.y : t.x) + eps * pre);
   each_value<T, V, MOMENTUM>(p, b, [&](uint32_t r, uint32_t c, const float* u, const float* m, float*) {
     __half h[V], l[V];
 #pragma unroll

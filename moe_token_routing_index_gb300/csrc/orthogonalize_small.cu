@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const Args p) {
   }
   const bool big = isinf(t.x);
   const float pre = big ? kDown : 1.0f;
-  const float f = kScale / (big ? sqrtf(t.y) : sqrtf(t.x) + p.eps);
+  const float f = kScale / (sqrtf(big ? t.y : t.x) + p.eps * pre);
 
   // this thread's row, chunk by chunk: X from tensor memory by take(v), which leaves X's scaled value in v;
   // its fp16 goes to shared memory and kScale * a * X back

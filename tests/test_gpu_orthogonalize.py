@@ -274,3 +274,15 @@ def test_matrices_that_stay_on_the_chip(B, N, K, dtype):
     assert float(((got - want).abs() - bound).max()) <= 0
     _check_five(mb.moe_orthogonalize(g.cuda()), g)
     assert mb.device_error() == 0
+
+
+@pytest.mark.parametrize("N,K", [(40, 56), (200, 272), (203, 301)])
+def test_eps_beside_a_norm_whose_square_overflows(N, K):
+    """eps counts whatever the norm's size: here both are about 2^77."""
+    mb = _mb()
+    g = torch.randn(2, N, K, generator=torch.Generator().manual_seed(20)) * 2.0 ** 70
+    eps = 2.0 ** 76
+    got = mb.moe_orthogonalize(g.cuda(), steps=1, eps=eps).cpu().double()
+    want, bound = ref.one_step_error(g, eps=eps)
+    assert float(((got - want).abs() - bound).max()) <= 0
+    assert mb.device_error() == 0
