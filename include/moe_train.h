@@ -214,7 +214,7 @@ int moe_grouped_weight_grad(const void* dy, const void* x, const uint8_t* x_expo
  * out [a_max, D], all bf16 and contiguous.  counts [E] device int32: negative entries count as 0
  * and a sum past a_max is cut there; both are flagged (MOE_DEVERR_BAD_COUNT).  Rows of the
  * outputs past the sum are not written, whatever x holds there.
- * D and H multiples of 16, E <= 1024, 16-byte aligned bases (MOE_ERR_UNSUPPORTED).
+ * D and H multiples of 16, E <= 1024, a_max < 2^31 - 2^24, 16-byte aligned bases (MOE_ERR_UNSUPPORTED).
  * D == 0 or H == 0 is MOE_ERR_INVALID; a_max == 0 is a no-op.
  */
 int moe_gated_mlp(const void* x, const void* w13, const void* w2, const int32_t* counts, int E, int a_max, int D, int H,

@@ -1068,6 +1068,8 @@ def _matrices(t, name: str):
         raise ValueError(f"{name} must be [N, K] or [B, N, K], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if max(t.shape) > 0x7fffffff:  # (ctypes would pass the low bits)
+        raise ValueError(f"{name} has a size past 31 bits: {tuple(t.shape)}")
     return t.shape if t.dim() == 3 else (1, *t.shape)
 
 

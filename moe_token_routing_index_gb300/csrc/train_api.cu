@@ -51,11 +51,14 @@ int check_rows(int a, int W) {
   return MOE_OK;
 }
 
+// The kernels add an expert's row tiles, 2^23 at most, to its rows in 32 bits.
+constexpr int kMaxGatedRows = INT32_MAX - (1 << 24);
+
 int check_gated(const void* x, const void* y, const void* w13, const void* w2, const int32_t* counts, int E, int a_max,
                 int D, int H, int activation, const void* z, const void* out) {
   if (E < 1 || a_max < 0 || D < 1 || H < 1) return MOE_ERR_INVALID;
   if (activation != MOE_ACT_SILU && activation != MOE_ACT_GELU) return MOE_ERR_INVALID;
-  if (E > 1024 || D % 16 != 0 || H % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (E > 1024 || D % 16 != 0 || H % 16 != 0 || a_max > kMaxGatedRows) return MOE_ERR_UNSUPPORTED;
   if (!w13 || !w2 || !counts) return MOE_ERR_INVALID;
   if (a_max > 0 && (!x || !out)) return MOE_ERR_INVALID;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(z, 16) ||

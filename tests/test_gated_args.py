@@ -252,3 +252,27 @@ def test_coefficients_that_leave_the_range_somewhere_are_refused(mb):  # noqa: F
                 assert _accepted(mb, c, steps) == inside, (c, steps)
                 seen.add((steps, inside))
     assert len(seen) == 10
+
+
+def test_rows_whose_tiles_pass_31_bits_are_refused(mb):  # noqa: F811
+    """The kernels round an expert's rows up to tiles in 32 bits, (rows + tiles - 1) / tiles, with at most 2^23 tiles."""
+    inv, uns = mb.MOE_ERR_INVALID, mb.MOE_ERR_UNSUPPORTED
+    limit = 2 ** 31 - 1 - 2 ** 24
+    for a, want in ((2 ** 31 - 1, uns), (limit + 1, uns), (limit, inv)):      # (inv: no x)
+        assert mb.library().moe_gated_mlp(None, FAKE, FAKE, FAKE, 1, a, 16, 16, 0, None, FAKE, FAKE, None) == want
+        assert mb.library().moe_gated_mlp_backward(None, FAKE, None, FAKE, FAKE, FAKE, 1, a, 16, 16, 0, FAKE, None, FAKE,
+                                                   None) == want
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 8, 1), (8, 2 ** 32 + 8), (2 ** 32 + 1, 4, 4)])
+def test_matrices_of_sizes_past_32_bits_are_refused(mb, monkeypatch, shape):  # noqa: F811
+    """A size that a C int cannot hold is refused, not cut to its low bits."""
+    world = World(monkeypatch, mb)
+    kind = type(_t(F32, 1))
+    g = torch.empty(shape, dtype=BF16, device="meta").as_subclass(kind)
+    m = torch.empty(shape, dtype=F32, device="meta").as_subclass(kind)
+    with pytest.raises(ValueError):
+        mb.moe_orthogonalize(g, out=g)
+    with pytest.raises(ValueError):
+        mb.moe_muon_update(g, g, m, lr=0.1)
+    assert not world.launched
