@@ -16,8 +16,9 @@
 // Bound by reading the weights below about 280 rows an expert, by the products above.  8192 rows of 16
 // experts, D = 5120, H = 8192: 755 us gate and up (1820 TFLOP/s), 410 us down (1680), 416 us the gradient
 // of dz (1650), 773 us dx (1780).  32768 rows of 128 experts, D = 7168, H = 2048: 1231 to 1241, 685 to 699, 713
-// to 720 and 1259 to 1272 us.  128 rows of 16 experts, D = 5120, H = 8192, forward: 603 us, 6.7 TB/s.  The
-// gradient's epilogue has y two chunks ahead in registers, from clamped addresses: loaded at their place
+// to 720 and 1259 to 1272 us.  128 rows of 16 experts, D = 5120, H = 8192, forward: 603 us, 6.7 TB/s.  These are
+// short runs; in a loop of calls the GPU is at its power limit, and that gradient takes 1547 to 1638 us in all (1260
+// to 1330 TFLOP/s), the uneven forward 2600 to 2670 (2360 to 2440 in short runs).  The gradient's epilogue has y two chunks ahead in registers, from clamped addresses: loaded at their place
 // behind a condition, its values came one after another (the first form, 1273 us for that gradient; 481
 // with addresses clamped and wider accesses, and 416 with all later steps).
 #include "common.cuh"

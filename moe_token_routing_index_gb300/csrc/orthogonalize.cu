@@ -17,7 +17,8 @@
 // one fp16).
 //
 // Bound by the products, and the power they take, where the sides are thousands: 8 matrices of 2048 x 7168,
-// 2680 us in all; 2 of 5120 x 8192 with the update, 5290.  Products cannot be timed inside the one launch; as
+// 2680 us in all; 2 of 5120 x 8192 with the update, 5290 (in a loop of calls, at the power limit, 2900 to 3040 and
+// 5390 to 5620).  Products cannot be timed inside the one launch; as
 // launches of their own, an earlier form, A, P and X took 171 to 180, 92 and 339 to 342 us, and 2 of
 // 5120 x 8192 300 to 319, 213 to 229 and 566 to 588.  X's epilogue reads and writes its two halves.  By latency
 // where they are hundreds: 3 of 517 x 1003, 146 us for 15 turns.
